@@ -35,6 +35,7 @@ EXPORTS = (
     "vq_qgemm_dequant_residual", "vq_mx_code_bytes", "vq_mx_scale_bytes", "vq_mx_quant", "vq_mx_quant_rotated",
     "vq_mx_gemm",
     "vq_mx_gemm_workspace_bytes", "vq_gemm_dense",
+    "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts", "vq_gemm_dense_experts",
     "vq_calib_hist_bins", "vq_calib_static_scale", "vq_control_workspace_elems", "vq_step_control",
     "vq_status_string", "vq_last_hip_error", "vq_version",
 )
@@ -86,6 +87,12 @@ def _load():
         "vq_mx_gemm": (I, [P, P, I, P, P, I, I64, I64, I64, P, I, I64, P, P]),
         "vq_mx_gemm_workspace_bytes": (I64, [I64, I64, I64]),
         "vq_gemm_dense": (I, [P, P, I, I64, I64, I64, I64, I64, P, I, I64, P]),
+        "vq_rmsnorm": (I, [P, P, I, I64, I64, I64, I64, P, I, D, P, I64, P, I64, P]),
+        "vq_rmsnorm_quant": (I, [P, P, I, I64, I64, I64, I64, P, I, D, I, P, I, P, I32, P, P, P, P, I64, P]),
+        "vq_pack_weights_group": (I, [P, I, I64, I64, I64, I, P, P, P]),
+        "vq_w4_gemv": (I, [P, I, I64, I64, I64, I64, P, P, I, P, I, I64, P]),
+        "vq_qgemm_experts": (I, [P, P, P, I, P, P, I64, P, I64, I64, I64, I64, P, I, I64, P]),
+        "vq_gemm_dense_experts": (I, [P, P, I, P, I64, P, I64, I64, I64, I64, I64, I64, I64, P, I, I64, P]),
         "vq_calib_hist_bins": (I64, []),
         "vq_calib_static_scale": (I, [P, I, I64, I64, I64, I, P, I32, P, P, P, P, P, P, P]),
         "vq_status_string": (ctypes.c_char_p, [I]),
@@ -656,6 +663,244 @@ def vq_step_control(state: torch.Tensor, params: ControlParams, delta_new=None, 
     return skip, bits, e, gamma
 
 
+# ------------------------------------------------------------------ norm, single tokens, experts
+
+_HALF = (torch.float16, torch.bfloat16)
+
+
+class _on_device:
+    """Makes t's device the current one for a launch on its stream, where it is not."""
+    __slots__ = ("index", "prev")
+
+    def __init__(self, t):
+        self.index = t.get_device()
+        self.prev = -1
+
+    def __enter__(self):
+        if torch._C._cuda_getDevice() != self.index:
+            self.prev = torch._C._cuda_exchangeDevice(self.index)
+
+    def __exit__(self, *exc):
+        if self.prev >= 0:
+            torch._C._cuda_exchangeDevice(self.prev)
+        return False
+
+
+def _rows16(t, name, device=None, dtype=None):
+    """A 2-D 16-bit device tensor with unit stride along its rows and a row pitch of at
+    least a row (the pitch of a single row is taken as dense).  Returns the pitch."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and (device is None or t.device == device)):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor{'' if device is None else f' on {device}'}")
+    if t.dtype not in _HALF if dtype is None else t.dtype != dtype:
+        raise TypeError(f"{name} must be {'float16 or bfloat16' if dtype is None else dtype}, not {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    m, k = t.shape
+    ld, unit = t.stride()
+    if (k > 1 and unit != 1) or (m > 1 and ld < k):
+        raise ValueError(f"{name} must have unit stride along its rows and a pitch of at least a row")
+    return ld if m > 1 else k
+
+
+def _norm_operands(x, weight, residual, sum_out):
+    ldx = _rows16(x, "x")
+    m, k = x.shape
+    dev = x.device
+    if weight is not None:
+        _in(weight, "weight", (x.dtype, torch.float32), k, dev)
+        if weight.numel() != k:
+            raise ValueError(f"weight must hold {k} elements")
+    ldr = k
+    if residual is not None:
+        ldr = _rows16(residual, "residual", dev, x.dtype)
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+    if sum_out is not None:
+        if residual is None:
+            raise ValueError("sum_out goes with a residual")
+        ldh = _rows16(sum_out, "sum_out", dev, x.dtype)
+        if sum_out.shape != x.shape:
+            raise ValueError("sum_out must have x's shape")
+    elif residual is not None:
+        sum_out, ldh = torch.empty((m, k), dtype=x.dtype, device=dev), k
+    else:
+        ldh = k
+    w_dt = _DT[x.dtype] if weight is None else _DT[weight.dtype]
+    return m, k, ldx, ldr, w_dt, sum_out, ldh
+
+
+def vq_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, residual=None, y=None, sum_out=None):
+    """Root-mean-square norm of the rows of x (+ residual), times weight (None: ones).
+    Returns y, or (y, h) with a residual, h = x + residual (sum_out; it may be x or residual)."""
+    m, k, ldx, ldr, w_dt, sum_out, ldh = _norm_operands(x, weight, residual, sum_out)
+    if y is None:
+        y, ldy = torch.empty((m, k), dtype=x.dtype, device=x.device), k
+    else:
+        ldy = _rows16(y, "y", x.device, x.dtype)
+        if y.shape != x.shape:
+            raise ValueError("y must have x's shape")
+    with _on_device(x):
+        _check("vq_rmsnorm", _lib.vq_rmsnorm(
+            _ptr(x), _ptr(residual), _DT[x.dtype], m, k, ldx, ldr, _ptr(weight), w_dt, eps, _ptr(y), ldy,
+            _ptr(sum_out), ldh, _stream(x)))
+    return y if residual is None else (y, sum_out)
+
+
+def vq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, bits: int, eps: float = 1e-6, residual=None,
+                     gran: str = "token", idx: torch.Tensor | None = None, static_scale: torch.Tensor | None = None,
+                     bits_dev: torch.Tensor | None = None, codes=None, scales=None, sum_out=None):
+    """vq_rmsnorm's rows as activation codes, quantized as vq_quant_act does (gran "token" or
+    "static").  Returns (codes int8 [M x kp], scales), or (codes, scales, h) with a residual."""
+    m, k, ldx, ldr, w_dt, sum_out, ldh = _norm_operands(x, weight, residual, sum_out)
+    dev = x.device
+    n_out = 0
+    if idx is not None:
+        n_out = int(idx.numel())
+        _in(idx, "idx", _I32, n_out, dev)
+    parts = 2 if n_out else 1
+    if static_scale is not None:
+        _in(static_scale, "static_scale", _F32, parts, dev)
+    if bits_dev is not None:
+        _in(bits_dev, "bits_dev", _I32, 1, dev)
+    kp = vq_packed_k(k, n_out)
+    g = _GRAN.get(gran, -1)
+    if codes is None:
+        codes = torch.empty((m, kp), dtype=torch.int8, device=dev)
+    else:
+        _in(codes, "codes", (torch.int8,), m * kp, dev)
+    if scales is None:
+        shape = ((m, 2) if n_out else (m,)) if g == VQ_PER_TOKEN else (parts,)
+        scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _in(scales, "scales", _F32, (m if g == VQ_PER_TOKEN else 1) * parts, dev)
+    with _on_device(x):
+        _check("vq_rmsnorm_quant", _lib.vq_rmsnorm_quant(
+            _ptr(x), _ptr(residual), _DT[x.dtype], m, k, ldx, ldr, _ptr(weight), w_dt, eps, bits, _ptr(bits_dev), g,
+            _ptr(idx), n_out, _ptr(static_scale), _ptr(codes), _ptr(scales), _ptr(sum_out), ldh, _stream(x)))
+    return (codes, scales) if residual is None else (codes, scales, sum_out)
+
+
+def vq_pack_weights_group(w: torch.Tensor, group: int = 128, codes=None, scales=None):
+    """4-bit codes of W [N x K] with a scale for each `group` (32, 64, 128) input channels.
+    Returns (codes uint8 [N x K/2], scales [N x K/group] of w's dtype)."""
+    ldw = _rows16(w, "w")
+    n, k = w.shape
+    if group not in (32, 64, 128) or k % group:
+        raise ValueError("group must be 32, 64 or 128 and divide K")
+    if codes is None:
+        codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+    if scales is None:
+        scales = torch.empty((n, k // group), dtype=w.dtype, device=w.device)
+    _in(codes, "codes", _U8, n * (k // 2), w.device)
+    _in(scales, "scales", (w.dtype,), n * (k // group), w.device)
+    with _on_device(w):
+        _check("vq_pack_weights_group", _lib.vq_pack_weights_group(
+            _ptr(w), _DT[w.dtype], n, k, ldw, group, _ptr(codes), _ptr(scales), _stream(w)))
+    return codes, scales
+
+
+def vq_w4_gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out_dtype=None, y=None):
+    """Y = X . W^T of a few 16-bit rows x [M x K] with vq_pack_weights_group's weights (the
+    group is K over the scales per row).  out_dtype defaults to x's.  Returns y."""
+    ldx = _rows16(x, "x")
+    m, k = x.shape
+    dev = x.device
+    _in(codes, "codes", _U8, 0, dev)
+    _in(scales, "scales", (x.dtype,), 0, dev)
+    if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0] or 2 * codes.shape[1] != k:
+        raise ValueError(f"codes and scales must be [N x {k // 2}] and [N x {k} / group]")
+    n, groups = scales.shape
+    if not groups or k % groups:
+        raise ValueError(f"scales must be [N x {k} / group]")
+    if y is None:
+        y, ldy = torch.empty((m, n), dtype=out_dtype or x.dtype, device=dev), n
+    else:
+        _out2d(y, "y", m, n, dev)
+        ldy = y.stride(0) if m > 1 else n
+    with _on_device(x):
+        _check("vq_w4_gemv", _lib.vq_w4_gemv(
+            _ptr(x), _DT[x.dtype], m, n, k, ldx, _ptr(codes), _ptr(scales), k // groups, _ptr(y),
+            _DT.get(y.dtype, -1), ldy, _stream(x)))
+    return y
+
+
+def _experts_rows(offsets, rows, m, dev, y, n, out_dtype):
+    """Experts, output rows and the output of an experts' product."""
+    _in(offsets, "offsets", _I32, 2, dev)
+    t = m
+    if rows is not None:
+        _in(rows, "rows", _I32, 0, dev)
+        t = rows.numel()
+    if y is None:
+        return offsets.numel() - 1, t, torch.empty((t, n), dtype=out_dtype, device=dev), n
+    _out2d(y, "y", t, n, dev)
+    return offsets.numel() - 1, t, y, y.stride(0) if t > 1 else n
+
+
+def vq_qgemm_experts(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, b_bits: int,
+                     offsets: torch.Tensor, rows: torch.Tensor | None = None, out_dtype=torch.bfloat16, y=None):
+    """Output row i in [offsets[e], offsets[e + 1]): row rows[i] of the codes a (row i without
+    rows) times expert e's packed weights, dequantized as vq_qgemm_dequant does.
+
+    b, sb: one vq_pack_weights of all experts' weights, [E * N x K] (row-major or in K
+    pieces).  Rows of y outside the offsets are not written.  Returns y [T x N]."""
+    if not (isinstance(a, torch.Tensor) and a.is_cuda and a.dim() == 2):
+        raise TypeError("a must be a 2-D CUDA (HIP) tensor")
+    m, kp = a.shape
+    dev = a.device
+    _in(a, "a", (torch.int8,), m * kp, dev)
+    if not (isinstance(b, torch.Tensor) and b.dim() in (2, 3)):
+        raise TypeError("b must be a 2-D (row-major) or 3-D (K pieces) CUDA (HIP) tensor of packed weight codes")
+    _in(offsets, "offsets", _I32, 2, dev)
+    experts = offsets.numel() - 1
+    kblock = b.dim() == 3
+    total = b.shape[1] if kblock else b.shape[0]
+    n = total // experts
+    if total % experts or not n:
+        raise ValueError(f"b must hold the same number of rows for each of the {experts} experts")
+    if b_bits in (4, 8):
+        row_bytes = kp if b_bits == 8 else kp // 2
+        _in(b, "b", (torch.int8,) if b_bits == 8 else _U8, 0, dev)
+        if tuple(b.shape) != (((row_bytes + 63) // 64, total, 64) if kblock else (total, row_bytes)):
+            raise ValueError(f"b must be packed {b_bits}-bit codes of [E * N x {kp}] weights")
+    _in(sa, "sa", _F32, m, dev)
+    _in(sb, "sb", _F32, total, dev)
+    experts, t, y, ldy = _experts_rows(offsets, rows, m, dev, y, n, out_dtype)
+    with _on_device(a):
+        _check("vq_qgemm_experts", _lib.vq_qgemm_experts(
+            _ptr(a), _ptr(sa), _ptr(b), b_bits | (VQ_W_KBLOCK if kblock else 0), _ptr(sb), _ptr(offsets), experts,
+            _ptr(rows), m, t, n, kp, _ptr(y), _DT.get(y.dtype, -1), ldy, _stream(a)))
+    return y
+
+
+def vq_gemm_dense_experts(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                          out_dtype=None, y=None):
+    """vq_gemm_dense with rows sorted by expert: output row i in [offsets[e], offsets[e + 1]) is
+    row rows[i] of x (row i without rows) times w[e]^T.  w [E x N x K], unit stride along K.
+    Rows of y outside the offsets are not written.  Returns y [T x N]."""
+    ldx = _rows16(x, "x")
+    m, k = x.shape
+    dev = x.device
+    if not (isinstance(w, torch.Tensor) and w.dtype == x.dtype and w.device == dev):
+        raise TypeError(f"w must be a {x.dtype} tensor on {dev}")
+    if w.dim() != 3 or w.shape[2] != k or not w.shape[0] or not w.shape[1]:
+        raise ValueError(f"w must be [E x N x {k}]")
+    es, ldw, unit = w.stride()
+    e, n = w.shape[0], w.shape[1]
+    if n == 1:
+        ldw = max(ldw, k)
+    if (k > 1 and unit != 1) or ldw < k or es < 0:
+        raise ValueError("w must have unit stride along K and rows that do not overlap")
+    experts, t, y, ldy = _experts_rows(offsets, rows, m, dev, y, n, out_dtype or x.dtype)
+    if experts != e:
+        raise ValueError(f"offsets must hold {e + 1} elements")
+    with _on_device(x):
+        _check("vq_gemm_dense_experts", _lib.vq_gemm_dense_experts(
+            _ptr(x), _ptr(w), _DT[x.dtype], _ptr(offsets), e, _ptr(rows), m, t, n, k, ldx, ldw, es, _ptr(y),
+            _DT.get(y.dtype, -1), ldy, _stream(x)))
+    return y
+
+
 # ------------------------------------------------------------------ prepared calls
 
 # Entry points that only enqueue work on a stream (their last argument).
@@ -663,6 +908,8 @@ _LAUNCHES = frozenset((
     "vq_pack_weights", "vq_quant_act", "vq_hadamard_block", "vq_qgemm_dequant", "vq_qgemm_dequant_noalloc",
     "vq_route_rel_l1", "vq_quant_residual", "vq_qgemm_dequant_residual", "vq_mx_quant", "vq_mx_quant_rotated",
     "vq_mx_gemm", "vq_gemm_dense", "vq_calib_static_scale", "vq_step_control",
+    "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts",
+    "vq_gemm_dense_experts",
 ))
 
 

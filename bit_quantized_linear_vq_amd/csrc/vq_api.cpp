@@ -447,6 +447,201 @@ vq_status vq_gemm_dense(const void* x, const void* w, vq_dtype dt, int64_t m, in
   return hip_status(vq_internal::launch_gemm_dense(p, stream));
 }
 
+// ------------------------------------------------------------------ norm
+
+namespace {
+// Shared checks of the norm entry points; fills p.
+vq_status check_norm(const void* x, const void* res, vq_dtype dt, int64_t m, int64_t k, int64_t ldx, int64_t ldr,
+                     const void* weight, vq_dtype w_dt, double eps, const void* h, int64_t ldh,
+                     vq_internal::NormParams& p) {
+  if (m < 0 || k < 1 || m >= kMaxDim || k >= kMaxDim) return VQ_ERR_INVALID_ARG;
+  if (!is_16bit(dt) || (weight && w_dt != dt && w_dt != VQ_F32)) return VQ_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.0) return VQ_ERR_INVALID_ARG;
+  if (m > 0 && !x) return VQ_ERR_INVALID_ARG;
+  if (ldx < k || (res && ldr < k) || (h && ldh < k)) return VQ_ERR_INVALID_ARG;
+  if (k > vq_internal::norm_max_k()) return VQ_ERR_UNSUPPORTED;
+  const uintptr_t w_align = w_dt == VQ_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % 2 || reinterpret_cast<uintptr_t>(res) % 2 ||
+      reinterpret_cast<uintptr_t>(h) % 2 || reinterpret_cast<uintptr_t>(weight) % w_align)
+    return VQ_ERR_SHAPE;
+  p.x = x;
+  p.res = res;
+  p.dtype = (int)dt;
+  p.rows = m;
+  p.k = k;
+  p.ldx = ldx;
+  p.ldr = ldr;
+  p.w = weight;
+  p.w_f32 = w_dt == VQ_F32;
+  p.eps = eps;
+  p.h = const_cast<void*>(h);
+  p.ldh = ldh;
+  return VQ_OK;
+}
+}  // namespace
+
+vq_status vq_rmsnorm(const void* x, const void* res, vq_dtype dt, int64_t m, int64_t k, int64_t ldx, int64_t ldr,
+                     const void* weight, vq_dtype w_dt, double eps, void* y, int64_t ldy, void* h, int64_t ldh,
+                     hipStream_t stream) {
+  vq_internal::NormParams p{};
+  vq_status s = check_norm(x, res, dt, m, k, ldx, ldr, weight, w_dt, eps, h, ldh, p);
+  if (s != VQ_OK) return s;
+  if ((m > 0 && !y) || ldy < k) return VQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(y) % 2) return VQ_ERR_SHAPE;
+  if (m == 0) return VQ_OK;
+  p.y = y;
+  p.ldy = ldy;
+  return hip_status(vq_internal::launch_norm(p, stream));
+}
+
+vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t m, int64_t k, int64_t ldx,
+                           int64_t ldr, const void* weight, vq_dtype w_dt, double eps, int bits,
+                           const int32_t* bits_dev, vq_gran gran, const int32_t* idx_dev, int32_t n_out,
+                           const float* static_scale_dev, int8_t* codes, float* scales, void* h, int64_t ldh,
+                           hipStream_t stream) {
+  vq_internal::NormParams p{};
+  vq_status s = check_norm(x, res, dt, m, k, ldx, ldr, weight, w_dt, eps, h, ldh, p);
+  if (s != VQ_OK) return s;
+  if (m > 0 && (!codes || !scales)) return VQ_ERR_INVALID_ARG;
+  if (n_out < 0 || (n_out > 0 && !idx_dev)) return VQ_ERR_INVALID_ARG;
+  if (gran != VQ_PER_TENSOR && gran != VQ_PER_TOKEN && gran != VQ_PER_TENSOR_STATIC) return VQ_ERR_INVALID_ARG;
+  if (gran == VQ_PER_TENSOR_STATIC && !static_scale_dev) return VQ_ERR_INVALID_ARG;
+  if (gran == VQ_PER_TENSOR || !ok_bits(bits)) return VQ_ERR_UNSUPPORTED;
+  if (n_out > VQ_MAX_OUTLIERS || n_out >= k) return VQ_ERR_UNSUPPORTED;
+  if (k % VQ_K_ALIGN) return VQ_ERR_SHAPE;
+  if (!aligned16(x) || ldx % 8 || !aligned16(codes)) return VQ_ERR_SHAPE;
+  if (res && (!aligned16(res) || ldr % 8)) return VQ_ERR_SHAPE;
+  if (h && (!aligned16(h) || ldh % 8)) return VQ_ERR_SHAPE;
+  if (m == 0) return VQ_OK;
+  p.codes = codes;
+  p.scales = scales;
+  p.bits = bits;
+  p.bits_dev = bits_dev;
+  p.idx = idx_dev;
+  p.n_out = n_out;
+  p.p1 = (int)part_len(n_out);
+  p.kp = k + part_len(n_out);
+  p.static_scale = gran == VQ_PER_TENSOR_STATIC ? static_scale_dev : nullptr;
+  return hip_status(vq_internal::launch_norm(p, stream));
+}
+
+// ------------------------------------------------------------------ group-scaled 4-bit weights
+
+namespace {
+bool ok_group(int group) { return group == 32 || group == 64 || group == 128; }
+}  // namespace
+
+vq_status vq_pack_weights_group(const void* w, vq_dtype dt, int64_t n, int64_t k, int64_t ldw, int group,
+                                uint8_t* codes, void* scales, hipStream_t stream) {
+  if (!w || !codes || !scales) return VQ_ERR_INVALID_ARG;
+  if (!is_16bit(dt)) return VQ_ERR_INVALID_ARG;
+  if (n < 1 || k < 1 || n >= kMaxDim || k >= kMaxDim || ldw < k) return VQ_ERR_INVALID_ARG;
+  if (!ok_group(group)) return VQ_ERR_UNSUPPORTED;
+  if (k % group || !aligned16(w) || ldw % 8 || !aligned16(codes) || reinterpret_cast<uintptr_t>(scales) % 2)
+    return VQ_ERR_SHAPE;
+  return hip_status(vq_internal::launch_pack_group(w, (int)dt, n, k, ldw, group, codes, scales, stream));
+}
+
+vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k, int64_t ldx, const uint8_t* codes,
+                     const void* scales, int group, void* y, vq_dtype out_dt, int64_t ldy, hipStream_t stream) {
+  if (!is_16bit(dt) || !valid_dt(out_dt)) return VQ_ERR_INVALID_ARG;
+  if (m < 0 || n < 1 || k < 1 || m >= kMaxDim || n >= kMaxDim || k >= kMaxDim) return VQ_ERR_INVALID_ARG;
+  if (!codes || !scales || (m > 0 && (!x || !y)) || ldx < k || ldy < n) return VQ_ERR_INVALID_ARG;
+  if (!ok_group(group)) return VQ_ERR_UNSUPPORTED;
+  if (k % group || !aligned16(x) || ldx % 8 || !aligned16(codes) || reinterpret_cast<uintptr_t>(scales) % 2)
+    return VQ_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(y) % (uintptr_t)elem_size(out_dt)) return VQ_ERR_SHAPE;
+  if (m == 0) return VQ_OK;
+  vq_internal::W4GemvParams p{x, (int)dt, m, n, k, ldx, codes, scales, group, y, (int)out_dt, ldy};
+  return hip_status(vq_internal::launch_w4gemv(p, stream));
+}
+
+// ------------------------------------------------------------------ experts
+
+namespace {
+// Limits of the experts' launches (grid sizes and 32-bit tile counts).
+constexpr int64_t kMaxExpertRows = (int64_t)1 << 26, kMaxExpertCols = (int64_t)1 << 20, kMaxExperts = 4096;
+
+vq_status check_experts(const void* a, const void* b, const int32_t* offsets, int64_t experts, const int32_t* rows,
+                        int64_t m_a, int64_t t, int64_t n, int64_t k, const void* y, vq_dtype out_dt, int64_t ldy) {
+  if (!offsets || !b || (t > 0 && (!a || !y))) return VQ_ERR_INVALID_ARG;
+  if (!valid_dt(out_dt)) return VQ_ERR_INVALID_ARG;
+  if (experts < 1 || t < 0 || m_a < 0 || n < 1 || k < 1 || m_a >= kMaxDim || k >= kMaxDim || ldy < n)
+    return VQ_ERR_INVALID_ARG;
+  if ((!rows && t > m_a) || (t > 0 && m_a < 1)) return VQ_ERR_INVALID_ARG;
+  if (t > kMaxExpertRows || n > kMaxExpertCols || experts > kMaxExperts) return VQ_ERR_UNSUPPORTED;
+  if (k % VQ_K_ALIGN || !aligned16(a) || !aligned16(b)) return VQ_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(y) % (uintptr_t)elem_size(out_dt)) return VQ_ERR_SHAPE;
+  return VQ_OK;
+}
+}  // namespace
+
+vq_status vq_qgemm_experts(const int8_t* a, const float* sa, const void* b, int b_bits, const float* sb,
+                           const int32_t* offsets, int64_t experts, const int32_t* rows, int64_t m_a, int64_t t,
+                           int64_t n, int64_t kp, void* y, vq_dtype out_dt, int64_t ldy, hipStream_t stream) {
+  if (!sb || (t > 0 && !sa)) return VQ_ERR_INVALID_ARG;
+  if (!wfmt_ok(b_bits)) return VQ_ERR_UNSUPPORTED;
+  vq_status s = check_experts(a, b, offsets, experts, rows, m_a, t, n, kp, y, out_dt, ldy);
+  if (s != VQ_OK) return s;
+  const int bits = b_bits & ~VQ_W_KBLOCK;
+  if ((double)kp * 127.0 * (bits == 8 ? 127.0 : 112.0) >= 2147483648.0) return VQ_ERR_SHAPE;
+  if (t == 0) return VQ_OK;
+  const bool kblock = (b_bits & VQ_W_KBLOCK) != 0;
+  const int64_t row_bytes = kblock ? 64 : weight_row_bytes(kp, bits);
+  vq_internal::ExpertsParams p{};
+  p.kind = bits == 8 ? 0 : 1;
+  p.a = a;
+  p.sa = sa;
+  p.b = b;
+  p.sb = sb;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.experts = experts;
+  p.m_a = m_a;
+  p.t = t;
+  p.n = n;
+  p.k = kp;
+  p.lda = kp;
+  p.ldb = row_bytes;
+  p.b_expert = n * row_bytes;
+  p.b_piece = kblock ? 64 * n * experts : 64;
+  p.y = y;
+  p.out_dt = (int)out_dt;
+  p.ldy = ldy;
+  return hip_status(vq_internal::launch_experts(p, stream));
+}
+
+vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const int32_t* offsets, int64_t experts,
+                                const int32_t* rows, int64_t m_x, int64_t t, int64_t n, int64_t k, int64_t ldx,
+                                int64_t ldw, int64_t expert_stride, void* y, vq_dtype out_dt, int64_t ldy,
+                                hipStream_t stream) {
+  if (!is_16bit(dt)) return VQ_ERR_INVALID_ARG;
+  vq_status s = check_experts(x, w, offsets, experts, rows, m_x, t, n, k, y, out_dt, ldy);
+  if (s != VQ_OK) return s;
+  if (ldx < k || ldw < k || expert_stride < 0) return VQ_ERR_INVALID_ARG;
+  if (ldx % 8 || ldw % 8 || expert_stride % 8) return VQ_ERR_SHAPE;
+  if (t == 0) return VQ_OK;
+  vq_internal::ExpertsParams p{};
+  p.kind = dt == VQ_BF16 ? 3 : 2;
+  p.a = x;
+  p.b = w;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.experts = experts;
+  p.m_a = m_x;
+  p.t = t;
+  p.n = n;
+  p.k = k;
+  p.lda = 2 * ldx;
+  p.ldb = 2 * ldw;
+  p.b_expert = 2 * expert_stride;
+  p.b_piece = 64;
+  p.y = y;
+  p.out_dt = (int)out_dt;
+  p.ldy = ldy;
+  return hip_status(vq_internal::launch_experts(p, stream));
+}
+
 // ------------------------------------------------------------------ calibration
 
 int64_t vq_calib_hist_bins(void) { return vq_internal::calib_hist_bins(); }

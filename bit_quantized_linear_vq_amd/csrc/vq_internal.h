@@ -94,6 +94,61 @@ struct DenseParams {
 };
 hipError_t launch_gemm_dense(const DenseParams& p, hipStream_t st);
 
+struct NormParams {
+  const void* x;
+  const void* res;  // or nullptr
+  int dtype;        // 0 f16, 1 bf16
+  int64_t rows, k, ldx, ldr;
+  const void* w;  // or nullptr: ones
+  int w_f32;      // w in float32 instead of dtype
+  double eps;
+  void* h;  // the sum x + r, or nullptr
+  int64_t ldh;
+  void* y;  // 16-bit output, or nullptr with codes
+  int64_t ldy;
+  int8_t* codes;
+  float* scales;
+  int bits;
+  const int32_t* bits_dev;
+  const int32_t* idx;
+  int n_out, p1;
+  int64_t kp;
+  const float* static_scale;
+};
+int norm_max_k();
+hipError_t launch_norm(const NormParams& p, hipStream_t st);
+
+hipError_t launch_pack_group(const void* w, int dtype, int64_t n, int64_t k, int64_t ldw, int group, uint8_t* codes,
+                             void* scales, hipStream_t st);
+struct W4GemvParams {
+  const void* x;
+  int in_dt;  // 0 f16, 1 bf16
+  int64_t m, n, k, ldx;
+  const uint8_t* codes;
+  const void* scales;
+  int group;
+  void* y;
+  int out_dt;
+  int64_t ldy;
+};
+hipError_t launch_w4gemv(const W4GemvParams& p, hipStream_t st);
+
+struct ExpertsParams {
+  int kind;  // 0 int8 weights, 1 4-bit weights, 2 f16, 3 bf16 operands
+  const void* a;
+  const float* sa;
+  const void* b;
+  const float* sb;
+  const int32_t* offsets;
+  const int32_t* rows;
+  int64_t experts, m_a, t, n, k;
+  int64_t lda, ldb, b_expert, b_piece;  // bytes
+  void* y;
+  int out_dt;
+  int64_t ldy;
+};
+hipError_t launch_experts(const ExpertsParams& p, hipStream_t st);
+
 int calib_hist_bins();
 constexpr int CALIB_MAX_CAND = 64;
 hipError_t launch_calib(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int bits,

@@ -373,6 +373,105 @@ vq_status vq_gemm_dense(const void* x, const void* w, vq_dtype dt, int64_t m, in
                         int64_t ldx, int64_t ldw, void* y, vq_dtype out_dt, int64_t ldy, hipStream_t stream);
 
 /*
+ * Root-mean-square norm with the residual's addition: the rows that enter a layer.
+ *   h = RNE_dt(fl32(x + r)) (h = x without a residual);  q = sum_k h^2 / k (float64)
+ *   rstd = fl32(1 / sqrt(q + eps)) (float64, rounded once);  v = fl32(fl32(h * rstd) * w)
+ * vq_rmsnorm stores y = RNE_dt(v), for the unquantized layers (vq_gemm_dense, vq_w4_gemv);
+ * vq_rmsnorm_quant stores the codes and scales of v, exactly as vq_quant_act derives them
+ * from its x (v is not rounded to 16 bits in between), for vq_qgemm_dequant and
+ * vq_qgemm_experts.
+ *   x, res     device, dt in {F16, BF16}, [m x k], strides ldx, ldr; res NULL: no residual
+ *   weight     device [k] of w_dt (dt or F32), or NULL for ones
+ *   eps        finite, >= 0
+ *   h          device dt [m x k], stride ldh, or NULL: receives the sum.  It may be x or res
+ *              itself (same pointer and stride); no other overlap of inputs and outputs
+ *   y          device dt [m x k], stride ldy
+ *   bits, bits_dev, idx_dev, n_out, static_scale_dev, codes, scales: as for vq_quant_act
+ *              (an outlier index outside [0, k) gives code 0); gran VQ_PER_TOKEN or
+ *              VQ_PER_TENSOR_STATIC
+ * m = 0 enqueues nothing.  An infinity or NaN in a row makes that row's dynamic scale NaN
+ * (its codes are then unspecified), and a scale that overflows nothing else.
+ * vq_rmsnorm takes any k up to 32768 and any stride or element-aligned address (multiples
+ * of 8 elements and 16-byte addresses are faster); vq_rmsnorm_quant has the alignment rules
+ * of vq_quant_act, for x, res and h.
+ * Launches one kernel; nothing is allocated.  Errors: INVALID_ARG, SHAPE, UNSUPPORTED
+ * (k > 32768, gran VQ_PER_TENSOR, bits, n_out as for vq_quant_act).
+ */
+vq_status vq_rmsnorm(const void* x, const void* res, vq_dtype dt, int64_t m, int64_t k, int64_t ldx, int64_t ldr,
+                     const void* weight, vq_dtype w_dt, double eps, void* y, int64_t ldy, void* h, int64_t ldh,
+                     hipStream_t stream);
+vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t m, int64_t k, int64_t ldx,
+                           int64_t ldr, const void* weight, vq_dtype w_dt, double eps, int bits,
+                           const int32_t* bits_dev, vq_gran gran, const int32_t* idx_dev, int32_t n_out,
+                           const float* static_scale_dev, int8_t* codes, float* scales, void* h, int64_t ldh,
+                           hipStream_t stream);
+
+/*
+ * 4-bit weights with a scale for each group of `group` consecutive input channels, and
+ * their product with a few unquantized rows: the layer's form for single tokens, which is
+ * bound by the weights' bytes, so the activations stay at 16 bits.
+ *   s[j,g] = RNE_dt(fl32(max|w| / 7)) over the group;  r = fl32(1 / s)
+ *   c[j,k] = clamp(rne(fl32(w * r)), -7, 7); a group with s = 0 (or 1 / s infinite) has
+ *            zero codes
+ *   y[i,j] = RNE_out(sum_g s[j,g] * sum_{k in g} c[j,k] x[i,k]), products exact, sums in
+ *            float32 (in an order fixed by the sizes).  The inner sums run over
+ *            (c + 24) x with 24 sum x subtracted, so their float32 rounding is relative to
+ *            24 max-magnitude weights: |y - exact| <= (k / 8 + 16) 2^-24 * sum_k s 32 |x_k|
+ *            before the output rounding.
+ *   group      32, 64 or 128; k % group == 0
+ *   w          device, dt in {F16, BF16}, [n x k], stride ldw (16-byte aligned, ldw % 8 == 0)
+ *   codes      device uint8 [n x k/2], 16-byte aligned: two codes per byte, low nibble =
+ *              even k, as vq_pack_weights packs them (any nibble -8..7 is read as such)
+ *   scales     device [n x k/group] of dt
+ *   x          device dt [m x k], stride ldx (16-byte aligned, ldx % 8 == 0)
+ *   y          device out_dt in {F16, BF16, F32}, [m x n], stride ldy
+ * m is any number of rows (0 enqueues nothing), but the weights are read once for every
+ * 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x reach
+ * the outputs of their row as NaN.  One kernel; nothing is allocated.
+ * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group).
+ */
+vq_status vq_pack_weights_group(const void* w, vq_dtype dt, int64_t n, int64_t k, int64_t ldw, int group,
+                                uint8_t* codes, void* scales, hipStream_t stream);
+vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k, int64_t ldx, const uint8_t* codes,
+                     const void* scales, int group, void* y, vq_dtype out_dt, int64_t ldy, hipStream_t stream);
+
+/*
+ * Matrix products of several experts in one launch.  Rows are sorted by expert: output
+ * row i in [offsets[e], offsets[e + 1]) is row rows[i] of a (row i without `rows`) times
+ * expert e's weights.
+ *   vq_qgemm_experts       codes and scales as vq_qgemm_dequant takes them (per-token
+ *                          scales, single partition); a row's output is that call's, bit
+ *                          for bit
+ *   vq_gemm_dense_experts  16-bit rows and weights as vq_gemm_dense takes them, with its
+ *                          error bound
+ *   offsets    device int32 [experts + 1], 0 <= offsets[e] <= offsets[e + 1] <= t.  Rows of y
+ *              outside [offsets[0], offsets[experts]) are left as they were.  The values are
+ *              read by the kernel, clamped to [0, t]: others give unspecified outputs, never
+ *              an access outside the buffers
+ *   rows       device int32 [t], or NULL: the row of a for each output row (a token may
+ *              appear under several experts).  An index outside [0, m_a) gives a row of zeros
+ *   a, sa      device int8 [m_a x kp] and float [m_a];  x: device dt [m_x x k], stride ldx
+ *   b, sb      one packing of all experts' weights [experts * n x kp] by vq_pack_weights (8
+ *              or 4 bits, optionally OR VQ_W_KBLOCK), scales float [experts * n]
+ *   w          device dt: expert e's row j at w + e * expert_stride + j * ldw (elements,
+ *              both multiples of 8)
+ *   y          device out_dt in {F16, BF16, F32}, [t x n], stride ldy
+ * t = 0 enqueues nothing.  One kernel, sized by t and experts alone; no workspace, nothing
+ * is allocated, and the host never reads the offsets, so a call may be captured in a graph
+ * and replayed with other offsets.
+ * Errors: INVALID_ARG (without `rows`, t <= m_a), SHAPE (k % 64, alignment, kp beyond the
+ * int32 accumulators as for vq_qgemm_dequant), UNSUPPORTED (b_bits, t > 2^26, n > 2^20,
+ * experts > 4096).
+ */
+vq_status vq_qgemm_experts(const int8_t* a, const float* sa, const void* b, int b_bits, const float* sb,
+                           const int32_t* offsets, int64_t experts, const int32_t* rows, int64_t m_a, int64_t t,
+                           int64_t n, int64_t kp, void* y, vq_dtype out_dt, int64_t ldy, hipStream_t stream);
+vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const int32_t* offsets, int64_t experts,
+                                const int32_t* rows, int64_t m_x, int64_t t, int64_t n, int64_t k, int64_t ldx,
+                                int64_t ldw, int64_t expert_stride, void* y, vq_dtype out_dt, int64_t ldy,
+                                hipStream_t stream);
+
+/*
  * Static per-tensor activation scale by clipping-percentile search (Q-ARVD, Technical
  * details: per-tensor activations with a clipping percentile and a scale learned during
  * reconstruction).  One pass builds the histogram of |x| over its 32768 16-bit magnitude

@@ -34,5 +34,10 @@ Steps and the passages they follow:
 * ``mx``        MX block formats (FP4 E2M1, FP6 E2M3, E8M0 block scales of 32) and their
                 exact GEMM: the 4-bit floating-point route of the 6Bit-Diffusion page
                 (Methodology B.1) in the form gfx950's scaled MFMA consumes.
+* ``norm``      root-mean-square norm with the residual's addition, as 16-bit rows or codes.
+* ``group4``    4-bit weights with group scales and their product with a few 16-bit rows.
+* ``experts``   products of several experts over rows sorted by expert.
 """
-from . import numerics, detect, quantizer, fwht, gemm, route, linear, decompose, mx, calib, control, dense  # noqa: F401
+from . import (  # noqa: F401
+    numerics, detect, quantizer, fwht, gemm, route, linear, decompose, mx, calib, control, dense, norm, group4, experts,
+)
