@@ -33,6 +33,7 @@ struct XArgs {
   int64_t b_piece;        // bytes from one 64-byte K piece to the next (64: row-major)
   int64_t ldy;
   int vec_store;
+  int max_items;          // tiles of 256 x 256 that ascending offsets can have at most
 };
 
 // The tile-th row tile of BM rows over all experts: its expert, first row and the
@@ -144,8 +145,372 @@ __global__ __launch_bounds__(64) void k_experts_block(XArgs g) {
     }
 }
 
+// ---------------------------------------------------------------------------------------
+// Many rows per expert: 256 x 256 output tiles on the ping-pong schedule of the single
+// layers (k_qgemm_pp, k_gemm_dense): 8 waves, the two of a SIMD alternating between a
+// memory phase (the fragment reads of a 64-byte K stage and its share of the direct loads
+// two stages ahead) and a compute phase (that stage's MFMAs from registers).
+//
+// Ragged shares: an expert's last tile has any number of rows, so a wave's four 32-row
+// blocks are spread over the tile (block 2 mb + wm) and a tile of NM * 64 rows at most runs
+// a K loop of NM blocks per wave: its matrix time follows its rows, in steps of 64, and
+// only the weights' traffic is that of a whole tile.
+//
+// Tiles: the experts' tile counts are summed into a table in LDS once per workgroup; a
+// wave finds a tile's expert with two ballots over it.  The rows' indices of the tile after
+// next are requested a whole tile ahead of their use.
+namespace xp {
+constexpr int BM = 256, BN = 256, NT = 512;
+constexpr int WTN = 64, MBLK = 4, NBLK = 2;
+constexpr int ROW = 64;                  // bytes of an A row per stage: 64 codes or 32 elements
+constexpr int NST = 4, D = 2;
+constexpr int A_BYTES = BM * ROW;
+constexpr int LA = A_BYTES / (NT * 16);  // direct loads per wave and stage (2)
+constexpr int MAX_EXPERTS = 2048;        // of the table in LDS
+}  // namespace xp
+
+__device__ const float x_zero = 0.0f, x_one = 1.0f;
+
+template <int KIND, int OUT_DT>
+__global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_experts_pp(XArgs g) {
+  using namespace xp;
+  constexpr bool INT = KIND == X_I8 || KIND == X_I4;
+  constexpr bool HALF_OUT = OUT_DT != DT_F32;
+  constexpr int B_ROW = KIND == X_I4 ? 32 : 64;
+  constexpr int STAGE = A_BYTES + BN * B_ROW;
+  constexpr int LB = BN * B_ROW / (NT * 16);
+  constexpr int L = LA + LB;
+  typedef typename std::conditional<KIND == X_BF16, __bf16, _Float16>::type in_t;
+  typedef in_t in8 __attribute__((ext_vector_type(8)));
+  typedef typename std::conditional<INT, v16i, v16f>::type acc_t;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * STAGE];
+  __shared__ float s_sa[2][BM];
+  __shared__ float s_sb[2][BN];
+  extern __shared__ int s_tab[];  // [experts] inclusive tile counts, [experts] first rows, [experts] ends
+  const int E = g.experts;
+  int* s_cnt = s_tab;
+  int* s_lo = s_tab + E;
+  int* s_hi = s_tab + 2 * E;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave >> 2;  // waves w and w + 4 share a SIMD
+  const int wm = wave & 1, wn = wave >> 1;
+  const int nk = INT ? g.k / 64 : g.k / 32;
+
+  if (wave == 0) {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = e0 + lane;
+      int lo = 0, hi = 0;
+      if (e < E) {
+        lo = min(max(g.off[e], 0), g.t);
+        hi = min(max(g.off[e + 1], 0), g.t);
+      }
+      int inc = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(inc, o, 64);
+        if (lane >= o) inc += u;
+      }
+      if (e < E) {
+        s_cnt[e] = base + inc;
+        s_lo[e] = lo;
+        s_hi[e] = hi;
+      }
+      base += __shfl(inc, 63, 64);
+    }
+  }
+  __syncthreads();
+  const int tiles_m = __builtin_amdgcn_readfirstlane(s_cnt[E - 1]);
+  const int tiles_n = (g.n + BN - 1) / BN;
+  if ((int64_t)tiles_m * tiles_n > g.max_items) return;  // offsets that do not ascend
+  const int items = tiles_m * tiles_n;
+  int t = blockIdx.x;
+  if (t >= items) return;
+
+  struct Tile {
+    int e, r0, rows, n0;
+  };
+  const int chunk = (E + 63) / 64;
+  auto locate = [&](int w) {
+    int tm, tn;
+    tile_of(w, tiles_m, tiles_n, tm, tn);
+    const uint64_t h0 = __ballot(s_cnt[min((lane + 1) * chunk, E) - 1] > tm);
+    const int c0 = __builtin_ctzll(h0) * chunk;
+    const uint64_t h1 = __ballot(s_cnt[min(c0 + lane, E - 1)] > tm);
+    Tile x;
+    x.e = c0 + __builtin_ctzll(h1);
+    const int lo = __builtin_amdgcn_readfirstlane(s_lo[x.e]), hi = __builtin_amdgcn_readfirstlane(s_hi[x.e]);
+    const int before = x.e ? __builtin_amdgcn_readfirstlane(s_cnt[x.e - 1]) : 0;
+    x.r0 = lo + (tm - before) * BM;
+    x.rows = min(BM, hi - x.r0);
+    x.n0 = tn * BN;
+    return x;
+  };
+
+  int ra[LA], ca[LA], rb[LB], cb[LB];
+#pragma unroll
+  for (int i = 0; i < LA; ++i) dma_lane<ROW>(wave * LA + i, lane, ra[i], ca[i]);
+#pragma unroll
+  for (int i = 0; i < LB; ++i) dma_lane<B_ROW>(wave * LB + i, lane, rb[i], cb[i]);
+  const int rs = 64 * (wave & 3) + lane;  // the row or column whose scale this lane loads
+  int ia[LA], is = 0;                     // rows of a: of this lane's loads, of its scale
+  auto request_rows = [&](const Tile& x) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int r = x.r0 + min(ra[i], x.rows - 1);
+      ia[i] = g.rows ? g.rows[r] : r;
+    }
+    const int r = x.r0 + min(rs, x.rows - 1);
+    is = g.rows ? g.rows[r] : r;
+  };
+  const uint8_t* ga[LA];
+  const uint8_t* gb[LB];
+  int64_t boff = 0;
+  auto set_tile = [&](const Tile& x) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int r = (unsigned)ia[i] < (unsigned)g.m_a ? ia[i] : 0;
+      ga[i] = g.a + r * g.lda + ca[i];
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) gb[i] = g.b + x.e * g.b_expert + (int64_t)min(x.n0 + rb[i], g.n - 1) * g.ldb + cb[i];
+    boff = 0;
+  };
+  // Row scales (0 for an index outside a; 1 for 16-bit rows) and column scales, by direct
+  // loads ahead of the tile's first stage.
+  auto load_scales = [&](const Tile& x, int buf) {
+    if (wave < 4) {
+      const bool ok = (unsigned)is < (unsigned)g.m_a;
+      const float* src = !ok ? &x_zero : INT ? g.sa + is : &x_one;
+      dma4(src, &s_sa[buf][64 * wave]);
+    } else {
+      const float* src = INT ? g.sb + (int64_t)x.e * g.n + min(x.n0 + rs, g.n - 1) : &x_one;
+      dma4(src, &s_sb[buf][64 * (wave - 4)]);
+    }
+  };
+  auto issue = [&](int s) {  // called for s = 0, 1, 2, ... of a tile in order
+    uint8_t* base = lds + (s % NST) * STAGE;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) dma16(ga[i] + s * ROW, base + (wave * LA + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) dma16(gb[i] + boff, base + A_BYTES + (wave * LB + i) * 1024);
+    if constexpr (KIND == X_I4) boff += (s & 1) ? g.b_piece - 32 : 32;
+    else boff += g.b_piece;
+  };
+
+  const int rl = lane & 31, kc = lane >> 5;
+  int fa[2], fb[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    fa[h] = (wm * 32 + rl) * ROW + 16 * ((2 * h + kc) ^ swz64(rl));
+    if constexpr (KIND == X_I4) fb[h] = A_BYTES + (wn * WTN + rl) * B_ROW + 16 * (h ^ swz32(rl)) + 8 * kc;
+    else fb[h] = A_BYTES + (wn * WTN + rl) * B_ROW + 16 * ((2 * h + kc) ^ swz64(rl));
+  }
+  acc_t acc[MBLK][NBLK];
+  typedef typename std::conditional<KIND == X_I4, u2v, v4i>::type b_t;
+  v4i fA[2][MBLK];
+  b_t fB[2][NBLK];
+  auto wait_groups = [&](int later) {
+    if (later >= 1) wait_vmcnt<L>();
+    else wait_vmcnt<0>();
+  };
+  bool pend = false;  // the previous tile's 16 stores follow this tile's first loads
+
+  // The K loop of a tile whose rows need NM blocks per wave.
+  auto k_loop = [&](auto nm_c) {
+    constexpr int NM = decltype(nm_c)::value;
+    auto read_stage = [&](int slot) {
+      const uint8_t* base = lds + slot * STAGE;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int nb = 0; nb < NBLK; ++nb) fB[h][nb] = *reinterpret_cast<const b_t*>(base + fb[h] + nb * 32 * B_ROW);
+#pragma unroll
+        for (int mb = 0; mb < NM; ++mb) fA[h][mb] = *reinterpret_cast<const v4i*>(base + fa[h] + mb * 64 * ROW);
+      }
+    };
+    auto compute = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nb = 0; nb < NBLK; ++nb) {
+          v4i b;
+          if constexpr (KIND == X_I4) b = unpack4(fB[h][nb]);
+          else b = fB[h][nb];
+#pragma unroll
+          for (int mb = 0; mb < NM; ++mb) {
+            if constexpr (INT)
+              acc[mb][nb] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b, fA[h][mb], acc[mb][nb], 0, 0, 0);
+            else if constexpr (KIND == X_F16)
+              acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(in8, b), __builtin_bit_cast(in8, fA[h][mb]), acc[mb][nb], 0, 0, 0);
+            else
+              acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(in8, b), __builtin_bit_cast(in8, fA[h][mb]), acc[mb][nb], 0, 0, 0);
+          }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NM; ++i)
+#pragma unroll
+      for (int j = 0; j < NBLK; ++j) acc[i][j] = acc_t{};
+    if (pend && nk > D) wait_vmcnt<(D - 1) * L + 16>();
+    else wait_groups(min(D, nk) - 1);
+    sched_barrier_all();
+    if (grp == 1) sched_barrier_all();
+    int p = 0;
+    for (; p + D < nk; ++p) {
+      read_stage(p % NST);
+      issue(p + D);
+      const bool early = pend && p < D - 1;  // stage p + 1 was loaded before the stores
+      if (grp == 1) {
+        if (early) wait_vmcnt<(D - 1) * L + 16>();
+        else wait_vmcnt<(D - 1) * L>();
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      sched_barrier_all();
+      compute();
+      if (grp == 0) {
+        if (early) wait_vmcnt<(D - 1) * L + 16>();
+        else wait_vmcnt<(D - 1) * L>();
+      }
+      sched_barrier_all();
+    }
+    for (; p < nk; ++p) {
+      read_stage(p % NST);
+      const int later = nk - p - 2;
+      if (grp == 1) wait_groups(later < 0 ? 0 : later);
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      sched_barrier_all();
+      compute();
+      if (grp == 0) wait_groups(later < 0 ? 0 : later);
+      sched_barrier_all();
+    }
+    if (grp == 0) sched_barrier_all();
+  };
+
+  Tile cur = locate(t), nxt = cur;
+  request_rows(cur);
+  set_tile(cur);
+  load_scales(cur, 0);
+  if (t + (int)gridDim.x < items) {
+    nxt = locate(t + (int)gridDim.x);
+    request_rows(nxt);
+  }
+#pragma unroll
+  for (int s = 0; s < D; ++s)
+    if (s < nk) issue(s);
+  int buf = 0;
+  typedef typename std::conditional<OUT_DT == DT_BF16, __bf16, _Float16>::type h_t;
+  for (;;) {
+    const int nm = (cur.rows + 63) / 64;
+    if (nm == 4) k_loop(std::integral_constant<int, 4>{});
+    else if (nm == 3) k_loop(std::integral_constant<int, 3>{});
+    else if (nm == 2) k_loop(std::integral_constant<int, 2>{});
+    else k_loop(std::integral_constant<int, 1>{});
+
+    const int nt = t + (int)gridDim.x;
+    const bool has_next = nt < items;
+    const Tile c = cur;
+    if (has_next) {
+      cur = nxt;
+      set_tile(cur);
+      load_scales(cur, buf ^ 1);
+      if (nt + (int)gridDim.x < items) {
+        nxt = locate(nt + (int)gridDim.x);
+        request_rows(nxt);
+      }
+#pragma unroll
+      for (int s = 0; s < D; ++s)
+        if (s < nk) issue(s);
+    }
+    const bool full = g.vec_store && c.rows == BM && c.n0 + BN <= g.n;
+    pend = HALF_OUT && has_next && full;
+    v4f sb_r[NBLK][4];
+    if constexpr (INT) {
+#pragma unroll
+      for (int nb = 0; nb < NBLK; ++nb)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sb_r[nb][q] = *reinterpret_cast<const v4f*>(&s_sb[buf][wn * WTN + 4 * kc + nb * 32 + 8 * q]);
+    }
+#pragma unroll
+    for (int mb = 0; mb < MBLK; ++mb) {
+      if (mb >= nm) break;
+      const int ml = 64 * mb + 32 * wm + rl;
+      const int m = c.r0 + ml;
+      const float sa0 = s_sa[buf][ml];
+#pragma unroll
+      for (int nb = 0; nb < NBLK; ++nb) {
+        unsigned pk[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = c.n0 + wn * WTN + 4 * kc + nb * 32 + 8 * q;
+          float out[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (INT) {
+              int a0 = acc[mb][nb][4 * q + r];
+              if constexpr (KIND == X_I4) a0 >>= 4;
+              const float t0 = sa0 * sb_r[nb][q][r];
+              out[r] = (float)a0 * t0;
+            } else {
+              out[r] = sa0 != 0.0f ? acc[mb][nb][4 * q + r] : 0.0f;
+            }
+          }
+          if constexpr (HALF_OUT) {
+            pk[2 * q] = cvt_pair<OUT_DT>(out[0], out[1]);
+            pk[2 * q + 1] = cvt_pair<OUT_DT>(out[2], out[3]);
+          } else {
+            if (ml < c.rows && n < g.n) store4_f32(g.y, (int64_t)m * g.ldy + n, out, min(4, g.n - n), g.vec_store != 0);
+          }
+        }
+        if constexpr (HALF_OUT) {
+#pragma unroll
+          for (int pr = 0; pr < 2; ++pr) {
+            const auto s0 = __builtin_amdgcn_permlane32_swap(pk[4 * pr], pk[4 * pr + 2], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(pk[4 * pr + 1], pk[4 * pr + 3], false, false);
+            const u4v w = {s0[0], s1[0], s0[1], s1[1]};
+            const int no = c.n0 + wn * WTN + nb * 32 + 16 * pr + 8 * kc;
+            h_t* dst = reinterpret_cast<h_t*>(g.y) + (int64_t)m * g.ldy + no;
+            if (full) {
+              *reinterpret_cast<u4v*>(dst) = w;
+            } else if (ml < c.rows && no < g.n) {
+              if (g.vec_store && no + 8 <= g.n) {
+                *reinterpret_cast<u4v*>(dst) = w;
+              } else {
+                for (int e = 0; e < 8 && no + e < g.n; ++e) {
+                  const unsigned d = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
+                  dst[e] = __builtin_bit_cast(h_t, (unsigned short)(d >> (16 * (e & 1))));
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+    if (!has_next) break;
+    buf ^= 1;
+    t = nt;
+  }
+}
+
+template <int KIND>
+static hipError_t launch_pp_kind(XArgs a, int out_dt, hipStream_t st) {
+  const int64_t tiles = (a.t / xp::BM + (a.experts < a.t ? a.experts : a.t)) * (int64_t)((a.n + xp::BN - 1) / xp::BN);
+  a.max_items = (int)tiles;  // at most 2^30 (the entry point's limits)
+  const int pb = vq_internal::persistent_blocks();
+  const dim3 grid((unsigned)(tiles < pb ? tiles : pb));
+  const size_t shm = (size_t)a.experts * 12;
+  switch (out_dt) {
+    case DT_F16: hipLaunchKernelGGL((k_experts_pp<KIND, DT_F16>), grid, dim3(xp::NT), shm, st, a); break;
+    case DT_BF16: hipLaunchKernelGGL((k_experts_pp<KIND, DT_BF16>), grid, dim3(xp::NT), shm, st, a); break;
+    default: hipLaunchKernelGGL((k_experts_pp<KIND, DT_F32>), grid, dim3(xp::NT), shm, st, a); break;
+  }
+  return hipGetLastError();
+}
+
 template <int KIND>
 static hipError_t launch_kind(const XArgs& a, int out_dt, hipStream_t st) {
+  if (a.t > (int64_t)16 * a.experts) return launch_pp_kind<KIND>(a, out_dt, st);
   const int64_t tiles = a.t / 32 + (a.experts < a.t ? a.experts : a.t);
   const dim3 grid((unsigned)tiles, (unsigned)((a.n + 31) / 32));
   switch (out_dt) {
