@@ -16,6 +16,12 @@
 
 namespace vqk {
 
+// A 16-byte store at any element's address (the hardware takes unaligned ones): an odd
+// number of outputs leaves every other row unaligned, and storing those element by element
+// took the 8190 x 2048 -> 5759 16-bit case from XXX to 365 us.
+typedef u4v u4v_any __attribute__((aligned(2)));
+typedef v4f v4f_any __attribute__((aligned(4)));
+
 // Operand kinds.
 enum : int { X_I8 = 0, X_I4 = 1, X_F16 = 2, X_BF16 = 3 };
 
@@ -32,7 +38,6 @@ struct XArgs {
   int64_t b_expert;       // bytes from one expert's weights to the next
   int64_t b_piece;        // bytes from one 64-byte K piece to the next (64: row-major)
   int64_t ldy;
-  int vec_store;
   int max_items;          // tiles of 256 x 256 that ascending offsets can have at most
 };
 
@@ -163,10 +168,12 @@ namespace xp {
 constexpr int BM = 256, BN = 256, NT = 512;
 constexpr int WTN = 64, MBLK = 4, NBLK = 2;
 constexpr int ROW = 64;                  // bytes of an A row per stage: 64 codes or 32 elements
-constexpr int NST = 4, D = 2;
+#ifndef XP_D
+#define XP_D 2
+#endif
+constexpr int NST = 4, D = XP_D;
 constexpr int A_BYTES = BM * ROW;
 constexpr int LA = A_BYTES / (NT * 16);  // direct loads per wave and stage (2)
-constexpr int MAX_EXPERTS = 2048;        // of the table in LDS
 }  // namespace xp
 
 __device__ const float x_zero = 0.0f, x_one = 1.0f;
@@ -186,11 +193,12 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NST * STAGE];
   __shared__ float s_sa[2][BM];
   __shared__ float s_sb[2][BN];
-  extern __shared__ int s_tab[];  // [experts] inclusive tile counts, [experts] first rows, [experts] ends
+  extern __shared__ int s_tab[];  // [experts] each: sums of whole tiles and of tails up to an expert, its rows
   const int E = g.experts;
-  int* s_cnt = s_tab;
-  int* s_lo = s_tab + E;
-  int* s_hi = s_tab + 2 * E;
+  int* s_whole = s_tab;
+  int* s_tail = s_tab + E;
+  int* s_lo = s_tab + 2 * E;
+  int* s_hi = s_tab + 3 * E;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = wave >> 2;  // waves w and w + 4 share a SIMD
@@ -198,7 +206,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   const int nk = INT ? g.k / 64 : g.k / 32;
 
   if (wave == 0) {
-    int base = 0;
+    int whole = 0, tails = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
       const int e = e0 + lane;
       int lo = 0, hi = 0;
@@ -206,25 +214,34 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         lo = min(max(g.off[e], 0), g.t);
         hi = min(max(g.off[e + 1], 0), g.t);
       }
-      int inc = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+      const int len = hi > lo ? hi - lo : 0;
+      int inc = len / BM;
+      const uint64_t has_tail = __ballot(len % BM != 0);
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int u = __shfl_up(inc, o, 64);
         if (lane >= o) inc += u;
       }
       if (e < E) {
-        s_cnt[e] = base + inc;
+        s_whole[e] = whole + inc;
+        s_tail[e] = tails + __builtin_popcountll(has_tail & (~0ull >> (63 - lane)));
         s_lo[e] = lo;
         s_hi[e] = hi;
       }
-      base += __shfl(inc, 63, 64);
+      whole += __shfl(inc, 63, 64);
+      tails += __builtin_popcountll(has_tail);
     }
   }
   __syncthreads();
-  const int tiles_m = __builtin_amdgcn_readfirstlane(s_cnt[E - 1]);
+  const int whole_m = __builtin_amdgcn_readfirstlane(s_whole[E - 1]);
+  const int tiles_m = whole_m + __builtin_amdgcn_readfirstlane(s_tail[E - 1]);
   const int tiles_n = (g.n + BN - 1) / BN;
   if ((int64_t)tiles_m * tiles_n > g.max_items) return;  // offsets that do not ascend
-  const int items = tiles_m * tiles_n;
+  const int tiles = tiles_m * tiles_n;
+  const int rest = tiles % (int)gridDim.x;
+  const int split = 4 * rest <= (int)gridDim.x ? 4 : 2 * rest <= (int)gridDim.x ? 2 : 1;
+  const int whole_items = tiles - rest;
+  const int items = whole_items + rest * split;
   int t = blockIdx.x;
   if (t >= items) return;
 
@@ -233,17 +250,23 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   };
   const int chunk = (E + 63) / 64;
   auto locate = [&](int w) {
+    const int j = max(w - whole_items, 0);  // past the whole rounds: piece j % split of a tile
+    const int part = j % split;
     int tm, tn;
-    tile_of(w, tiles_m, tiles_n, tm, tn);
-    const uint64_t h0 = __ballot(s_cnt[min((lane + 1) * chunk, E) - 1] > tm);
+    tile_of(w < whole_items ? w : whole_items + j / split, tiles_m, tiles_n, tm, tn);
+    const bool tail = tm >= whole_m;
+    const int* cnt = tail ? s_tail : s_whole;
+    const int want = tail ? tm - whole_m : tm;
+    const uint64_t h0 = __ballot(cnt[min((lane + 1) * chunk, E) - 1] > want);
     const int c0 = __builtin_ctzll(h0) * chunk;
-    const uint64_t h1 = __ballot(s_cnt[min(c0 + lane, E - 1)] > tm);
+    const uint64_t h1 = __ballot(cnt[min(c0 + lane, E - 1)] > want);
     Tile x;
     x.e = c0 + __builtin_ctzll(h1);
     const int lo = __builtin_amdgcn_readfirstlane(s_lo[x.e]), hi = __builtin_amdgcn_readfirstlane(s_hi[x.e]);
-    const int before = x.e ? __builtin_amdgcn_readfirstlane(s_cnt[x.e - 1]) : 0;
-    x.r0 = lo + (tm - before) * BM;
-    x.rows = min(BM, hi - x.r0);
+    const int before = !tail && x.e ? __builtin_amdgcn_readfirstlane(s_whole[x.e - 1]) : 0;
+    const int step = BM / split;
+    x.r0 = (tail ? hi - (hi - lo) % BM : lo + (want - before) * BM) + part * step;
+    x.rows = w < whole_items ? min(BM, hi - x.r0) : min(step, hi - x.r0);  // <= 0: a piece of a short tail
     x.n0 = tn * BN;
     return x;
   };
@@ -289,10 +312,13 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       dma4(src, &s_sb[buf][64 * (wave - 4)]);
     }
   };
-  auto issue = [&](int s) {  // called for s = 0, 1, 2, ... of a tile in order
+  // A wave loads 32 rows of A; the waves past a tile's last 64-row block load none.
+  auto issue = [&](int s, bool with_a) {  // called for s = 0, 1, 2, ... of a tile in order
     uint8_t* base = lds + (s % NST) * STAGE;
+    if (with_a) {
 #pragma unroll
-    for (int i = 0; i < LA; ++i) dma16(ga[i] + s * ROW, base + (wave * LA + i) * 1024);
+      for (int i = 0; i < LA; ++i) dma16(ga[i] + s * ROW, base + (wave * LA + i) * 1024);
+    }
 #pragma unroll
     for (int i = 0; i < LB; ++i) dma16(gb[i] + boff, base + A_BYTES + (wave * LB + i) * 1024);
     if constexpr (KIND == X_I4) boff += (s & 1) ? g.b_piece - 32 : 32;
@@ -311,15 +337,21 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   typedef typename std::conditional<KIND == X_I4, u2v, v4i>::type b_t;
   v4i fA[2][MBLK];
   b_t fB[2][NBLK];
-  auto wait_groups = [&](int later) {
-    if (later >= 1) wait_vmcnt<L>();
-    else wait_vmcnt<0>();
-  };
   bool pend = false;  // the previous tile's 16 stores follow this tile's first loads
 
   // The K loop of a tile whose rows need NM blocks per wave.
   auto k_loop = [&](auto nm_c) {
     constexpr int NM = decltype(nm_c)::value;
+    const bool with_a = NM == MBLK || wave < 2 * NM;
+    auto wait_next = [&](bool stores) {  // every load but the last stage's done
+      if (stores) wait_vmcnt<(D - 1) * L + 16>();  // whole tiles only: see pend
+      else if (with_a) wait_vmcnt<(D - 1) * L>();
+      else wait_vmcnt<(D - 1) * LB>();
+    };
+    auto wait_groups = [&](int later) {
+      if (later < 1) wait_vmcnt<0>();
+      else wait_next(false);
+    };
     auto read_stage = [&](int slot) {
       const uint8_t* base = lds + slot * STAGE;
 #pragma unroll
@@ -353,52 +385,49 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     for (int i = 0; i < NM; ++i)
 #pragma unroll
       for (int j = 0; j < NBLK; ++j) acc[i][j] = acc_t{};
-    if (pend && nk > D) wait_vmcnt<(D - 1) * L + 16>();
+    if (pend && with_a && nk > D) wait_next(true);
     else wait_groups(min(D, nk) - 1);
     sched_barrier_all();
     if (grp == 1) sched_barrier_all();
     int p = 0;
     for (; p + D < nk; ++p) {
       read_stage(p % NST);
-      issue(p + D);
-      const bool early = pend && p < D - 1;  // stage p + 1 was loaded before the stores
-      if (grp == 1) {
-        if (early) wait_vmcnt<(D - 1) * L + 16>();
-        else wait_vmcnt<(D - 1) * L>();
-      }
+      issue(p + D, with_a);
+      const bool early = pend && with_a && p < D - 1;  // stage p + 1 was loaded before the stores
+      if (grp == 1) wait_next(early);
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       sched_barrier_all();
       compute();
-      if (grp == 0) {
-        if (early) wait_vmcnt<(D - 1) * L + 16>();
-        else wait_vmcnt<(D - 1) * L>();
-      }
+      if (grp == 0) wait_next(early);
       sched_barrier_all();
     }
     for (; p < nk; ++p) {
       read_stage(p % NST);
       const int later = nk - p - 2;
-      if (grp == 1) wait_groups(later < 0 ? 0 : later);
+      if (grp == 1) wait_groups(later);
       __builtin_amdgcn_s_waitcnt(0xC07F);
       sched_barrier_all();
       compute();
-      if (grp == 0) wait_groups(later < 0 ? 0 : later);
+      if (grp == 0) wait_groups(later);
       sched_barrier_all();
     }
     if (grp == 0) sched_barrier_all();
   };
 
   Tile cur = locate(t), nxt = cur;
+  if (cur.rows <= 0) return;  // only a workgroup's last item can be empty
   request_rows(cur);
   set_tile(cur);
   load_scales(cur, 0);
-  if (t + (int)gridDim.x < items) {
+  bool more = t + (int)gridDim.x < items;
+  if (more) {
     nxt = locate(t + (int)gridDim.x);
-    request_rows(nxt);
+    more = nxt.rows > 0;
+    if (more) request_rows(nxt);
   }
 #pragma unroll
   for (int s = 0; s < D; ++s)
-    if (s < nk) issue(s);
+    if (s < nk) issue(s, wave < 2 * ((cur.rows + 63) / 64));
   int buf = 0;
   typedef typename std::conditional<OUT_DT == DT_BF16, __bf16, _Float16>::type h_t;
   for (;;) {
@@ -409,21 +438,23 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     else k_loop(std::integral_constant<int, 1>{});
 
     const int nt = t + (int)gridDim.x;
-    const bool has_next = nt < items;
+    const bool has_next = more;
     const Tile c = cur;
     if (has_next) {
       cur = nxt;
       set_tile(cur);
       load_scales(cur, buf ^ 1);
-      if (nt + (int)gridDim.x < items) {
+      more = nt + (int)gridDim.x < items;
+      if (more) {
         nxt = locate(nt + (int)gridDim.x);
-        request_rows(nxt);
+        more = nxt.rows > 0;
+        if (more) request_rows(nxt);
       }
 #pragma unroll
       for (int s = 0; s < D; ++s)
-        if (s < nk) issue(s);
+        if (s < nk) issue(s, wave < 2 * ((cur.rows + 63) / 64));
     }
-    const bool full = g.vec_store && c.rows == BM && c.n0 + BN <= g.n;
+    const bool full = c.rows == BM && c.n0 + BN <= g.n;
     pend = HALF_OUT && has_next && full;
     v4f sb_r[NBLK][4];
     if constexpr (INT) {
@@ -460,7 +491,12 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
             pk[2 * q] = cvt_pair<OUT_DT>(out[0], out[1]);
             pk[2 * q + 1] = cvt_pair<OUT_DT>(out[2], out[3]);
           } else {
-            if (ml < c.rows && n < g.n) store4_f32(g.y, (int64_t)m * g.ldy + n, out, min(4, g.n - n), g.vec_store != 0);
+            float* dst = reinterpret_cast<float*>(g.y) + (int64_t)m * g.ldy + n;
+            if (ml < c.rows && n + 4 <= g.n) {
+              *reinterpret_cast<v4f_any*>(dst) = v4f{out[0], out[1], out[2], out[3]};
+            } else if (ml < c.rows) {
+              for (int r = 0; r < 4 && n + r < g.n; ++r) dst[r] = out[r];
+            }
           }
         }
         if constexpr (HALF_OUT) {
@@ -472,10 +508,10 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
             const int no = c.n0 + wn * WTN + nb * 32 + 16 * pr + 8 * kc;
             h_t* dst = reinterpret_cast<h_t*>(g.y) + (int64_t)m * g.ldy + no;
             if (full) {
-              *reinterpret_cast<u4v*>(dst) = w;
+              *reinterpret_cast<u4v_any*>(dst) = w;
             } else if (ml < c.rows && no < g.n) {
-              if (g.vec_store && no + 8 <= g.n) {
-                *reinterpret_cast<u4v*>(dst) = w;
+              if (no + 8 <= g.n) {
+                *reinterpret_cast<u4v_any*>(dst) = w;
               } else {
                 for (int e = 0; e < 8 && no + e < g.n; ++e) {
                   const unsigned d = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
@@ -499,7 +535,7 @@ static hipError_t launch_pp_kind(XArgs a, int out_dt, hipStream_t st) {
   a.max_items = (int)tiles;  // at most 2^30 (the entry point's limits)
   const int pb = vq_internal::persistent_blocks();
   const dim3 grid((unsigned)(tiles < pb ? tiles : pb));
-  const size_t shm = (size_t)a.experts * 12;
+  const size_t shm = (size_t)a.experts * 16;  // at most 16 KB beside the 132 KB of the ring and scales
   switch (out_dt) {
     case DT_F16: hipLaunchKernelGGL((k_experts_pp<KIND, DT_F16>), grid, dim3(xp::NT), shm, st, a); break;
     case DT_BF16: hipLaunchKernelGGL((k_experts_pp<KIND, DT_BF16>), grid, dim3(xp::NT), shm, st, a); break;
@@ -546,8 +582,6 @@ hipError_t launch_experts(const ExpertsParams& p, hipStream_t st) {
   a.b_expert = p.b_expert;
   a.b_piece = p.b_piece;
   a.ldy = p.ldy;
-  const int64_t esize = p.out_dt == DT_F32 ? 4 : 2;
-  a.vec_store = ((reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && (p.ldy * esize) % 16 == 0) ? 1 : 0;
   switch (p.kind) {
     case X_I8: return launch_kind<X_I8>(a, p.out_dt, st);
     case X_I4: return launch_kind<X_I4>(a, p.out_dt, st);

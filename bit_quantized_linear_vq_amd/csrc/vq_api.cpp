@@ -560,7 +560,7 @@ vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k
 
 namespace {
 // Limits of the experts' launches (grid sizes and 32-bit tile counts).
-constexpr int64_t kMaxExpertRows = (int64_t)1 << 26, kMaxExpertCols = (int64_t)1 << 20, kMaxExperts = 2048;
+constexpr int64_t kMaxExpertRows = (int64_t)1 << 26, kMaxExpertCols = (int64_t)1 << 20, kMaxExperts = 1024;
 
 vq_status check_experts(const void* a, const void* b, const int32_t* offsets, int64_t experts, const int32_t* rows,
                         int64_t m_a, int64_t t, int64_t n, int64_t k, const void* y, vq_dtype out_dt, int64_t ldy) {

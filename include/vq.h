@@ -461,7 +461,7 @@ vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k
  * and replayed with other offsets.
  * Errors: INVALID_ARG (without `rows`, t <= m_a), SHAPE (k % 64, alignment, kp beyond the
  * int32 accumulators as for vq_qgemm_dequant), UNSUPPORTED (b_bits, t > 2^26, n > 2^20,
- * experts > 2048).
+ * experts > 1024).
  */
 vq_status vq_qgemm_experts(const int8_t* a, const float* sa, const void* b, int b_bits, const float* sb,
                            const int32_t* offsets, int64_t experts, const int32_t* rows, int64_t m_a, int64_t t,
