@@ -8,6 +8,7 @@
 // expert e's rows.  A launch covers the most tiles that any distribution of the rows can
 // have, and a workgroup finds its tile from the offsets (a prefix sum of the experts' tile
 // counts, 64 experts per wave step) or ends.
+#include <algorithm>
 #include <type_traits>
 
 #include "dev_common.h"
@@ -20,6 +21,7 @@ namespace vqk {
 // number of outputs leaves every other row unaligned, and storing those element by element
 // took the 8190 x 2048 -> 5759 16-bit case from XXX to 365 us.
 typedef u4v u4v_any __attribute__((aligned(2)));
+typedef u2v u2v_any __attribute__((aligned(2)));
 typedef v4f v4f_any __attribute__((aligned(4)));
 
 // Operand kinds.
@@ -90,64 +92,180 @@ __device__ __forceinline__ v4i unpack4(u2v w) {
   return r;
 }
 
-// One wave per 32 x 32 block of outputs, operands straight from memory into registers.
-// A step is 32 bytes of an A row: 32 codes or 16 elements.
-template <int KIND, int OUT_DT>
-__global__ __launch_bounds__(64) void k_experts_block(XArgs g) {
+// ---------------------------------------------------------------------------------------
+// Few rows per expert (decoding): a product is bound by the weights' bytes, and each is
+// needed by one tile only.  A workgroup owns 16 rows x 32 columns of outputs; its four
+// waves take a quarter of K each, with both operands straight from memory into registers
+// (no LDS and no barriers in the K loop), and the quarters are joined through LDS.  A
+// 16-row fragment load covers whole 64-byte pieces of the weights, 1 KB in all; with the
+// weights in K pieces that is one contiguous block.
+constexpr int FEW_STEPS = 2;   // 64-byte pieces of weights in a batch; two batches in flight
+constexpr int FEW_M = 16, FEW_N = 32;
+
+template <int KIND, int OUT_DT, int KS>
+__global__ __launch_bounds__(256) void k_experts_few(XArgs g, int tiles_n) {
   constexpr bool INT = KIND == X_I8 || KIND == X_I4;
+  constexpr int AP = KIND == X_I4 ? 2 : 1;  // fragments of A for a piece of weights
   typedef typename std::conditional<KIND == X_BF16, __bf16, _Float16>::type in_t;
   typedef in_t in8 __attribute__((ext_vector_type(8)));
+  typedef typename std::conditional<INT, v4i, v4f>::type acc_t;
+  typedef typename std::conditional<INT, int, float>::type el_t;
+  __shared__ acc_t s_part[4][2][64];
   RowTile tl;
-  if (!find_tile(g, 32, blockIdx.x, tl)) return;
-  const int lane = threadIdx.x, rl = lane & 31, kc = lane >> 5;
-  const int n0 = blockIdx.y * 32;
+  const int tm = blockIdx.x / tiles_n;
+  if (!find_tile(g, FEW_M, tm, tl)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rl = lane & 15, kq = lane >> 4;
+  const int kw = wave % KS;
+  const int n0 = (((int)blockIdx.x - tm * tiles_n) * (4 / KS) + wave / KS) * FEW_N;
   const int row = tl.r0 + rl;
   const bool row_ok = row < tl.r1;
   int ar = row_ok ? row : tl.r0;
   if (g.rows) ar = g.rows[ar];
-  const bool a_ok = ar >= 0 && ar < g.m_a;  // an index outside a gives a row of zeros
+  const uint8_t* pb[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+    pb[b] = g.b + tl.e * g.b_expert + (int64_t)min(n0 + 16 * b + rl, g.n - 1) * g.ldb + 16 * kq;
+  // Pieces of a weight row: 64 bytes each, the last one of a 4-bit row possibly half.
+  const int pieces = KIND == X_I8 ? g.k / 64 : KIND == X_I4 ? (g.k + 127) / 128 : g.k / 32;
+  const int p0 = pieces * kw / KS, p1 = pieces * (kw + 1) / KS;
+  acc_t acc[2] = {acc_t{}, acc_t{}};
+  v4i fa[2][FEW_STEPS][AP], fb[2][FEW_STEPS][2];
+  auto load_b = [&](int set, int p) {
+#pragma unroll
+    for (int u = 0; u < FEW_STEPS; ++u) {
+      const int q = min(p + u, p1 - 1);  // past the end: a valid piece, not used
+      // the half piece's second half lies past a 4-bit row: its first half again, against zeros
+      const int back = KIND == X_I4 && 128 * q + 32 * kq >= g.k ? 32 : 0;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        fb[set][u][b] = *reinterpret_cast<const v4i*>(pb[b] + (int64_t)q * g.b_piece - back);
+      }
+    }
+  };
+  if (p0 < p1) load_b(0, p0);
+  const bool a_ok = (unsigned)ar < (unsigned)g.m_a;  // an index outside a gives a row of zeros
   ar = a_ok ? ar : 0;
-  const uint8_t* pa = g.a + ar * g.lda + 16 * kc;
-  const uint8_t* pb = g.b + tl.e * g.b_expert + (int64_t)min(n0 + rl, g.n - 1) * g.ldb;
-  const int steps = INT ? g.k / 32 : g.k / 16;
-  typedef typename std::conditional<INT, v16i, v16f>::type acc_t;
-  acc_t acc = acc_t{};
-  for (int s = 0; s < steps; ++s) {
-    const v4i fa = *reinterpret_cast<const v4i*>(pa + 32 * s);
-    const int c = KIND == X_I4 ? 16 * s + 8 * kc : 32 * s + 16 * kc;  // byte of the weight row
-    const uint8_t* q = pb + (int64_t)(c >> 6) * g.b_piece + (c & 63);
-    if constexpr (KIND == X_I4) {
-      acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(unpack4(*reinterpret_cast<const u2v*>(q)), fa, acc, 0, 0, 0);
-    } else {
-      const v4i fb = *reinterpret_cast<const v4i*>(q);
-      if constexpr (KIND == X_I8) acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb, fa, acc, 0, 0, 0);
-      else if constexpr (KIND == X_F16)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(in8, fb), __builtin_bit_cast(in8, fa), acc, 0, 0, 0);
-      else
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(in8, fb), __builtin_bit_cast(in8, fa), acc, 0, 0, 0);
+  const uint8_t* pa = g.a + ar * g.lda + 16 * AP * kq;
+  auto load_a = [&](int set, int p) {
+#pragma unroll
+    for (int u = 0; u < FEW_STEPS; ++u) {
+      const int q = min(p + u, p1 - 1);
+#pragma unroll
+      for (int h = 0; h < AP; ++h) {
+        if (KIND == X_I4 && 128 * q + 32 * kq >= g.k) fa[set][u][h] = v4i{0, 0, 0, 0};
+        else fa[set][u][h] = *reinterpret_cast<const v4i*>(pa + 64 * AP * q + 16 * h);
+      }
+    }
+  };
+  auto mma = [&](int set, int p) {
+#pragma unroll
+    for (int u = 0; u < FEW_STEPS; ++u) {
+      if (p + u >= p1) break;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const v4i w = fb[set][u][b];
+        if constexpr (KIND == X_I4) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(unpack4(h ? u2v{(unsigned)w.z, (unsigned)w.w} : u2v{(unsigned)w.x, (unsigned)w.y}), fa[set][u][h], acc[b], 0, 0, 0);
+        } else if constexpr (KIND == X_I8) {
+          acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, fa[set][u][0], acc[b], 0, 0, 0);
+        } else if constexpr (KIND == X_F16) {
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(in8, w), __builtin_bit_cast(in8, fa[set][u][0]), acc[b], 0, 0, 0);
+        } else {
+          acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(in8, w), __builtin_bit_cast(in8, fa[set][u][0]), acc[b], 0, 0, 0);
+        }
+      }
+    }
+  };
+  if (p0 < p1) {
+    load_a(0, p0);
+    for (int p = p0; p < p1; p += 2 * FEW_STEPS) {
+      if (p + FEW_STEPS < p1) {
+        load_b(1, p + FEW_STEPS);
+        load_a(1, p + FEW_STEPS);
+      }
+      mma(0, p);
+      if (p + 2 * FEW_STEPS < p1) {
+        load_b(0, p + 2 * FEW_STEPS);
+        load_a(0, p + 2 * FEW_STEPS);
+      }
+      mma(1, p + FEW_STEPS);
     }
   }
-  if (!row_ok) return;
+  // Lane l of a 16 x 16 block holds row l mod 16 and columns 4 (l div 16) + 0..3.  The
+  // first two waves of a K split finish a block each.
+  if constexpr (KS > 1) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) s_part[wave][b][lane] = acc[b];
+    __syncthreads();
+  }
   const float sa = INT ? g.sa[ar] : 1.0f;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int b = 0; b < 2; ++b) {
+    if (KS > 1 && kw != b) continue;
+    const int nq = n0 + 16 * b + 4 * kq;
+    if (!row_ok || nq >= g.n) continue;
+    const int cnt = min(4, g.n - nq);
+    acc_t v = acc[b];
+    if constexpr (KS > 1) {
+      v = s_part[wave - kw][b][lane];
+#pragma unroll
+      for (int w = 1; w < KS; ++w) v += s_part[wave - kw + w][b][lane];
+    }
+    float out[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int n = n0 + 8 * q + 4 * kc + r;
-      if (n >= g.n) continue;
-      float v;
+      el_t x = v[r];
       if constexpr (INT) {
-        int a0 = acc[4 * q + r];
-        if constexpr (KIND == X_I4) a0 >>= 4;
-        v = (float)a0 * (sa * g.sb[(int64_t)tl.e * g.n + n]);
+        if constexpr (KIND == X_I4) x >>= 4;
+        out[r] = (float)x * (sa * g.sb[(int64_t)tl.e * g.n + min(nq + r, g.n - 1)]);
       } else {
-        v = acc[4 * q + r];
+        out[r] = x;
       }
-      if (!a_ok) v = 0.0f;
-      const int64_t o = (int64_t)row * g.ldy + n;
-      if constexpr (OUT_DT == DT_F32) reinterpret_cast<float*>(g.y)[o] = v;
-      else reinterpret_cast<uint16_t*>(g.y)[o] = (uint16_t)(cvt_pair<OUT_DT>(v, 0.0f) & 0xFFFFu);
+      if (!a_ok) out[r] = 0.0f;
     }
+    const int64_t o = (int64_t)row * g.ldy + nq;
+    if constexpr (OUT_DT == DT_F32) {
+      float* dst = reinterpret_cast<float*>(g.y) + o;
+      if (cnt == 4) {
+        *reinterpret_cast<v4f_any*>(dst) = v4f{out[0], out[1], out[2], out[3]};
+      } else {
+        for (int r = 0; r < cnt; ++r) dst[r] = out[r];
+      }
+    } else {
+      const unsigned q0 = cvt_pair<OUT_DT>(out[0], out[1]), q1 = cvt_pair<OUT_DT>(out[2], out[3]);
+      uint16_t* dst = reinterpret_cast<uint16_t*>(g.y) + o;
+      if (cnt == 4) {
+        *reinterpret_cast<u2v_any*>(dst) = u2v{q0, q1};
+      } else {
+        for (int r = 0; r < cnt; ++r) dst[r] = (uint16_t)((r < 2 ? q0 : q1) >> (16 * (r & 1)));
+      }
+    }
+  }
+}
+
+template <int KIND, int KS>
+static hipError_t launch_few_split(const XArgs& a, int out_dt, hipStream_t st) {
+  const int64_t tiles = a.t / FEW_M + (a.experts < a.t ? a.experts : a.t);
+  const int tiles_n = (a.n + FEW_N * (4 / KS) - 1) / (FEW_N * (4 / KS));
+  const dim3 grid((unsigned)(tiles * tiles_n));
+  switch (out_dt) {
+    case DT_F16: hipLaunchKernelGGL((k_experts_few<KIND, DT_F16, KS>), grid, dim3(256), 0, st, a, tiles_n); break;
+    case DT_BF16: hipLaunchKernelGGL((k_experts_few<KIND, DT_BF16, KS>), grid, dim3(256), 0, st, a, tiles_n); break;
+    default: hipLaunchKernelGGL((k_experts_few<KIND, DT_F32, KS>), grid, dim3(256), 0, st, a, tiles_n); break;
+  }
+  return hipGetLastError();
+}
+
+template <int KIND>
+static hipError_t launch_few_kind(const XArgs& a, int out_dt, hipStream_t st) {
+  // Four waves on K, two where a row has so few pieces that a quarter is three or less
+  // (16 rows over 16 experts, 1920 -> 5760, 4-bit: 12.9 us against 14.6; 24 rows over 8,
+  // 4096 -> 1920, 16-bit: 32.8 against 24.7).
+  const int pieces = KIND == X_I8 ? a.k / 64 : KIND == X_I4 ? a.k / 128 : a.k / 32;
+  return pieces < 16 ? launch_few_split<KIND, 2>(a, out_dt, st) : launch_few_split<KIND, 4>(a, out_dt, st);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -241,9 +359,17 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   const int rest = tiles % (int)gridDim.x;
   const int split = 4 * rest <= (int)gridDim.x ? 4 : 2 * rest <= (int)gridDim.x ? 2 : 1;
   const int whole_items = tiles - rest;
-  const int items = whole_items + rest * split;
+  // Whole tiles come first, so in the last round the workgroups with the highest numbers
+  // have had the short ones: they take its pieces.
+  const int G = (int)gridDim.x;
+  const int last = G - 1 - (int)blockIdx.x;  // this workgroup's piece of the last round, if there are so many
   int t = blockIdx.x;
-  if (t >= items) return;
+  auto next_item = [&](int w) {  // the item after w (-1: none)
+    if (w >= 0 && w < whole_items && w + G < whole_items) return w + G;
+    return w < whole_items && last < rest * split ? whole_items + last : -1;
+  };
+  if (t >= whole_items) t = next_item(whole_items - 1);
+  if (t < 0) return;
 
   struct Tile {
     int e, r0, rows, n0;
@@ -419,9 +545,10 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   request_rows(cur);
   set_tile(cur);
   load_scales(cur, 0);
-  bool more = t + (int)gridDim.x < items;
+  t = next_item(t);
+  bool more = t >= 0;
   if (more) {
-    nxt = locate(t + (int)gridDim.x);
+    nxt = locate(t);
     more = nxt.rows > 0;
     if (more) request_rows(nxt);
   }
@@ -437,16 +564,16 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     else if (nm == 2) k_loop(std::integral_constant<int, 2>{});
     else k_loop(std::integral_constant<int, 1>{});
 
-    const int nt = t + (int)gridDim.x;
     const bool has_next = more;
     const Tile c = cur;
     if (has_next) {
       cur = nxt;
       set_tile(cur);
       load_scales(cur, buf ^ 1);
-      more = nt + (int)gridDim.x < items;
+      t = next_item(t);
+      more = t >= 0;
       if (more) {
-        nxt = locate(nt + (int)gridDim.x);
+        nxt = locate(t);
         more = nxt.rows > 0;
         if (more) request_rows(nxt);
       }
@@ -525,7 +652,6 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     }
     if (!has_next) break;
     buf ^= 1;
-    t = nt;
   }
 }
 
@@ -546,15 +672,18 @@ static hipError_t launch_pp_kind(XArgs a, int out_dt, hipStream_t st) {
 
 template <int KIND>
 static hipError_t launch_kind(const XArgs& a, int out_dt, hipStream_t st) {
-  if (a.t > (int64_t)16 * a.experts) return launch_pp_kind<KIND>(a, out_dt, st);
-  const int64_t tiles = a.t / 32 + (a.experts < a.t ? a.experts : a.t);
-  const dim3 grid((unsigned)tiles, (unsigned)((a.n + 31) / 32));
-  switch (out_dt) {
-    case DT_F16: hipLaunchKernelGGL((k_experts_block<KIND, DT_F16>), grid, dim3(64), 0, st, a); break;
-    case DT_BF16: hipLaunchKernelGGL((k_experts_block<KIND, DT_BF16>), grid, dim3(64), 0, st, a); break;
-    default: hipLaunchKernelGGL((k_experts_block<KIND, DT_F32>), grid, dim3(64), 0, st, a); break;
-  }
-  return hipGetLastError();
+  // The few-row kernel reads the weights again for every 16 rows; the other one needs
+  // about as many 256-column tiles as compute units to reach the memory's rate.  Measured
+  // over 32 experts, 2048 -> 2048 (256 such tiles), us: 8-bit weights, 4 / 8 / 16 rows each,
+  // 28.4 / 29.8 / 37.8 against 29.1 / 29.5 / 30.3; 4-bit 16.9 / 19.0 / 25.1 against 20.1 /
+  // 20.8 / 20.7; 16-bit 50.6 / 55.0 / 73.0 against 67.9 / 67.8 / 68.8.  With fewer tiles the
+  // limit of 8 rows goes up as their number goes down.
+  const int64_t tiles = std::min<int64_t>(a.experts, a.t) * ((a.n + xp::BN - 1) / xp::BN);
+  const int64_t cus = vq_internal::persistent_blocks();
+  const int64_t few_tiles = (a.t / FEW_M + std::min<int64_t>(a.experts, a.t)) * ((a.n + FEW_N - 1) / FEW_N);
+  if (a.t * std::min(tiles, cus) > 8 * a.experts * cus || few_tiles > (1 << 23))
+    return launch_pp_kind<KIND>(a, out_dt, st);
+  return launch_few_kind<KIND>(a, out_dt, st);
 }
 
 }  // namespace vqk
