@@ -4,6 +4,8 @@
 //
 //   s[j,g] = RNE16(fl32(max|w| / 7)),  c[j,k] = clamp(rne(fl32(w * fl32(1 / s))), -7, 7)
 //   y[i,j] = sum_g s[j,g] * sum_{k in g} c[j,k] x[i,k]      (float32)
+#include <type_traits>
+
 #include "dev_common.h"
 #include "gemm_common.h"
 #include "vq_internal.h"
@@ -54,37 +56,265 @@ struct GemvArgs {
   const uint16_t* scales;
   void* y;
   int64_t ldx, ldy;
-  int m, n, k, group;
+  int m, n, k, group, out_dt;
 };
 
-// One wave per output channel and row.
-template <int DT, int OUT_DT>
-__global__ __launch_bounds__(256) void k_w4gemv(GemvArgs g) {
-  const int lane = threadIdx.x & 63;
-  const int j = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (j >= g.n) return;
-  const int words = g.k / 8, wpg = g.group / 8;
-  for (int i = blockIdx.y; i < g.m; i += gridDim.y) {
-    float acc = 0.0f;
-    for (int q = lane; q < words; q += 64) {
-      const unsigned c = *reinterpret_cast<const unsigned*>(g.codes + (int64_t)j * (g.k / 2) + 4 * q);
-      const float s = load1<DT>(g.scales, (int64_t)j * (words / wpg) + q / wpg);
-      float part = 0.0f;
+// ---------------------------------------------------------------------------------------
+// The product on the 16 x 16 x 32 matrix instruction: 16 rows of x against 16 output
+// channels, so that up to 16 rows cost what one does.
+//
+// Codes to 16-bit floats: with u = c + 8 (one exclusive or for eight codes) the nibble goes
+// into the top four mantissa bits of 16.0, which makes the operand 16 + u = c + 24 exactly,
+// two of them per shift and and-or.  The excess 24 sum x comes off first: a group's
+// accumulators start from the product of x with a constant -24, which is one more matrix
+// instruction per fragment of x, not per fragment of weights, and lands in the layout that
+// the accumulators have.
+//
+// Layout: a lane loads 16 bytes of a weight row, 32 codes, the 64 lanes 64 bytes of 16
+// rows.  A matrix instruction wants 32 consecutive channels spread over the lanes' four
+// groups of 16, 8 each, so the 4 x 4 dwords of the four lanes of a row are transposed by
+// two swaps between half-waves and two between rows of 16 lanes.  Instruction j of a 64-byte
+// piece then covers channels 32 j .. 32 j + 31, never two groups, and dword pairs (t, t + 4)
+// of x meet the codes' pairs.
+//
+// A lane's accumulators hold one output channel (lane mod 16) and rows 4 (lane div 16) + i, so
+// a group's scale is one value per lane: y += s * acc.
+//
+// A workgroup's four waves take KS parts of K times 4 / KS blocks of 16 channels.  x goes
+// through LDS in chunks of 4 pieces (512 channels) of every part, its pairs put in order
+// once per workgroup (rows 1040 bytes apart: 16 rows then read 16 bytes each without a bank
+// conflict); the weights come straight to registers, a chunk ahead (two ahead was even or
+// slower: it costs registers, and with them waves).  The parts
+// are joined through LDS in a fixed order.
+constexpr int GV_SETS = 2;
+constexpr int GV_CHUNK = 4;                         // pieces
+constexpr int GV_ROW = GV_CHUNK * 256 + 16;         // bytes of a row of a chunk of x in LDS
+constexpr int GV_ROWS = 32;                         // rows times parts at most
+
+template <int DT, int GROUP, int KS, int MB, int XL>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k_w4gemv(GemvArgs g) {
+  typedef typename std::conditional<DT == DT_BF16, __bf16, _Float16>::type in_t;
+  typedef in_t in8 __attribute__((ext_vector_type(8)));
+  constexpr int GPP = 128 / GROUP;     // groups of a piece
+  constexpr int GPC = GPP * GV_CHUNK;  // and of a chunk
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];  // [2][part][row][GV_ROW]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rl = lane & 15, kq = lane >> 4;
+  const int kw = wave % KS, nw = wave / KS;
+  const int n0 = ((int)blockIdx.x * (4 / KS) + nw) * 16, m0 = blockIdx.y * (16 * MB);
+  const int rows = min(16 * MB, g.m - m0);
+  const int pieces = (g.k + 127) / 128;
+  const int p0 = pieces * kw / KS, p1 = pieces * (kw + 1) / KS;
+  const int chunks = ((pieces + KS - 1) / KS + GV_CHUNK - 1) / GV_CHUNK;  // of the longest part
+  const int groups = g.k / GROUP;
+  const int64_t jn = min(n0 + rl, g.n - 1);
+  const uint8_t* pw = g.codes + jn * (g.k / 2);
+  const uint16_t* ps = g.scales + jn * groups;
+
+  v4i w[GV_SETS][GV_CHUNK];
+  unsigned sc[GV_SETS][GPC / 2];  // two scales each
+  auto load_w = [&](int set, int c) __attribute__((always_inline)) {
+    const int q0 = p0 + GV_CHUNK * c;
+    if (q0 >= p1) return;
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-        part += (float)((int)(c << (28 - 4 * t)) >> 28) * load1<DT>(g.x, i * g.ldx + 8 * q + t);
-      acc += s * part;
+    for (int u = 0; u < GV_CHUNK; ++u) {
+      // Past the part's end or the row's last group: the row's first bytes, not used.
+      const int at = q0 + u < p1 && 128 * (q0 + u) + 32 * kq < g.k ? 64 * (q0 + u) + 16 * kq : 0;
+      w[set][u] = *reinterpret_cast<const v4i*>(pw + at);
     }
+    const int g0 = q0 * GPP;
+    if (g0 + GPC <= groups) {
+      typedef unsigned vec __attribute__((ext_vector_type(GPC / 2 <= 4 ? GPC / 2 : 4)));
+      typedef vec vec_any __attribute__((aligned(2)));
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) acc += __shfl_xor(acc, o, 64);
-    if (lane == 0) {
-      if constexpr (OUT_DT == DT_F32) {
-        reinterpret_cast<float*>(g.y)[i * g.ldy + j] = acc;
-      } else {
-        reinterpret_cast<uint16_t*>(g.y)[i * g.ldy + j] = (uint16_t)(cvt_pair<OUT_DT>(acc, 0.0f) & 0xFFFFu);
+      for (int t = 0; t < GPC; t += 8) {
+        const vec v = *reinterpret_cast<const vec_any*>(ps + g0 + t);
+#pragma unroll
+        for (int e = 0; e < (GPC < 8 ? GPC : 8) / 2; ++e) sc[set][t / 2 + e] = v[e];
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < GPC; t += 2)
+        sc[set][t / 2] = ps[min(g0 + t, groups - 1)] | ((unsigned)ps[min(g0 + t + 1, groups - 1)] << 16);
+    }
+  };
+  v4i xr[XL];
+  auto load_x = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < XL; ++t) {
+      const int rp = wave + 4 * t, part = rp % KS, row = rp / KS;
+      if (row >= rows) break;
+      const int q0 = pieces * part / KS + GV_CHUNK * c, q1 = pieces * (part + 1) / KS;
+      const int at = 128 * q0 + 8 * lane;
+      xr[t] = at < min(g.k, 128 * q1) ? *reinterpret_cast<const v4i*>(g.x + (m0 + row) * g.ldx + at) : v4i{};
+    }
+  };
+  auto store_x = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < XL; ++t) {
+      const int rp = wave + 4 * t, part = rp % KS, row = rp / KS;
+      if (row >= rows) break;
+      const v4i v = xr[t];
+      // dword pairs (e, e + 4)
+      const v4i o = {(int)__builtin_amdgcn_perm((unsigned)v.z, (unsigned)v.x, 0x05040100u),
+                     (int)__builtin_amdgcn_perm((unsigned)v.z, (unsigned)v.x, 0x07060302u),
+                     (int)__builtin_amdgcn_perm((unsigned)v.w, (unsigned)v.y, 0x05040100u),
+                     (int)__builtin_amdgcn_perm((unsigned)v.w, (unsigned)v.y, 0x07060302u)};
+      *reinterpret_cast<v4i*>(s_x + ((buf * KS + part) * rows + row) * GV_ROW + 16 * lane) = o;
+    }
+  };
+  auto mma = [&](v4i a, v4i b, v4f c) {
+    if constexpr (DT == DT_BF16)
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(in8, a), __builtin_bit_cast(in8, b), c, 0, 0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(in8, a), __builtin_bit_cast(in8, b), c, 0, 0, 0);
+  };
+  // Eight codes of a dword as c + 24, pairs (t, t + 4).  The constants are kept in registers:
+  // and-or takes one literal at most.
+  unsigned mask = DT == DT_BF16 ? 0x00780078u : 0x03C003C0u, sixteen = DT == DT_BF16 ? 0x41804180u : 0x4C004C00u;
+  asm("" : "+v"(mask), "+v"(sixteen));
+  auto widen = [&](unsigned c) {
+    const unsigned u = c ^ 0x88888888u;
+    if constexpr (DT == DT_BF16)
+      return v4i{(int)(((u << 3) & mask) | sixteen), (int)(((u >> 1) & mask) | sixteen),
+                 (int)(((u >> 5) & mask) | sixteen), (int)(((u >> 9) & mask) | sixteen)};
+    else
+      return v4i{(int)(((u << 6) & mask) | sixteen), (int)(((u << 2) & mask) | sixteen),
+                 (int)(((u >> 2) & mask) | sixteen), (int)(((u >> 6) & mask) | sixteen)};
+  };
+  constexpr int M24 = DT == DT_BF16 ? (int)0xC1C0C1C0u : (int)0xCE00CE00u;
+  const v4i minus24 = {M24, M24, M24, M24};
+
+  v4f y[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) y[i] = v4f{};
+  // whole: every piece of the chunk is there in full (no branch between the pieces).
+  auto compute = [&](auto whole, int set, int buf, int c) __attribute__((always_inline)) {
+    const uint8_t* xb[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+      xb[i] = s_x + ((buf * KS + kw) * rows + min(16 * i + rl, rows - 1)) * GV_ROW + 16 * kq;
+#pragma unroll
+    for (int u = 0; u < GV_CHUNK; ++u) {
+      const int q = p0 + GV_CHUNK * c + u;
+      if (!decltype(whole)::value && q >= p1) break;
+      const v4i t = w[set][u];
+      const auto r02 = __builtin_amdgcn_permlane32_swap((unsigned)t.x, (unsigned)t.z, false, false);
+      const auto r13 = __builtin_amdgcn_permlane32_swap((unsigned)t.y, (unsigned)t.w, false, false);
+      const auto e01 = __builtin_amdgcn_permlane16_swap(r02[0], r13[0], false, false);
+      const auto e23 = __builtin_amdgcn_permlane16_swap(r02[1], r13[1], false, false);
+      const unsigned wt[4] = {e01[0], e01[1], e23[0], e23[1]};
+#pragma unroll
+      for (int j0 = 0; j0 < 4; j0 += GROUP / 32) {
+        if (!decltype(whole)::value && 128 * q + 32 * j0 >= g.k) break;
+        v4i xf[GROUP / 32][MB];
+        v4f acc[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          acc[i] = v4f{};
+#pragma unroll
+          for (int j = 0; j < GROUP / 32; ++j) {
+            xf[j][i] = *reinterpret_cast<const v4i*>(xb[i] + 256 * u + 64 * (j0 + j));
+            acc[i] = mma(xf[j][i], minus24, acc[i]);
+          }
+        }
+        float s0, s1;
+        const int si = u * GPP + j0 / (GROUP / 32);
+        decode2<DT>(sc[set][si / 2], s0, s1);
+        const float s = si & 1 ? s1 : s0;
+#pragma unroll
+        for (int j = 0; j < GROUP / 32; ++j) {
+          const v4i wf = widen(wt[j0 + j]);
+#pragma unroll
+          for (int i = 0; i < MB; ++i) acc[i] = mma(xf[j][i], wf, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y[i][r] = __builtin_fmaf(s, acc[i][r], y[i][r]);
+      }
+    }
+  };
+  load_x(0);
+#pragma unroll
+  for (int i = 0; i < GV_SETS - 1; ++i) load_w(i, i);
+  store_x(0);
+  __syncthreads();
+  for (int c0 = 0; c0 < chunks; c0 += GV_SETS) {
+#pragma unroll
+    for (int i = 0; i < GV_SETS; ++i) {
+      const int c = c0 + i;
+      if (c < chunks) {
+        if (c + 1 < chunks) load_x(c + 1);
+        load_w((i + GV_SETS - 1) % GV_SETS, c + GV_SETS - 1);
+        const int qe = p0 + GV_CHUNK * (c + 1);
+        if (qe <= p1 && 128 * qe <= g.k) compute(std::true_type{}, i, c & 1, c);
+        else compute(std::false_type{}, i, c & 1, c);
+        if (c + 1 < chunks) store_x((c + 1) & 1);
+        __syncthreads();
       }
     }
   }
+  if constexpr (KS > 1) {
+    v4f* part = reinterpret_cast<v4f*>(s_x);  // [wave][MB][64]
+#pragma unroll
+    for (int i = 0; i < MB; ++i) part[(wave * MB + i) * 64 + lane] = y[i];
+    __syncthreads();
+    if (kw) return;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int q = 1; q < KS; ++q) y[i] += part[((wave + q) * MB + i) * 64 + lane];
+  }
+  const int n = n0 + rl;
+  if (n >= g.n) return;
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = m0 + 16 * i + 4 * kq + r;
+      if (m >= g.m) continue;
+      const int64_t o = m * g.ldy + n;
+      if (g.out_dt == DT_F32) reinterpret_cast<float*>(g.y)[o] = y[i][r];
+      else reinterpret_cast<uint16_t*>(g.y)[o] = (uint16_t)((g.out_dt == DT_BF16 ? cvt_pair<DT_BF16>(y[i][r], 0.0f) : cvt_pair<DT_F16>(y[i][r], 0.0f)) & 0xFFFFu);
+    }
+}
+
+template <int DT, int GROUP, int KS, int MB>
+static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
+  const int rows = a.m < 16 * MB ? a.m : 16 * MB;
+  size_t shm = (size_t)2 * KS * rows * GV_ROW;
+  if (shm < (size_t)4 * MB * 64 * 16) shm = (size_t)4 * MB * 64 * 16;  // the parts' joining
+  const dim3 grid((unsigned)((a.n + 64 / KS - 1) / (64 / KS)), (unsigned)((a.m + 16 * MB - 1) / (16 * MB)));
+#define VQ_GEMV_XL(X) hipLaunchKernelGGL((k_w4gemv<DT, GROUP, KS, MB, X>), grid, dim3(256), shm, st, a)
+  if constexpr (MB == 2) {
+    VQ_GEMV_XL(8);
+  } else {
+    if (rows * KS <= 4) VQ_GEMV_XL(1);
+    else if (rows * KS <= 8) VQ_GEMV_XL(2);
+    else if (rows * KS <= 16) VQ_GEMV_XL(4);
+    else VQ_GEMV_XL(8);
+  }
+#undef VQ_GEMV_XL
+}
+
+template <int DT, int GROUP>
+static void launch_gemv_group(const GemvArgs& a, hipStream_t st) {
+  // Parts of K: four up to 16384 channels, then two.  One row, us with 2 / 4: 4096 -> 12288
+  // 10.2 / 9.4, 16384 -> 2048 28.4 / 15.9, 8192 -> 28672 30.3 / 31.0; seven rows, groups of 32,
+  // 8192 -> 28671 42.9 / 53.8.  x of more than 8 rows leaves room in LDS for two parts,
+  // of more than 16 for one.
+  const int ks = a.n <= 16384 ? 4 : 2;
+  if (a.m > 16) launch_gemv_part<DT, GROUP, 1, 2>(a, st);
+  else if (ks == 4 && a.m <= 8) launch_gemv_part<DT, GROUP, 4, 1>(a, st);
+  else launch_gemv_part<DT, GROUP, 2, 1>(a, st);
+}
+
+template <int DT>
+static void launch_gemv_dt(const GemvArgs& a, hipStream_t st) {
+  if (a.group == 32) launch_gemv_group<DT, 32>(a, st);
+  else if (a.group == 64) launch_gemv_group<DT, 64>(a, st);
+  else launch_gemv_group<DT, 128>(a, st);
 }
 
 }  // namespace vqk
@@ -126,22 +356,9 @@ hipError_t launch_w4gemv(const W4GemvParams& p, hipStream_t st) {
   a.n = (int)p.n;
   a.k = (int)p.k;
   a.group = p.group;
-  const dim3 grid((unsigned)((p.n + 3) / 4), (unsigned)(p.m < 1024 ? p.m : 1024));
-#define VQ_GEMV(I, O) hipLaunchKernelGGL((k_w4gemv<I, O>), grid, dim3(256), 0, st, a)
-  if (p.in_dt == DT_BF16) {
-    switch (p.out_dt) {
-      case DT_F16: VQ_GEMV(DT_BF16, DT_F16); break;
-      case DT_BF16: VQ_GEMV(DT_BF16, DT_BF16); break;
-      default: VQ_GEMV(DT_BF16, DT_F32); break;
-    }
-  } else {
-    switch (p.out_dt) {
-      case DT_F16: VQ_GEMV(DT_F16, DT_F16); break;
-      case DT_BF16: VQ_GEMV(DT_F16, DT_BF16); break;
-      default: VQ_GEMV(DT_F16, DT_F32); break;
-    }
-  }
-#undef VQ_GEMV
+  a.out_dt = p.out_dt;
+  if (p.in_dt == DT_BF16) launch_gemv_dt<DT_BF16>(a, st);
+  else launch_gemv_dt<DT_F16>(a, st);
   return hipGetLastError();
 }
 
