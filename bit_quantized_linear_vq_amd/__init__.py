@@ -668,30 +668,32 @@ def vq_step_control(state: torch.Tensor, params: ControlParams, delta_new=None, 
 _HALF = (torch.float16, torch.bfloat16)
 
 
-class _on_device:
-    """Makes t's device the current one for a launch on its stream, where it is not."""
-    __slots__ = ("index", "prev")
-
-    def __init__(self, t):
-        self.index = t.get_device()
-        self.prev = -1
-
-    def __enter__(self):
-        if torch._C._cuda_getDevice() != self.index:
-            self.prev = torch._C._cuda_exchangeDevice(self.index)
-
-    def __exit__(self, *exc):
-        if self.prev >= 0:
-            torch._C._cuda_exchangeDevice(self.prev)
-        return False
+_getdev = torch._C._cuda_getDevice
+_rawstream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows16(t, name, device=None, dtype=None):
+def _launch(fn, index, *args):
+    """Calls a launch entry point of the library on torch's current stream of device `index`,
+    with that device current."""
+    f = getattr(_lib, fn)
+    if _getdev() == index:
+        status = f(*args, _rawstream(index))
+    else:
+        prev = torch._C._cuda_exchangeDevice(index)
+        try:
+            status = f(*args, _rawstream(index))
+        finally:
+            torch._C._cuda_exchangeDevice(prev)
+    if status:
+        _check(fn, status)
+
+
+def _rows16(t, name, index=None, dtype=None):
     """A 2-D 16-bit device tensor with unit stride along its rows and a row pitch of at
     least a row (the pitch of a single row is taken as dense).  Returns the pitch."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and (device is None or t.device == device)):
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor{'' if device is None else f' on {device}'}")
-    if t.dtype not in _HALF if dtype is None else t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (index is not None and t.get_device() != index):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor{'' if index is None else f' on device {index}'}")
+    if t.dtype not in _HALF if dtype is None else t.dtype is not dtype:
         raise TypeError(f"{name} must be {'float16 or bfloat16' if dtype is None else dtype}, not {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
@@ -702,47 +704,59 @@ def _rows16(t, name, device=None, dtype=None):
     return ld if m > 1 else k
 
 
+def _dense(t, name, index, dtypes, numel):
+    """_in for a device index: a contiguous tensor there, of one of dtypes, with numel elements at least."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor on device {index}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, {numel} are needed")
+
+
 def _norm_operands(x, weight, residual, sum_out):
     ldx = _rows16(x, "x")
     m, k = x.shape
-    dev = x.device
+    dt, index = x.dtype, x.get_device()
+    w_ptr, w_dt = None, _DT[dt]
     if weight is not None:
-        _in(weight, "weight", (x.dtype, torch.float32), k, dev)
+        _dense(weight, "weight", index, (dt, torch.float32), k)
         if weight.numel() != k:
             raise ValueError(f"weight must hold {k} elements")
-    ldr = k
+        w_ptr, w_dt = weight.data_ptr(), _DT[weight.dtype]
+    r_ptr, ldr = None, k
     if residual is not None:
-        ldr = _rows16(residual, "residual", dev, x.dtype)
+        ldr = _rows16(residual, "residual", index, dt)
         if residual.shape != x.shape:
             raise ValueError("residual must have x's shape")
+        r_ptr = residual.data_ptr()
+    h_ptr, ldh = None, k
     if sum_out is not None:
         if residual is None:
             raise ValueError("sum_out goes with a residual")
-        ldh = _rows16(sum_out, "sum_out", dev, x.dtype)
+        ldh = _rows16(sum_out, "sum_out", index, dt)
         if sum_out.shape != x.shape:
             raise ValueError("sum_out must have x's shape")
+        h_ptr = sum_out.data_ptr()
     elif residual is not None:
-        sum_out, ldh = torch.empty((m, k), dtype=x.dtype, device=dev), k
-    else:
-        ldh = k
-    w_dt = _DT[x.dtype] if weight is None else _DT[weight.dtype]
-    return m, k, ldx, ldr, w_dt, sum_out, ldh
+        sum_out = torch.empty((m, k), dtype=dt, device=x.device)
+        h_ptr = sum_out.data_ptr()
+    return m, k, index, (x.data_ptr(), r_ptr, _DT[dt], m, k, ldx, ldr, w_ptr, w_dt), sum_out, h_ptr, ldh
 
 
 def vq_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, residual=None, y=None, sum_out=None):
     """Root-mean-square norm of the rows of x (+ residual), times weight (None: ones).
     Returns y, or (y, h) with a residual, h = x + residual (sum_out; it may be x or residual)."""
-    m, k, ldx, ldr, w_dt, sum_out, ldh = _norm_operands(x, weight, residual, sum_out)
+    m, k, index, head, sum_out, h_ptr, ldh = _norm_operands(x, weight, residual, sum_out)
     if y is None:
         y, ldy = torch.empty((m, k), dtype=x.dtype, device=x.device), k
     else:
-        ldy = _rows16(y, "y", x.device, x.dtype)
+        ldy = _rows16(y, "y", index, x.dtype)
         if y.shape != x.shape:
             raise ValueError("y must have x's shape")
-    with _on_device(x):
-        _check("vq_rmsnorm", _lib.vq_rmsnorm(
-            _ptr(x), _ptr(residual), _DT[x.dtype], m, k, ldx, ldr, _ptr(weight), w_dt, eps, _ptr(y), ldy,
-            _ptr(sum_out), ldh, _stream(x)))
+    _launch("vq_rmsnorm", index, *head, eps, y.data_ptr(), ldy, h_ptr, ldh)
     return y if residual is None else (y, sum_out)
 
 
@@ -751,32 +765,29 @@ def vq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, bits: int, ep
                      bits_dev: torch.Tensor | None = None, codes=None, scales=None, sum_out=None):
     """vq_rmsnorm's rows as activation codes, quantized as vq_quant_act does (gran "token" or
     "static").  Returns (codes int8 [M x kp], scales), or (codes, scales, h) with a residual."""
-    m, k, ldx, ldr, w_dt, sum_out, ldh = _norm_operands(x, weight, residual, sum_out)
-    dev = x.device
+    m, k, index, head, sum_out, h_ptr, ldh = _norm_operands(x, weight, residual, sum_out)
     n_out = 0
     if idx is not None:
         n_out = int(idx.numel())
-        _in(idx, "idx", _I32, n_out, dev)
+        _dense(idx, "idx", index, _I32, n_out)
     parts = 2 if n_out else 1
     if static_scale is not None:
-        _in(static_scale, "static_scale", _F32, parts, dev)
+        _dense(static_scale, "static_scale", index, _F32, parts)
     if bits_dev is not None:
-        _in(bits_dev, "bits_dev", _I32, 1, dev)
-    kp = vq_packed_k(k, n_out)
+        _dense(bits_dev, "bits_dev", index, _I32, 1)
+    kp = vq_packed_k(k, n_out) if n_out else k
     g = _GRAN.get(gran, -1)
     if codes is None:
-        codes = torch.empty((m, kp), dtype=torch.int8, device=dev)
+        codes = torch.empty((m, kp), dtype=torch.int8, device=x.device)
     else:
-        _in(codes, "codes", (torch.int8,), m * kp, dev)
+        _dense(codes, "codes", index, (torch.int8,), m * kp)
     if scales is None:
         shape = ((m, 2) if n_out else (m,)) if g == VQ_PER_TOKEN else (parts,)
-        scales = torch.empty(shape, dtype=torch.float32, device=dev)
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
     else:
-        _in(scales, "scales", _F32, (m if g == VQ_PER_TOKEN else 1) * parts, dev)
-    with _on_device(x):
-        _check("vq_rmsnorm_quant", _lib.vq_rmsnorm_quant(
-            _ptr(x), _ptr(residual), _DT[x.dtype], m, k, ldx, ldr, _ptr(weight), w_dt, eps, bits, _ptr(bits_dev), g,
-            _ptr(idx), n_out, _ptr(static_scale), _ptr(codes), _ptr(scales), _ptr(sum_out), ldh, _stream(x)))
+        _dense(scales, "scales", index, _F32, (m if g == VQ_PER_TOKEN else 1) * parts)
+    _launch("vq_rmsnorm_quant", index, *head, eps, bits, _ptr(bits_dev), g, _ptr(idx), n_out, _ptr(static_scale),
+            codes.data_ptr(), scales.data_ptr(), h_ptr, ldh)
     return (codes, scales) if residual is None else (codes, scales, sum_out)
 
 
@@ -787,15 +798,15 @@ def vq_pack_weights_group(w: torch.Tensor, group: int = 128, codes=None, scales=
     n, k = w.shape
     if group not in (32, 64, 128) or k % group:
         raise ValueError("group must be 32, 64 or 128 and divide K")
+    index = w.get_device()
     if codes is None:
         codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
     if scales is None:
         scales = torch.empty((n, k // group), dtype=w.dtype, device=w.device)
-    _in(codes, "codes", _U8, n * (k // 2), w.device)
-    _in(scales, "scales", (w.dtype,), n * (k // group), w.device)
-    with _on_device(w):
-        _check("vq_pack_weights_group", _lib.vq_pack_weights_group(
-            _ptr(w), _DT[w.dtype], n, k, ldw, group, _ptr(codes), _ptr(scales), _stream(w)))
+    _dense(codes, "codes", index, _U8, n * (k // 2))
+    _dense(scales, "scales", index, (w.dtype,), n * (k // group))
+    _launch("vq_pack_weights_group", index, w.data_ptr(), _DT[w.dtype], n, k, ldw, group, codes.data_ptr(),
+            scales.data_ptr())
     return codes, scales
 
 
@@ -804,37 +815,34 @@ def vq_w4_gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out_d
     group is K over the scales per row).  out_dtype defaults to x's.  Returns y."""
     ldx = _rows16(x, "x")
     m, k = x.shape
-    dev = x.device
-    _in(codes, "codes", _U8, 0, dev)
-    _in(scales, "scales", (x.dtype,), 0, dev)
+    dt, index = x.dtype, x.get_device()
+    _dense(codes, "codes", index, _U8, 0)
+    _dense(scales, "scales", index, (dt,), 0)
     if codes.dim() != 2 or scales.dim() != 2 or codes.shape[0] != scales.shape[0] or 2 * codes.shape[1] != k:
         raise ValueError(f"codes and scales must be [N x {k // 2}] and [N x {k} / group]")
     n, groups = scales.shape
     if not groups or k % groups:
         raise ValueError(f"scales must be [N x {k} / group]")
     if y is None:
-        y, ldy = torch.empty((m, n), dtype=out_dtype or x.dtype, device=dev), n
+        y, ldy = torch.empty((m, n), dtype=out_dtype or dt, device=x.device), n
     else:
-        _out2d(y, "y", m, n, dev)
+        _out2d(y, "y", m, n, x.device)
         ldy = y.stride(0) if m > 1 else n
-    with _on_device(x):
-        _check("vq_w4_gemv", _lib.vq_w4_gemv(
-            _ptr(x), _DT[x.dtype], m, n, k, ldx, _ptr(codes), _ptr(scales), k // groups, _ptr(y),
-            _DT.get(y.dtype, -1), ldy, _stream(x)))
+    _launch("vq_w4_gemv", index, x.data_ptr(), _DT[dt], m, n, k, ldx, codes.data_ptr(), scales.data_ptr(),
+            k // groups, y.data_ptr(), _DT.get(y.dtype, -1), ldy)
     return y
 
 
-def _experts_rows(offsets, rows, m, dev, y, n, out_dtype):
-    """Experts, output rows and the output of an experts' product."""
-    _in(offsets, "offsets", _I32, 2, dev)
-    t = m
+def _experts_rows(t, rows, index, device, y, n, out_dtype):
+    """Output rows, the rows' address and the output of an experts' product over t rows of its operand."""
+    r_ptr = None
     if rows is not None:
-        _in(rows, "rows", _I32, 0, dev)
-        t = rows.numel()
+        _dense(rows, "rows", index, _I32, 0)
+        t, r_ptr = rows.numel(), rows.data_ptr()
     if y is None:
-        return offsets.numel() - 1, t, torch.empty((t, n), dtype=out_dtype, device=dev), n
-    _out2d(y, "y", t, n, dev)
-    return offsets.numel() - 1, t, y, y.stride(0) if t > 1 else n
+        return t, r_ptr, torch.empty((t, n), dtype=out_dtype, device=device), n
+    _out2d(y, "y", t, n, device)
+    return t, r_ptr, y, y.stride(0) if t > 1 else n
 
 
 def vq_qgemm_experts(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, b_bits: int,
@@ -847,11 +855,11 @@ def vq_qgemm_experts(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: tor
     if not (isinstance(a, torch.Tensor) and a.is_cuda and a.dim() == 2):
         raise TypeError("a must be a 2-D CUDA (HIP) tensor")
     m, kp = a.shape
-    dev = a.device
-    _in(a, "a", (torch.int8,), m * kp, dev)
-    if not (isinstance(b, torch.Tensor) and b.dim() in (2, 3)):
+    index = a.get_device()
+    _dense(a, "a", index, (torch.int8,), 0)
+    if not isinstance(b, torch.Tensor) or b.dim() not in (2, 3):
         raise TypeError("b must be a 2-D (row-major) or 3-D (K pieces) CUDA (HIP) tensor of packed weight codes")
-    _in(offsets, "offsets", _I32, 2, dev)
+    _dense(offsets, "offsets", index, _I32, 2)
     experts = offsets.numel() - 1
     kblock = b.dim() == 3
     total = b.shape[1] if kblock else b.shape[0]
@@ -860,16 +868,15 @@ def vq_qgemm_experts(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: tor
         raise ValueError(f"b must hold the same number of rows for each of the {experts} experts")
     if b_bits in (4, 8):
         row_bytes = kp if b_bits == 8 else kp // 2
-        _in(b, "b", (torch.int8,) if b_bits == 8 else _U8, 0, dev)
-        if tuple(b.shape) != (((row_bytes + 63) // 64, total, 64) if kblock else (total, row_bytes)):
+        _dense(b, "b", index, (torch.int8,) if b_bits == 8 else _U8, 0)
+        if b.shape != (((row_bytes + 63) // 64, total, 64) if kblock else (total, row_bytes)):
             raise ValueError(f"b must be packed {b_bits}-bit codes of [E * N x {kp}] weights")
-    _in(sa, "sa", _F32, m, dev)
-    _in(sb, "sb", _F32, total, dev)
-    experts, t, y, ldy = _experts_rows(offsets, rows, m, dev, y, n, out_dtype)
-    with _on_device(a):
-        _check("vq_qgemm_experts", _lib.vq_qgemm_experts(
-            _ptr(a), _ptr(sa), _ptr(b), b_bits | (VQ_W_KBLOCK if kblock else 0), _ptr(sb), _ptr(offsets), experts,
-            _ptr(rows), m, t, n, kp, _ptr(y), _DT.get(y.dtype, -1), ldy, _stream(a)))
+    _dense(sa, "sa", index, _F32, m)
+    _dense(sb, "sb", index, _F32, total)
+    t, r_ptr, y, ldy = _experts_rows(m, rows, index, a.device, y, n, out_dtype)
+    _launch("vq_qgemm_experts", index, a.data_ptr(), sa.data_ptr(), b.data_ptr(),
+            b_bits | (VQ_W_KBLOCK if kblock else 0), sb.data_ptr(), offsets.data_ptr(), experts, r_ptr, m, t, n, kp,
+            y.data_ptr(), _DT.get(y.dtype, -1), ldy)
     return y
 
 
@@ -880,24 +887,23 @@ def vq_gemm_dense_experts(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     Rows of y outside the offsets are not written.  Returns y [T x N]."""
     ldx = _rows16(x, "x")
     m, k = x.shape
-    dev = x.device
-    if not (isinstance(w, torch.Tensor) and w.dtype == x.dtype and w.device == dev):
-        raise TypeError(f"w must be a {x.dtype} tensor on {dev}")
+    index = x.get_device()
+    if not isinstance(w, torch.Tensor) or w.dtype is not x.dtype or not w.is_cuda or w.get_device() != index:
+        raise TypeError(f"w must be a {x.dtype} tensor on device {index}")
     if w.dim() != 3 or w.shape[2] != k or not w.shape[0] or not w.shape[1]:
         raise ValueError(f"w must be [E x N x {k}]")
+    e, n = w.shape[:2]
     es, ldw, unit = w.stride()
-    e, n = w.shape[0], w.shape[1]
     if n == 1:
         ldw = max(ldw, k)
     if (k > 1 and unit != 1) or ldw < k or es < 0:
         raise ValueError("w must have unit stride along K and rows that do not overlap")
-    experts, t, y, ldy = _experts_rows(offsets, rows, m, dev, y, n, out_dtype or x.dtype)
-    if experts != e:
+    _dense(offsets, "offsets", index, _I32, 2)
+    if offsets.numel() != e + 1:
         raise ValueError(f"offsets must hold {e + 1} elements")
-    with _on_device(x):
-        _check("vq_gemm_dense_experts", _lib.vq_gemm_dense_experts(
-            _ptr(x), _ptr(w), _DT[x.dtype], _ptr(offsets), e, _ptr(rows), m, t, n, k, ldx, ldw, es, _ptr(y),
-            _DT.get(y.dtype, -1), ldy, _stream(x)))
+    t, r_ptr, y, ldy = _experts_rows(m, rows, index, x.device, y, n, out_dtype or x.dtype)
+    _launch("vq_gemm_dense_experts", index, x.data_ptr(), w.data_ptr(), _DT[x.dtype], offsets.data_ptr(), e, r_ptr, m, t,
+            n, k, ldx, ldw, es, y.data_ptr(), _DT.get(y.dtype, -1), ldy)
     return y
 
 
