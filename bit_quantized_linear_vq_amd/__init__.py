@@ -741,7 +741,7 @@ def _norm_operands(x, weight, residual, sum_out):
             raise ValueError("sum_out must have x's shape")
         h_ptr = sum_out.data_ptr()
     elif residual is not None:
-        sum_out = torch.empty((m, k), dtype=dt, device=x.device)
+        sum_out = torch.empty(m, k, dtype=dt, device=x.device)
         h_ptr = sum_out.data_ptr()
     return m, k, index, (x.data_ptr(), r_ptr, _DT[dt], m, k, ldx, ldr, w_ptr, w_dt), sum_out, h_ptr, ldh
 
@@ -751,7 +751,7 @@ def vq_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, 
     Returns y, or (y, h) with a residual, h = x + residual (sum_out; it may be x or residual)."""
     m, k, index, head, sum_out, h_ptr, ldh = _norm_operands(x, weight, residual, sum_out)
     if y is None:
-        y, ldy = torch.empty((m, k), dtype=x.dtype, device=x.device), k
+        y, ldy = torch.empty(m, k, dtype=x.dtype, device=x.device), k
     else:
         ldy = _rows16(y, "y", index, x.dtype)
         if y.shape != x.shape:
@@ -778,12 +778,12 @@ def vq_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None, bits: int, ep
     kp = vq_packed_k(k, n_out) if n_out else k
     g = _GRAN.get(gran, -1)
     if codes is None:
-        codes = torch.empty((m, kp), dtype=torch.int8, device=x.device)
+        codes = torch.empty(m, kp, dtype=torch.int8, device=x.device)
     else:
         _dense(codes, "codes", index, (torch.int8,), m * kp)
     if scales is None:
         shape = ((m, 2) if n_out else (m,)) if g == VQ_PER_TOKEN else (parts,)
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scales = torch.empty(*shape, dtype=torch.float32, device=x.device)
     else:
         _dense(scales, "scales", index, _F32, (m if g == VQ_PER_TOKEN else 1) * parts)
     _launch("vq_rmsnorm_quant", index, *head, eps, bits, _ptr(bits_dev), g, _ptr(idx), n_out, _ptr(static_scale),
@@ -824,7 +824,7 @@ def vq_w4_gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out_d
     if not groups or k % groups:
         raise ValueError(f"scales must be [N x {k} / group]")
     if y is None:
-        y, ldy = torch.empty((m, n), dtype=out_dtype or dt, device=x.device), n
+        y, ldy = torch.empty(m, n, dtype=out_dtype or dt, device=x.device), n
     else:
         _out2d(y, "y", m, n, x.device)
         ldy = y.stride(0) if m > 1 else n
@@ -840,7 +840,7 @@ def _experts_rows(t, rows, index, device, y, n, out_dtype):
         _dense(rows, "rows", index, _I32, 0)
         t, r_ptr = rows.numel(), rows.data_ptr()
     if y is None:
-        return t, r_ptr, torch.empty((t, n), dtype=out_dtype, device=device), n
+        return t, r_ptr, torch.empty(t, n, dtype=out_dtype, device=device), n
     _out2d(y, "y", t, n, device)
     return t, r_ptr, y, y.stride(0) if t > 1 else n
 

@@ -372,7 +372,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   if (t < 0) return;
 
   struct Tile {
-    int e, r0, rows, n0;
+    int e, r0, rows, n0, cols;
   };
   const int chunk = (E + 63) / 64;
   auto locate = [&](int w) {
@@ -390,10 +390,16 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     x.e = c0 + __builtin_ctzll(h1);
     const int lo = __builtin_amdgcn_readfirstlane(s_lo[x.e]), hi = __builtin_amdgcn_readfirstlane(s_hi[x.e]);
     const int before = !tail && x.e ? __builtin_amdgcn_readfirstlane(s_whole[x.e - 1]) : 0;
-    const int step = BM / split;
-    x.r0 = (tail ? hi - (hi - lo) % BM : lo + (want - before) * BM) + part * step;
-    x.rows = w < whole_items ? min(BM, hi - x.r0) : min(step, hi - x.r0);  // <= 0: a piece of a short tail
-    x.n0 = tn * BN;
+    // A piece is a part of the tile's columns where the rows are few (the time is then that
+    // of the weights), else of its rows.
+    const int r0 = tail ? hi - (hi - lo) % BM : lo + (want - before) * BM;
+    const int rows = min(BM, hi - r0);
+    const bool pieces = w >= whole_items, by_cols = pieces && rows <= 128;
+    const int step = pieces && !by_cols ? BM / split : BM;
+    x.cols = by_cols ? BN / split : BN;
+    x.r0 = r0 + (pieces && !by_cols ? part * step : 0);
+    x.n0 = tn * BN + (by_cols ? part * x.cols : 0);
+    x.rows = x.n0 < g.n ? min(step, r0 + rows - x.r0) : 0;  // <= 0: an empty piece
     return x;
   };
 
@@ -439,14 +445,17 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     }
   };
   // A wave loads 32 rows of A; the waves past a tile's last 64-row block load none.
-  auto issue = [&](int s, bool with_a) {  // called for s = 0, 1, 2, ... of a tile in order
+  // Likewise 32 rows of B, and none past a piece's columns.
+  auto issue = [&](int s, bool with_a, bool with_b) {  // called for s = 0, 1, 2, ... of a tile in order
     uint8_t* base = lds + (s % NST) * STAGE;
     if (with_a) {
 #pragma unroll
       for (int i = 0; i < LA; ++i) dma16(ga[i] + s * ROW, base + (wave * LA + i) * 1024);
     }
+    if (with_b) {
 #pragma unroll
-    for (int i = 0; i < LB; ++i) dma16(gb[i] + boff, base + A_BYTES + (wave * LB + i) * 1024);
+      for (int i = 0; i < LB; ++i) dma16(gb[i] + boff, base + A_BYTES + (wave * LB + i) * 1024);
+    }
     if constexpr (KIND == X_I4) boff += (s & 1) ? g.b_piece - 32 : 32;
     else boff += g.b_piece;
   };
@@ -466,13 +475,15 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   bool pend = false;  // the previous tile's 16 stores follow this tile's first loads
 
   // The K loop of a tile whose rows need NM blocks per wave.
-  auto k_loop = [&](auto nm_c) {
+  auto k_loop = [&](auto nm_c, int cols) {
     constexpr int NM = decltype(nm_c)::value;
     const bool with_a = NM == MBLK || wave < 2 * NM;
+    const bool with_b = NM > 2 || 32 * wave < cols, active = NM > 2 || WTN * wn < cols;
     auto wait_next = [&](bool stores) {  // every load but the last stage's done
       if (stores) wait_vmcnt<(D - 1) * L + 16>();  // whole tiles only: see pend
-      else if (with_a) wait_vmcnt<(D - 1) * L>();
-      else wait_vmcnt<(D - 1) * LB>();
+      else if (with_a && with_b) wait_vmcnt<(D - 1) * L>();
+      else if (with_b) wait_vmcnt<(D - 1) * LB>();
+      else wait_vmcnt<(D - 1) * LA>();  // (a wave without loads waits for nothing)
     };
     auto wait_groups = [&](int later) {
       if (later < 1) wait_vmcnt<0>();
@@ -517,23 +528,23 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     if (grp == 1) sched_barrier_all();
     int p = 0;
     for (; p + D < nk; ++p) {
-      read_stage(p % NST);
-      issue(p + D, with_a);
+      if (active) read_stage(p % NST);
+      issue(p + D, with_a, with_b);
       const bool early = pend && with_a && p < D - 1;  // stage p + 1 was loaded before the stores
       if (grp == 1) wait_next(early);
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       sched_barrier_all();
-      compute();
+      if (active) compute();
       if (grp == 0) wait_next(early);
       sched_barrier_all();
     }
     for (; p < nk; ++p) {
-      read_stage(p % NST);
+      if (active) read_stage(p % NST);
       const int later = nk - p - 2;
       if (grp == 1) wait_groups(later);
       __builtin_amdgcn_s_waitcnt(0xC07F);
       sched_barrier_all();
-      compute();
+      if (active) compute();
       if (grp == 0) wait_groups(later);
       sched_barrier_all();
     }
@@ -554,15 +565,15 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   }
 #pragma unroll
   for (int s = 0; s < D; ++s)
-    if (s < nk) issue(s, wave < 2 * ((cur.rows + 63) / 64));
+    if (s < nk) issue(s, wave < 2 * ((cur.rows + 63) / 64), 32 * wave < cur.cols);
   int buf = 0;
   typedef typename std::conditional<OUT_DT == DT_BF16, __bf16, _Float16>::type h_t;
   for (;;) {
     const int nm = (cur.rows + 63) / 64;
-    if (nm == 4) k_loop(std::integral_constant<int, 4>{});
-    else if (nm == 3) k_loop(std::integral_constant<int, 3>{});
-    else if (nm == 2) k_loop(std::integral_constant<int, 2>{});
-    else k_loop(std::integral_constant<int, 1>{});
+    if (nm == 4) k_loop(std::integral_constant<int, 4>{}, cur.cols);
+    else if (nm == 3) k_loop(std::integral_constant<int, 3>{}, cur.cols);
+    else if (nm == 2) k_loop(std::integral_constant<int, 2>{}, cur.cols);
+    else k_loop(std::integral_constant<int, 1>{}, cur.cols);
 
     const bool has_next = more;
     const Tile c = cur;
@@ -579,9 +590,9 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       }
 #pragma unroll
       for (int s = 0; s < D; ++s)
-        if (s < nk) issue(s, wave < 2 * ((cur.rows + 63) / 64));
+        if (s < nk) issue(s, wave < 2 * ((cur.rows + 63) / 64), 32 * wave < cur.cols);
     }
-    const bool full = c.rows == BM && c.n0 + BN <= g.n;
+    const bool full = c.rows == BM && c.n0 + BN <= g.n;  // (of all columns: pieces by columns have few rows)
     pend = HALF_OUT && has_next && full;
     v4f sb_r[NBLK][4];
     if constexpr (INT) {
@@ -592,7 +603,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     }
 #pragma unroll
     for (int mb = 0; mb < MBLK; ++mb) {
-      if (mb >= nm) break;
+      if (mb >= nm || WTN * wn >= c.cols) break;
       const int ml = 64 * mb + 32 * wm + rl;
       const int m = c.r0 + ml;
       const float sa0 = s_sa[buf][ml];
@@ -660,7 +671,7 @@ static hipError_t launch_pp_kind(XArgs a, int out_dt, hipStream_t st) {
   const int64_t tiles = (a.t / xp::BM + (a.experts < a.t ? a.experts : a.t)) * (int64_t)((a.n + xp::BN - 1) / xp::BN);
   a.max_items = (int)tiles;  // at most 2^30 (the entry point's limits)
   const int pb = vq_internal::persistent_blocks();
-  const dim3 grid((unsigned)(tiles < pb ? tiles : pb));
+  const dim3 grid((unsigned)std::min<int64_t>(4 * tiles, pb));  // a tile may be cut in four
   const size_t shm = (size_t)a.experts * 16;  // at most 16 KB beside the 132 KB of the ring and scales
   switch (out_dt) {
     case DT_F16: hipLaunchKernelGGL((k_experts_pp<KIND, DT_F16>), grid, dim3(xp::NT), shm, st, a); break;
