@@ -9,6 +9,7 @@
 // have, and a workgroup finds its tile from the offsets (a prefix sum of the experts' tile
 // counts, 64 experts per wave step) or ends.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "dev_common.h"
@@ -688,11 +689,16 @@ static hipError_t launch_kind(const XArgs& a, int out_dt, hipStream_t st) {
   // over 32 experts, 2048 -> 2048 (256 such tiles), us: 8-bit weights, 4 / 8 / 16 rows each,
   // 28.4 / 29.8 / 37.8 against 29.1 / 29.5 / 30.3; 4-bit 16.9 / 19.0 / 25.1 against 20.1 /
   // 20.8 / 20.7; 16-bit 50.6 / 55.0 / 73.0 against 67.9 / 67.8 / 68.8.  With fewer tiles the
-  // limit of 8 rows goes up as their number goes down.
-  const int64_t tiles = std::min<int64_t>(a.experts, a.t) * ((a.n + xp::BN - 1) / xp::BN);
+  // rows from which the other one wins grow a little more slowly than their number falls:
+  // 64 tiles (8 experts, 4096 -> 2048), 16 / 32 rows each, 19.1 / 29.2 against 21.4 / 21.5,
+  // 14.3 / 21.0 against 25.0 / 25.1, 39.0 / 58.6 against 54.1 / 54.2; 16 tiles (2 experts), 64
+  // rows each, 18.1 against 23.2, 13.2 against 27.6, 32.6 against 41.0.
+  const int64_t used = std::min<int64_t>(a.experts, a.t);
   const int64_t cus = vq_internal::persistent_blocks();
-  const int64_t few_tiles = (a.t / FEW_M + std::min<int64_t>(a.experts, a.t)) * ((a.n + FEW_N - 1) / FEW_N);
-  if (a.t * std::min(tiles, cus) > 8 * a.experts * cus || few_tiles > (1 << 23))
+  const int64_t tiles = std::min<int64_t>(used * ((a.n + xp::BN - 1) / xp::BN), cus);
+  const int64_t few_tiles = (a.t / FEW_M + used) * ((a.n + FEW_N - 1) / FEW_N);
+  const double few_rows = (KIND == X_I8 ? 6.0 : 10.0) * std::pow((double)cus / (double)tiles, 0.75);
+  if ((double)a.t > few_rows * (double)a.experts || few_tiles > (1 << 23))
     return launch_pp_kind<KIND>(a, out_dt, st);
   return launch_few_kind<KIND>(a, out_dt, st);
 }

@@ -80,7 +80,8 @@ struct GemvArgs {
 // A lane's accumulators hold one output channel (lane mod 16) and rows 4 (lane div 16) + i, so
 // a group's scale is one value per lane: y += s * acc.
 //
-// A workgroup's four waves take KS parts of K times 4 / KS blocks of 16 channels.  x goes
+// A workgroup's waves (four, or KS where that is more) take KS parts of K times blocks of 16
+// channels.  x goes
 // through LDS in chunks of 4 pieces (512 channels) of every part, its pairs put in order
 // once per workgroup (rows 1040 bytes apart: 16 rows then read 16 bytes each without a bank
 // conflict); the weights come straight to registers, a chunk ahead (two ahead was even or
@@ -90,18 +91,20 @@ constexpr int GV_SETS = 2;
 constexpr int GV_CHUNK = 4;                         // pieces
 constexpr int GV_ROW = GV_CHUNK * 256 + 16;         // bytes of a row of a chunk of x in LDS
 constexpr int GV_ROWS = 32;                         // rows times parts at most
+constexpr int gv_waves(int ks) { return ks < 4 ? 4 : ks; }
 
 template <int DT, int GROUP, int KS, int MB, int XL>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k_w4gemv(GemvArgs g) {
+__global__ __launch_bounds__(64 * gv_waves(KS)) __attribute__((amdgpu_waves_per_eu(KS == 16 ? 4 : 3))) void k_w4gemv(GemvArgs g) {
   typedef typename std::conditional<DT == DT_BF16, __bf16, _Float16>::type in_t;
   typedef in_t in8 __attribute__((ext_vector_type(8)));
   constexpr int GPP = 128 / GROUP;     // groups of a piece
   constexpr int GPC = GPP * GV_CHUNK;  // and of a chunk
+  constexpr int WAVES = gv_waves(KS);
   extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];  // [2][part][row][GV_ROW]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rl = lane & 15, kq = lane >> 4;
   const int kw = wave % KS, nw = wave / KS;
-  const int n0 = ((int)blockIdx.x * (4 / KS) + nw) * 16, m0 = blockIdx.y * (16 * MB);
+  const int n0 = ((int)blockIdx.x * (WAVES / KS) + nw) * 16, m0 = blockIdx.y * (16 * MB);
   const int rows = min(16 * MB, g.m - m0);
   const int pieces = (g.k + 127) / 128;
   const int p0 = pieces * kw / KS, p1 = pieces * (kw + 1) / KS;
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k
   auto load_x = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < XL; ++t) {
-      const int rp = wave + 4 * t, part = rp % KS, row = rp / KS;
+      const int rp = wave + WAVES * t, part = rp % KS, row = rp / KS;
       if (row >= rows) break;
       const int q0 = pieces * part / KS + GV_CHUNK * c, q1 = pieces * (part + 1) / KS;
       const int at = 128 * q0 + 8 * lane;
@@ -152,7 +155,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k
   auto store_x = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < XL; ++t) {
-      const int rp = wave + 4 * t, part = rp % KS, row = rp / KS;
+      const int rp = wave + WAVES * t, part = rp % KS, row = rp / KS;
       if (row >= rows) break;
       const v4i v = xr[t];
       // dword pairs (e, e + 4)
@@ -282,17 +285,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3))) void k
 
 template <int DT, int GROUP, int KS, int MB>
 static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
+  constexpr int WAVES = gv_waves(KS), COLS = 16 * WAVES / KS;
   const int rows = a.m < 16 * MB ? a.m : 16 * MB;
   size_t shm = (size_t)2 * KS * rows * GV_ROW;
-  if (shm < (size_t)4 * MB * 64 * 16) shm = (size_t)4 * MB * 64 * 16;  // the parts' joining
-  const dim3 grid((unsigned)((a.n + 64 / KS - 1) / (64 / KS)), (unsigned)((a.m + 16 * MB - 1) / (16 * MB)));
-#define VQ_GEMV_XL(X) hipLaunchKernelGGL((k_w4gemv<DT, GROUP, KS, MB, X>), grid, dim3(256), shm, st, a)
+  if (shm < (size_t)WAVES * MB * 64 * 16) shm = (size_t)WAVES * MB * 64 * 16;  // the parts' joining
+  const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)((a.m + 16 * MB - 1) / (16 * MB)));
+  const int loads = (rows * KS + WAVES - 1) / WAVES;  // of x, per thread and chunk
+#define VQ_GEMV_XL(X) hipLaunchKernelGGL((k_w4gemv<DT, GROUP, KS, MB, X>), grid, dim3(64 * WAVES), shm, st, a)
   if constexpr (MB == 2) {
     VQ_GEMV_XL(8);
+  } else if constexpr (KS == 16) {
+    if (loads <= 1) VQ_GEMV_XL(1);
+    else VQ_GEMV_XL(2);
   } else {
-    if (rows * KS <= 4) VQ_GEMV_XL(1);
-    else if (rows * KS <= 8) VQ_GEMV_XL(2);
-    else if (rows * KS <= 16) VQ_GEMV_XL(4);
+    if (loads <= 1) VQ_GEMV_XL(1);
+    else if (loads <= 2) VQ_GEMV_XL(2);
+    else if constexpr (KS == 8) VQ_GEMV_XL(4);
+    else if (loads <= 4) VQ_GEMV_XL(4);
     else VQ_GEMV_XL(8);
   }
 #undef VQ_GEMV_XL
@@ -300,13 +309,17 @@ static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
 
 template <int DT, int GROUP>
 static void launch_gemv_group(const GemvArgs& a, hipStream_t st) {
-  // Parts of K: four up to 16384 channels, then two.  One row, us with 2 / 4: 4096 -> 12288
-  // 10.2 / 9.4, 16384 -> 2048 28.4 / 15.9, 8192 -> 28672 30.3 / 31.0; seven rows, groups of 32,
-  // 8192 -> 28671 42.9 / 53.8.  x of more than 8 rows leaves room in LDS for two parts,
-  // of more than 16 for one.
-  const int ks = a.n <= 16384 ? 4 : 2;
+  // Parts of K: waves enough for the whole card, at least two.  One row, us with 2 / 4 / 8 / 16
+  // parts: 16384 -> 2048 28.3 / 16.0 / 12.2 / 10.8; 8192 -> 8192 16.0 / 11.2 / 11.6 / 16.2; 4096 ->
+  // 14336 9.6 / 10.2 / 11.5 / 20.8; 8192 -> 28672 30.3 / 30.2 / 33.4 / 48.4; seven rows, groups of
+  // 32, 8192 -> 28671 40.8 / 53.7.  Many rows of x leave room in LDS for fewer parts.
+  int ks = 2;
+  while (ks < 16 && (int64_t)ks * ((a.n + 15) / 16) < 1600) ks *= 2;
+  while (a.m * ks > GV_ROWS) ks /= 2;
   if (a.m > 16) launch_gemv_part<DT, GROUP, 1, 2>(a, st);
-  else if (ks == 4 && a.m <= 8) launch_gemv_part<DT, GROUP, 4, 1>(a, st);
+  else if (ks == 16) launch_gemv_part<DT, GROUP, 16, 1>(a, st);
+  else if (ks == 8) launch_gemv_part<DT, GROUP, 8, 1>(a, st);
+  else if (ks == 4) launch_gemv_part<DT, GROUP, 4, 1>(a, st);
   else launch_gemv_part<DT, GROUP, 2, 1>(a, st);
 }
 
