@@ -529,6 +529,8 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
 
 namespace {
 bool ok_group(int group) { return group == 32 || group == 64 || group == 128; }
+// Limits of the product's launch grid.
+constexpr int64_t kMaxGemvRows = (int64_t)1 << 20, kMaxGemvCols = (int64_t)1 << 24;
 }  // namespace
 
 vq_status vq_pack_weights_group(const void* w, vq_dtype dt, int64_t n, int64_t k, int64_t ldw, int group,
@@ -547,7 +549,7 @@ vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k
   if (!is_16bit(dt) || !valid_dt(out_dt)) return VQ_ERR_INVALID_ARG;
   if (m < 0 || n < 1 || k < 1 || m >= kMaxDim || n >= kMaxDim || k >= kMaxDim) return VQ_ERR_INVALID_ARG;
   if (!codes || !scales || (m > 0 && (!x || !y)) || ldx < k || ldy < n) return VQ_ERR_INVALID_ARG;
-  if (!ok_group(group)) return VQ_ERR_UNSUPPORTED;
+  if (!ok_group(group) || m > kMaxGemvRows || n > kMaxGemvCols) return VQ_ERR_UNSUPPORTED;
   if (k % group || !aligned16(x) || ldx % 8 || !aligned16(codes) || reinterpret_cast<uintptr_t>(scales) % 2)
     return VQ_ERR_SHAPE;
   if (reinterpret_cast<uintptr_t>(y) % (uintptr_t)elem_size(out_dt)) return VQ_ERR_SHAPE;
@@ -561,6 +563,7 @@ vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k
 namespace {
 // Limits of the experts' launches (grid sizes and 32-bit tile counts).
 constexpr int64_t kMaxExpertRows = (int64_t)1 << 26, kMaxExpertCols = (int64_t)1 << 20, kMaxExperts = 1024;
+constexpr int64_t kMaxExpertK = (int64_t)1 << 24;  // 32-bit byte offsets in a row
 
 vq_status check_experts(const void* a, const void* b, const int32_t* offsets, int64_t experts, const int32_t* rows,
                         int64_t m_a, int64_t t, int64_t n, int64_t k, const void* y, vq_dtype out_dt, int64_t ldy) {
@@ -569,7 +572,7 @@ vq_status check_experts(const void* a, const void* b, const int32_t* offsets, in
   if (experts < 1 || t < 0 || m_a < 0 || n < 1 || k < 1 || m_a >= kMaxDim || k >= kMaxDim || ldy < n)
     return VQ_ERR_INVALID_ARG;
   if ((!rows && t > m_a) || (t > 0 && m_a < 1)) return VQ_ERR_INVALID_ARG;
-  if (t > kMaxExpertRows || n > kMaxExpertCols || experts > kMaxExperts) return VQ_ERR_UNSUPPORTED;
+  if (t > kMaxExpertRows || n > kMaxExpertCols || experts > kMaxExperts || k > kMaxExpertK) return VQ_ERR_UNSUPPORTED;
   if (k % VQ_K_ALIGN || !aligned16(a) || !aligned16(b)) return VQ_ERR_SHAPE;
   if (reinterpret_cast<uintptr_t>(y) % (uintptr_t)elem_size(out_dt)) return VQ_ERR_SHAPE;
   return VQ_OK;

@@ -390,10 +390,9 @@ vq_status vq_gemm_dense(const void* x, const void* w, vq_dtype dt, int64_t m, in
  *              (an outlier index outside [0, k) gives code 0); gran VQ_PER_TOKEN or
  *              VQ_PER_TENSOR_STATIC
  * m = 0 enqueues nothing.  An infinity or NaN in a row makes that row's dynamic scale NaN
- * (its codes are then unspecified), and a scale that overflows nothing else.
- * vq_rmsnorm takes any k up to 32768 and any stride or element-aligned address (multiples
- * of 8 elements and 16-byte addresses are faster); vq_rmsnorm_quant has the alignment rules
- * of vq_quant_act, for x, res and h.
+ * (its codes are then unspecified); one in the weight does so to every row.
+ * vq_rmsnorm takes any k up to 32768, any stride and any element-aligned address;
+ * vq_rmsnorm_quant has the alignment rules of vq_quant_act, for x, res and h.
  * Launches one kernel; nothing is allocated.  Errors: INVALID_ARG, SHAPE, UNSUPPORTED
  * (k > 32768, gran VQ_PER_TENSOR, bits, n_out as for vq_quant_act).
  */
@@ -415,9 +414,10 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  *            zero codes
  *   y[i,j] = RNE_out(sum_g s[j,g] * sum_{k in g} c[j,k] x[i,k]), products exact, sums in
  *            float32 (in an order fixed by the sizes).  The inner sums run over
- *            (c + 24) x with 24 sum x subtracted, so their float32 rounding is relative to
- *            24 max-magnitude weights: |y - exact| <= (k / 8 + 16) 2^-24 * sum_k s 32 |x_k|
- *            before the output rounding.
+ *            (c + 24) x from -24 sum x, so that with G = group
+ *            |y - exact| <= (2 G + k / G + 18) 2^-24 * sum_k 56 |s x_k| before the output
+ *            rounding: a group's 2 G terms pass through sums of magnitudes of at most
+ *            24 sum|x| + 31 sum|x|, and the k / G groups and 16 parts are added
  *   group      32, 64 or 128; k % group == 0
  *   w          device, dt in {F16, BF16}, [n x k], stride ldw (16-byte aligned, ldw % 8 == 0)
  *   codes      device uint8 [n x k/2], 16-byte aligned: two codes per byte, low nibble =
@@ -428,7 +428,7 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  * m is any number of rows (0 enqueues nothing), but the weights are read once for every
  * 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x reach
  * the outputs of their row as NaN.  One kernel; nothing is allocated.
- * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group).
+ * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group, m > 2^20, n > 2^24).
  */
 vq_status vq_pack_weights_group(const void* w, vq_dtype dt, int64_t n, int64_t k, int64_t ldw, int group,
                                 uint8_t* codes, void* scales, hipStream_t stream);
@@ -461,7 +461,7 @@ vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k
  * and replayed with other offsets.
  * Errors: INVALID_ARG (without `rows`, t <= m_a), SHAPE (k % 64, alignment, kp beyond the
  * int32 accumulators as for vq_qgemm_dequant), UNSUPPORTED (b_bits, t > 2^26, n > 2^20,
- * experts > 1024).
+ * k > 2^24, experts > 1024).
  */
 vq_status vq_qgemm_experts(const int8_t* a, const float* sa, const void* b, int b_bits, const float* sb,
                            const int32_t* offsets, int64_t experts, const int32_t* rows, int64_t m_a, int64_t t,

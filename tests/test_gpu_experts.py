@@ -292,3 +292,50 @@ def test_no_rows_and_refusals(vq):
         vq.vq_gemm_dense_experts(x, w.transpose(1, 2), off)
     with pytest.raises(vq.VQError):
         vq.vq_gemm_dense_experts(x[:, :32], w[:, :, :32], off)  # K % 64
+
+
+@pytest.mark.parametrize("counts,n,k,bits", [
+    ([1] * 1000, 24, 64, 8),                        # many experts, a row each
+    ([0] * 500 + [600] + [0] * 499 + [70], 300, 128, 4),  # two of a thousand, in another order of tables
+    ([64, 65, 128, 129, 1, 255, 257, 0, 300], 700, 192, 8),  # tails of every height
+    ([20] * 30, 512, 448, 4),
+    ([100], 2048, 256, 8),                          # one short tile a column, cut by columns
+    ([250, 3], 1030, 320, 4),
+])
+def test_tables_and_pieces(vq, counts, n, k, bits):
+    off = offsets_of(counts)
+    t = int(off[-1])
+    a, sa, b, sb = operands(t, len(counts), n, k, bits, 31)
+    check_int(vq, a, sa, b, sb, n, off, None, t, bits, "bf16", True)
+
+
+@pytest.mark.parametrize("t", [30, 900])
+def test_dense_rows_of_zeros_for_bad_indices(vq, t):
+    """An index outside x gives zeros even where x's first row is not finite."""
+    rng = np.random.default_rng(t)
+    x = gen.to_storage(rng.standard_normal((t, 128)).astype(np.float32), "bf16").to(DEV)
+    x[0] = float("nan")
+    x[1] = float("inf")
+    w = gen.to_storage((rng.standard_normal((2 * 70, 128)) * 0.1).astype(np.float32), "bf16").to(DEV).view(2, 70, 128)
+    rows = torch.arange(t, dtype=torch.int32, device=DEV)
+    rows[3], rows[t // 2], rows[t - 1] = -5, t, 2 ** 31 - 1
+    off = i32([0, t // 3, t])
+    y = vq.vq_gemm_dense_experts(x, w, off, rows=rows)
+    bad = torch.tensor([3, t // 2, t - 1], device=DEV)
+    assert not y[bad].any()
+    keep = torch.ones(t, dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    keep[:2] = False
+    want = vq.vq_gemm_dense_experts(x, w, off)
+    assert torch.equal(y[keep], want[keep]) and bool(torch.isnan(y[0]).all())
+
+
+def test_offsets_that_do_not_ascend(vq):
+    """Unspecified rows, but nothing outside y."""
+    for t, off in ((40, [0, 30, 10, 40]), (900, [0, 800, 100, 900]), (900, [900, 0, 900, 0])):
+        a, sa, b, sb = operands(t, 3, 64, 64, 8, 41)
+        buf = torch.full((t + 20, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+        vq.vq_qgemm_experts(torch.from_numpy(a).to(DEV), torch.from_numpy(sa).to(DEV), torch.from_numpy(b).to(DEV),
+                            torch.from_numpy(sb).to(DEV), 8, i32(off), y=buf[10:t + 10])
+        torch.cuda.synchronize()
+        assert bool((buf[:10] == 7.0).all()) and bool((buf[t + 10:] == 7.0).all())

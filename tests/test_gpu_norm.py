@@ -228,3 +228,36 @@ def test_refusals(vq):
         vq.vq_rmsnorm_quant(x[:, :100], None, 8)  # K % 64
     with pytest.raises(vq.VQError):
         vq.vq_rmsnorm(torch.zeros((1, 32769), dtype=torch.bfloat16, device=DEV), None)
+
+
+@pytest.mark.parametrize("m,k", [(1100, 64), (1030, 4088), (1500, 2056), (1024, 12288), (1200, 9), (1025, 15), (2000, 3)])
+def test_many_rows(vq, m, k):
+    """Row counts that take several pieces a thread, every way a row can end."""
+    x, r, ws, wf = make(m, k, "bf16", True, "f32", 5)
+    y, hs = vq.vq_rmsnorm(dev(x), dev(ws), EPS, residual=dev(r))
+    torch.cuda.synchronize()
+    h, v = onorm.rows(gen.as_numpy_bits(x), "bf16", wf, EPS, gen.as_numpy_bits(r))
+    assert np.array_equal(bits(npb(hs)), bits(h)) and np.array_equal(bits(npb(y)), bits(onum.from_f32(v, "bf16")))
+    xd = dev(x)  # in place, rows that end in an overlapping piece too
+    y2, h2 = vq.vq_rmsnorm(xd, dev(ws), EPS, residual=dev(r), sum_out=xd)
+    assert torch.equal(y2, y) and torch.equal(h2, hs)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_weights_that_are_not_finite(vq, bad):
+    x, _, ws, _ = make(5, 640, "bf16", False, "same")
+    ws = ws.clone()
+    ws[77] = bad
+    _, s = vq.vq_rmsnorm_quant(dev(x), dev(ws), 8, EPS)
+    assert bool(torch.isnan(s).all())
+
+
+def test_codes_of_a_norm_equal_those_of_its_rows_when_exact(vq):
+    """Rows whose normed values are 16-bit already: the fused codes equal the quantizer's."""
+    x = torch.zeros((4, 256), dtype=torch.bfloat16, device=DEV)
+    x[:, :64] = 2.0
+    x[1, :64] = -4.0  # every row's mean square is a power of four: rstd exact
+    c, s = vq.vq_rmsnorm_quant(x, None, 8, 0.0)
+    y = vq.vq_rmsnorm(x, None, 0.0)
+    c2, s2 = vq.vq_quant_act(y, 8, "token")
+    assert torch.equal(c, c2) and torch.equal(s, s2)

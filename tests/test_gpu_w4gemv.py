@@ -168,3 +168,19 @@ def test_captured_and_replayed(vq):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, vq.vq_w4_gemv(t, codes, scales))
+
+
+@pytest.mark.parametrize("m,n,k,group", [(1, 20000, 128, 64), (2, 30, 4128, 32), (9, 33, 640, 64), (16, 2048, 4096, 128)])
+def test_products_of_small_values(vq, m, n, k, group):
+    """fp16 rows and scales below the normal range: nothing is flushed to zero."""
+    rng = np.random.default_rng([m, n])
+    x = gen.to_storage((rng.standard_normal((m, k)) * 2e-6).astype(np.float32), "fp16")
+    w = gen.to_storage((rng.standard_normal((n, k)) * 2e-4).astype(np.float32), "fp16")
+    codes, scales = vq.vq_pack_weights_group(w.to(DEV), group)
+    y = vq.vq_w4_gemv(x.to(DEV), codes, scales, torch.float32)
+    torch.cuda.synchronize()
+    _, packed, s = group4.pack(gen.as_numpy_bits(w), "fp16", group)
+    assert np.array_equal(codes.cpu().numpy(), packed)
+    assert np.array_equal(npb(scales).view(np.uint16), np.asarray(s).view(np.uint16))
+    ex, b = group4.exact(gen.as_numpy_bits(x), "fp16", packed, s, group)
+    within(y, ex, b, "fp32")
