@@ -287,10 +287,7 @@ namespace xp {
 constexpr int BM = 256, BN = 256, NT = 512;
 constexpr int WTN = 64, MBLK = 4, NBLK = 2;
 constexpr int ROW = 64;                  // bytes of an A row per stage: 64 codes or 32 elements
-#ifndef XP_D
-#define XP_D 2
-#endif
-constexpr int NST = 4, D = XP_D;
+constexpr int NST = 4, D = 2;
 constexpr int A_BYTES = BM * ROW;
 constexpr int LA = A_BYTES / (NT * 16);  // direct loads per wave and stage (2)
 }  // namespace xp
@@ -481,7 +478,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     const bool with_a = NM == MBLK || wave < 2 * NM;
     const bool with_b = NM > 2 || 32 * wave < cols, active = NM > 2 || WTN * wn < cols;
     auto wait_next = [&](bool stores) {  // every load but the last stage's done
-      if (stores) wait_vmcnt<(D - 1) * L + 16>();  // whole tiles only: see pend
+      if (stores) wait_vmcnt<(D - 1) * L + 16>();  // whole tiles only: every wave then has L loads a stage
       else if (with_a && with_b) wait_vmcnt<(D - 1) * L>();
       else if (with_b) wait_vmcnt<(D - 1) * LB>();
       else wait_vmcnt<(D - 1) * LA>();  // (a wave without loads waits for nothing)
@@ -523,7 +520,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     for (int i = 0; i < NM; ++i)
 #pragma unroll
       for (int j = 0; j < NBLK; ++j) acc[i][j] = acc_t{};
-    if (pend && with_a && nk > D) wait_next(true);
+    if (pend && NM == MBLK && nk > D) wait_next(true);
     else wait_groups(min(D, nk) - 1);
     sched_barrier_all();
     if (grp == 1) sched_barrier_all();
@@ -531,7 +528,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     for (; p + D < nk; ++p) {
       if (active) read_stage(p % NST);
       issue(p + D, with_a, with_b);
-      const bool early = pend && with_a && p < D - 1;  // stage p + 1 was loaded before the stores
+      const bool early = pend && NM == MBLK && p < D - 1;  // stage p + 1 was loaded before the stores
       if (grp == 1) wait_next(early);
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       sched_barrier_all();

@@ -301,6 +301,9 @@ def test_no_rows_and_refusals(vq):
     ([20] * 30, 512, 448, 4),
     ([100], 2048, 256, 8),                          # one short tile a column, cut by columns
     ([250, 3], 1030, 320, 4),
+    ([4196], 4096, 128, 8),                         # whole rounds of 256 tiles, then a tail cut by columns
+    ([4096 + 70, 20], 4096, 192, 4),
+    ([4096 + 200], 4096, 64, 8),                    # and one cut by rows
 ])
 def test_tables_and_pieces(vq, counts, n, k, bits):
     off = offsets_of(counts)
