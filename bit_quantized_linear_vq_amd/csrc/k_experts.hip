@@ -5,9 +5,9 @@
 // 16-bit rows times 16-bit weights with float32 accumulation.
 //
 // The rows' distribution is known on the device only: offsets[e] .. offsets[e + 1] are
-// expert e's rows.  A launch covers the most tiles that any distribution of the rows can
-// have, and a workgroup finds its tile from the offsets (a prefix sum of the experts' tile
-// counts, 64 experts per wave step) or ends.
+// expert e's rows.  A launch is sized by the number of rows and experts alone, and a
+// workgroup finds its tiles from the offsets: k_experts_few from a prefix sum of the experts'
+// tile counts, 64 experts per wave step, k_experts_pp from a table of it in LDS.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -18,9 +18,9 @@
 
 namespace vqk {
 
-// A 16-byte store at any element's address (the hardware takes unaligned ones): an odd
-// number of outputs leaves every other row unaligned, and storing those element by element
-// took the 8190 x 2048 -> 5759 16-bit case from XXX to 365 us.
+// Wide stores at any element's address (the hardware takes unaligned ones): an odd number of
+// outputs leaves every other row unaligned.  Stored element by element, 8190 rows of 16-bit
+// elements over 8 experts, 2048 -> 5759, took 370 us instead of 281.
 typedef u4v u4v_any __attribute__((aligned(2)));
 typedef u2v u2v_any __attribute__((aligned(2)));
 typedef v4f v4f_any __attribute__((aligned(4)));
@@ -95,11 +95,14 @@ __device__ __forceinline__ v4i unpack4(u2v w) {
 
 // ---------------------------------------------------------------------------------------
 // Few rows per expert (decoding): a product is bound by the weights' bytes, and each is
-// needed by one tile only.  A workgroup owns 16 rows x 32 columns of outputs; its four
-// waves take a quarter of K each, with both operands straight from memory into registers
-// (no LDS and no barriers in the K loop), and the quarters are joined through LDS.  A
-// 16-row fragment load covers whole 64-byte pieces of the weights, 1 KB in all; with the
-// weights in K pieces that is one contiguous block.
+// needed by one tile only.  A workgroup owns 16 rows of outputs and 32 columns for each of
+// its 4 / KS column groups; KS waves share a group's K, with both operands straight from
+// memory into registers (no LDS and no barriers in the K loop), and their sums are joined
+// through LDS.  A 16-row fragment load covers whole 64-byte pieces of the weights, 1 KB in
+// all; with the weights in K pieces that is one contiguous block.  Two pieces a batch:
+// four take registers, and with them waves (16 rows over 16 experts, 1920 -> 5760, 4-bit:
+// 19.9 against 14.6 us).  Measured: 24 rows over 8 experts, 4096 -> 1920, 16-bit, 24.8 us = 4.9 TB/s
+// of weights; the 4-bit case above 12.8 us = 4.4 TB/s.
 constexpr int FEW_STEPS = 2;   // 64-byte pieces of weights in a batch; two batches in flight
 constexpr int FEW_M = 16, FEW_N = 32;
 
@@ -277,12 +280,23 @@ static hipError_t launch_few_kind(const XArgs& a, int out_dt, hipStream_t st) {
 //
 // Ragged shares: an expert's last tile has any number of rows, so a wave's four 32-row
 // blocks are spread over the tile (block 2 mb + wm) and a tile of NM * 64 rows at most runs
-// a K loop of NM blocks per wave: its matrix time follows its rows, in steps of 64, and
-// only the weights' traffic is that of a whole tile.
+// a K loop of NM blocks per wave: its matrix time follows its rows, in steps of 64, waves
+// load no rows that are not there, and only the weights' traffic is that of a whole tile.
 //
-// Tiles: the experts' tile counts are summed into a table in LDS once per workgroup; a
-// wave finds a tile's expert with two ballots over it.  The rows' indices of the tile after
-// next are requested a whole tile ahead of their use.
+// Tiles: the experts' tile counts are summed into a table in LDS once per workgroup (about
+// 3 us with the first loads); a wave finds a tile's expert with two ballots over it.  The rows'
+// indices of a tile are requested a whole tile ahead of their use.  Whole tiles come first,
+// the experts' last ones after them; the tiles of a last round that would leave half of the
+// grid idle are cut in two or four: by rows, or where they have 128 at most by columns,
+// since the time of a short tile is that of its weights (64 rows, 8192 -> 16384: 84 us whole,
+// 54 in four).
+//
+// Measured: 17776 rows over 8 experts, 1920 -> 5760, 8-bit, 238 us = 1.65 POP/s; 6001 over 4,
+// 12288 -> 1920, 4-bit, 167 us = 1.69; 8190 over 8, 2048 -> 5759, 16-bit, 265 us = 0.73 PFLOP/s (235
+// for 5760, 185 for one expert: 1.05).  The matrix units' power sets the rate of whole tiles:
+// dealing the last tiles out evenly by their measured cost changed nothing.  4124 rows over 32
+// experts, 2048 -> 2048, 8-bit: 54 us, where the weights alone take 27: a first round of 256 tiles
+// at 4 TB/s and a second one that is bound by the latency of its stages.
 namespace xp {
 constexpr int BM = 256, BN = 256, NT = 512;
 constexpr int WTN = 64, MBLK = 4, NBLK = 2;

@@ -81,12 +81,18 @@ struct GemvArgs {
 // a group's scale is one value per lane: y += s * acc.
 //
 // A workgroup's waves (four, or KS where that is more) take KS parts of K times blocks of 16
-// channels.  x goes
-// through LDS in chunks of 4 pieces (512 channels) of every part, its pairs put in order
-// once per workgroup (rows 1040 bytes apart: 16 rows then read 16 bytes each without a bank
-// conflict); the weights come straight to registers, a chunk ahead (two ahead was even or
-// slower: it costs registers, and with them waves).  The parts
-// are joined through LDS in a fixed order.
+// channels.  x goes through LDS in chunks of 4 pieces (512 channels) of every part, its pairs
+// put in order once per workgroup (rows 1040 bytes apart: 16 rows then read 16 bytes each
+// without a bank conflict); the weights come straight to registers, a chunk ahead (two ahead
+// was even or slower: it costs registers, and with them waves).  The parts are joined through
+// LDS in a fixed order.
+//
+// Measured, with the launch: 4096 -> 12288, one row, groups of 64, 9.4 us (27 MB); 8192 -> 28672, one row,
+// groups of 128, 30.2 us = 4.0 TB/s; 8192 -> 28671, seven rows, groups of 32, 40.7 us = 3.3 TB/s: the
+// vector units are busy 40% of that time (22 instructions for every 512 codes, 17 with groups of
+// 128), and on average 2.1 waves of a possible 4 are there, as the last workgroups end.
+// Two blocks of channels a wave (x read from LDS once for both) was slower nearly everywhere
+// (8192 -> 28672 32.0 us): half the waves.
 constexpr int GV_SETS = 2;
 constexpr int GV_CHUNK = 4;                         // pieces
 constexpr int GV_ROW = GV_CHUNK * 256 + 16;         // bytes of a row of a chunk of x in LDS
