@@ -18,8 +18,8 @@
 // that up to 2048 elements a row needs one wave and no barrier; with few, one piece, for the
 // latency.
 //
-// Measured: 17776 x 1920 with the residual, to codes 50.4 us = 4.75 TB/s, to 16 bits 53.7 us = 5.1 TB/s; 4113 x
-// 4096 to 16 bits 29.1 us, 4113 x 4095 30.4 us; one row of 1920 3.3 us.  A large copy reaches 5.0-5.4 TB/s.
+// Measured: 17776 x 1920 with the residual, to codes 46.2 us = 5.2 TB/s, to 16 bits 47.4 us = 5.8 TB/s; 4113 x
+// 4096 to 16 bits 27.0 us (21.6 where buffers are used again), 4113 x 4095 29.0 us; one row of 1920 3.3 us.  A large copy reaches 5.0-5.4 TB/s.
 #include <algorithm>
 
 #include "dev_common.h"
@@ -71,18 +71,29 @@ __device__ __forceinline__ double wave_sum_dpp(double v) {
   return (lane_d(v, 0) + lane_d(v, 16)) + (lane_d(v, 32) + lane_d(v, 48));
 }
 
-// Eight elements at any element's address; TINY: the row has only cnt < 8.
-template <bool TINY>
+// Eight elements at any element's address; TINY: the row has only cnt < 8; NT: past the cache.
+//
+// What goes past the cache.  The sum, always: nobody reads it before the product has run (4113 x 4096
+// to 16 bits 23.3 -> 21.6 us with buffers in use again, 8000 x 5760 to codes 69.7 -> 66.0; even also
+// where the next call's residual is this one's sum).  x and the residual, read once, where the call's
+// operands do not fit the last-level cache beside others: 17776 x 1920 to codes 49.1 -> 46.0 us, with the
+// product that reads the codes, 1920 -> 5760, 254 -> 245; but what the layer before left in that cache
+// should be found there (4113 x 4096 21.6, past it 26.0), and outlier channels are read twice.  Never what
+// the product reads next: codes sent past it made 64 rows of 4096 with their product 19.6 -> 22.2 us.
+template <bool TINY, bool NT>
 __device__ __forceinline__ u4v load8(const uint16_t* p, int cnt) {
+  if constexpr (!TINY && NT) return __builtin_nontemporal_load(reinterpret_cast<const u4v_el*>(p));
   if constexpr (!TINY) return *reinterpret_cast<const u4v_el*>(p);
   u4v v = {0u, 0u, 0u, 0u};
   for (int i = 0; i < 8; ++i)
     if (i < cnt) v[i >> 1] |= (unsigned)p[i] << (16 * (i & 1));
   return v;
 }
-template <bool TINY>
+template <bool TINY, bool NT>
 __device__ __forceinline__ void store8(uint16_t* p, const u4v& v, int cnt) {
-  if constexpr (!TINY) {
+  if constexpr (!TINY && NT) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u4v_el*>(p));
+  } else if constexpr (!TINY) {
     *reinterpret_cast<u4v_el*>(p) = v;
   } else {
     for (int i = 0; i < 8; ++i)
@@ -94,8 +105,8 @@ __device__ __forceinline__ void store8(uint16_t* p, const u4v& v, int cnt) {
 // first elements counted by their own piece; or fewer than 8 elements in all.
 enum : int { END_WHOLE = 0, END_OVERLAP = 1, END_TINY = 2 };
 
-// QUANT: codes and scales instead of y.  T threads a row.
-template <int DT, bool RES, bool QUANT, bool DUAL, int END, int NP>
+// QUANT: codes and scales instead of y.  PAST: x and the residual past the cache.  T threads a row.
+template <int DT, bool RES, bool QUANT, bool DUAL, int END, int NP, bool PAST = false>
 __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
   static_assert(END == END_WHOLE || !QUANT, "codes are written 8 at a time");
   constexpr bool TINY = END == END_TINY;
@@ -214,8 +225,8 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
     u4v raw[NP], rad[RES ? NP : 1];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      raw[j] = load8<TINY>(xr + at(j), a.k);
-      if constexpr (RES) rad[j] = load8<TINY>(sr + at(j), a.k);
+      raw[j] = load8<TINY, PAST>(xr + at(j), a.k);
+      if constexpr (RES) rad[j] = load8<TINY, PAST>(sr + at(j), a.k);
     }
     // The outlier channels' h, gathered before anyone stores h (h may be x or r itself).
     float ov[2] = {0.0f, 0.0f};
@@ -271,7 +282,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
       uint16_t* hr = a.h + row * a.ldh;
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if (elem(j) < a.k) store8<TINY>(hr + at(j), raw[j], a.k);
+        if (elem(j) < a.k) store8<TINY, true>(hr + at(j), raw[j], a.k);
     }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -290,7 +301,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
             u4v o;
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = cvt_pair<DT>(v[j][2 * i], v[j][2 * i + 1]);
-            store8<TINY>(yr + at(j), o, a.k);
+            store8<TINY, false>(yr + at(j), o, a.k);
           }
       }
     } else {
@@ -369,7 +380,13 @@ static void launch_norm_np(const NormArgs& a, int np, int grid, int block, int T
   switch (np) {
     case 1: hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 1>), dim3(grid), dim3(block), 0, st, a, T); break;
     case 2: hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 2>), dim3(grid), dim3(block), 0, st, a, T); break;
-    default: hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 4>), dim3(grid), dim3(block), 0, st, a, T); break;
+    default:
+      // Above three quarters of the 256 MiB last-level cache: load8.
+      if (!DUAL && a.rows * a.k * (2 + 2 * RES + 2 * (a.h != nullptr) + (QUANT ? 1 : 2)) > ((int64_t)192 << 20))
+        hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 4, !DUAL>), dim3(grid), dim3(block), 0, st, a, T);
+      else
+        hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 4>), dim3(grid), dim3(block), 0, st, a, T);
+      break;
   }
 }
 
@@ -436,7 +453,8 @@ hipError_t launch_norm(const NormParams& p, hipStream_t st) {
   const int block = T <= 128 ? 256 : T;
   const int64_t need = (p.rows + block / T - 1) / (block / T);
   // Workgroups of 32 waves per compute unit in all, two times what fits at once: 17776 x 1920 with
-  // residual and codes 51.7 us (8: 55.5, 16: 52.4, 64: 50.2), without the residual 27.9 (30.1, 26.7, 29.6).
+  // residual and codes 46.0 us (8: 53.1, 16: 46.9, 64: 45.8), without the residual 28.4 (30.7, 27.2, 30.4),
+  // 8000 x 5760 61.7 (70.3, 71.7, 62.2).
   const int64_t most = (int64_t)persistent_blocks() * 32 / (block / 64);
   const int grid = (int)std::min(need, most);
   if (p.dtype == DT_BF16) launch_norm_dt<DT_BF16>(a, quant, np, grid, block, T, st);

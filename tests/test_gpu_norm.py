@@ -261,3 +261,33 @@ def test_codes_of_a_norm_equal_those_of_its_rows_when_exact(vq):
     y = vq.vq_rmsnorm(x, None, 0.0)
     c2, s2 = vq.vq_quant_act(y, 8, "token")
     assert torch.equal(c, c2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("m,k", [(17776, 1920), (6500, 4095), (3700, 9001)])
+@pytest.mark.parametrize("res", [False, True])
+def test_larger_than_the_cache(vq, m, k, res):
+    """Rows do not depend on one another: the whole call, the sum in place of the residual, gives
+    bit for bit what calls of few rows give (which the oracle pins above)."""
+    if not res:
+        m *= 2
+    g = torch.Generator(device=DEV).manual_seed(m + k)
+    x = torch.randn(m, k, device=DEV, generator=g).bfloat16()
+    r = torch.randn(m, k, device=DEV, generator=g).bfloat16() if res else None
+    w = torch.randn(k, device=DEV, generator=g).bfloat16()
+    h = r.clone() if res else None
+    got = vq.vq_rmsnorm(x, w, EPS, residual=h, sum_out=h)
+    y = got[0] if res else got
+    if k % 64 == 0:
+        h2 = r.clone() if res else None
+        codes, scales = vq.vq_rmsnorm_quant(x, w, 8, EPS, residual=h2, sum_out=h2)[:2]
+    for i in range(0, m, 900):
+        s = slice(i, min(m, i + 900))
+        part = vq.vq_rmsnorm(x[s], w, EPS, residual=r[s] if res else None)
+        if res:
+            assert torch.equal(h[s], part[1])
+        assert torch.equal(y[s], part[0] if res else part)
+        if k % 64 == 0:
+            part = vq.vq_rmsnorm_quant(x[s], w, 8, EPS, residual=r[s] if res else None)
+            assert torch.equal(codes[s], part[0]) and torch.equal(scales[s], part[1])
+            if res:
+                assert torch.equal(h2[s], part[2])
