@@ -342,3 +342,24 @@ def test_offsets_that_do_not_ascend(vq):
                             torch.from_numpy(sb).to(DEV), 8, i32(off), y=buf[10:t + 10])
         torch.cuda.synchronize()
         assert bool((buf[:10] == 7.0).all()) and bool((buf[t + 10:] == 7.0).all())
+
+
+@pytest.mark.parametrize("counts,n,k,bits,pad,shift,out", [
+    ([300, 0, 513], 255, 128, 8, 0, 0, "bf16"), ([300, 0, 513], 256, 128, 8, 0, 1, "fp16"),
+    ([300, 0, 513], 256, 64, 4, 1, 0, "bf16"), ([300, 65, 513], 257, 64, 8, 0, 1, "bf16"),
+    ([300, 33, 513], 263, 64, 8, 2, 0, "fp16"), ([300, 1, 513], 264, 64, 8, 3, 1, "bf16"),
+    ([700, 127, 1], 321, 192, 4, 0, 0, "bf16"), ([700, 128, 3], 327, 64, 8, 4, 1, "bf16"),
+    ([700, 129, 3], 335, 64, 8, 0, 0, "fp16"), ([700, 200, 3], 65, 64, 8, 0, 1, "bf16"),
+    ([4000, 3990, 4100, 3901], 2049, 64, 8, 0, 0, "bf16"), ([4000, 3990, 4100, 3901], 2048, 192, 4, 1, 1, "bf16"),
+    ([60] * 8, 8191, 192, 8, 0, 0, "bf16"),
+])
+def test_rows_that_start_at_odd_elements(vq, counts, n, k, bits, pad, shift, out):
+    """Every output is written, and nothing before, between or behind the rows."""
+    off = offsets_of(counts)
+    t = int(off[-1])
+    a, sa, b, sb = operands(t, len(counts), n, k, bits, 3)
+    buf = torch.full((t * (n + pad) + shift + 8,), 7.0, dtype=TD[out], device=DEV)
+    y = buf[shift:shift + t * (n + pad)].view(t, n + pad)
+    check_int(vq, a, sa, b, sb, n, off, None, t, bits, out, True, y=y[:, :n])
+    assert bool((y[:, n:] == 7.0).all()) and bool((buf[:shift] == 7.0).all())
+    assert bool((buf[shift + t * (n + pad):] == 7.0).all())
