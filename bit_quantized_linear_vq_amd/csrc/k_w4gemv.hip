@@ -4,6 +4,7 @@
 //
 //   s[j,g] = RNE16(fl32(max|w| / 7)),  c[j,k] = clamp(rne(fl32(w * fl32(1 / s))), -7, 7)
 //   y[i,j] = sum_g s[j,g] * sum_{k in g} c[j,k] x[i,k]      (float32)
+#include <algorithm>
 #include <type_traits>
 
 #include "dev_common.h"
@@ -80,7 +81,7 @@ struct GemvArgs {
 // A lane's accumulators hold one output channel (lane mod 16) and rows 4 (lane div 16) + i, so
 // a group's scale is one value per lane: y += s * acc.
 //
-// A workgroup's waves (four, or KS where that is more) take KS parts of K times blocks of 16
+// A workgroup's waves (four, eight, or KS where that is more) take KS parts of K times blocks of 16
 // channels.  x goes through LDS in chunks of 4 pieces (512 channels) of every part, its pairs
 // put in order once per workgroup (rows 1040 bytes apart: 16 rows then read 16 bytes each
 // without a bank conflict); the weights come straight to registers, a chunk ahead (two ahead
@@ -97,15 +98,13 @@ constexpr int GV_SETS = 2;
 constexpr int GV_CHUNK = 4;                         // pieces
 constexpr int GV_ROW = GV_CHUNK * 256 + 16;         // bytes of a row of a chunk of x in LDS
 constexpr int GV_ROWS = 32;                         // rows times parts at most
-constexpr int gv_waves(int ks) { return ks < 4 ? 4 : ks; }
 
-template <int DT, int GROUP, int KS, int MB, int XL>
-__global__ __launch_bounds__(64 * gv_waves(KS)) __attribute__((amdgpu_waves_per_eu(KS == 16 ? 4 : 3))) void k_w4gemv(GemvArgs g) {
+template <int DT, int GROUP, int KS, int MB, int XL, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(KS == 16 ? 4 : 3))) void k_w4gemv(GemvArgs g) {
   typedef typename std::conditional<DT == DT_BF16, __bf16, _Float16>::type in_t;
   typedef in_t in8 __attribute__((ext_vector_type(8)));
   constexpr int GPP = 128 / GROUP;     // groups of a piece
   constexpr int GPC = GPP * GV_CHUNK;  // and of a chunk
-  constexpr int WAVES = gv_waves(KS);
   extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];  // [2][part][row][GV_ROW]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rl = lane & 15, kq = lane >> 4;
@@ -289,20 +288,26 @@ __global__ __launch_bounds__(64 * gv_waves(KS)) __attribute__((amdgpu_waves_per_
     }
 }
 
-template <int DT, int GROUP, int KS, int MB>
-static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
-  constexpr int WAVES = gv_waves(KS), COLS = 16 * WAVES / KS;
-  const int rows = a.m < 16 * MB ? a.m : 16 * MB;
-  size_t shm = (size_t)2 * KS * rows * GV_ROW;
-  if (shm < (size_t)WAVES * MB * 64 * 16) shm = (size_t)WAVES * MB * 64 * 16;  // the parts' joining
+constexpr size_t GV_LDS = 160 * 1024;  // of a compute unit
+static size_t gv_shared(int ks, int mb, int rows, int waves) {
+  return std::max((size_t)2 * ks * rows * GV_ROW, (size_t)waves * mb * 64 * 16);  // x, or the parts' joining
+}
+
+template <int DT, int GROUP, int KS, int MB, int WAVES>
+static void launch_gemv_waves(const GemvArgs& a, hipStream_t st) {
+  constexpr int COLS = 16 * WAVES / KS;
+  const int rows = std::min(a.m, 16 * MB);
+  const size_t shm = gv_shared(KS, MB, rows, WAVES);
   const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)((a.m + 16 * MB - 1) / (16 * MB)));
   const int loads = (rows * KS + WAVES - 1) / WAVES;  // of x, per thread and chunk
-#define VQ_GEMV_XL(X) hipLaunchKernelGGL((k_w4gemv<DT, GROUP, KS, MB, X>), grid, dim3(64 * WAVES), shm, st, a)
+#define VQ_GEMV_XL(X) hipLaunchKernelGGL((k_w4gemv<DT, GROUP, KS, MB, X, WAVES>), grid, dim3(64 * WAVES), shm, st, a)
   if constexpr (MB == 2) {
     VQ_GEMV_XL(8);
   } else if constexpr (KS == 16) {
     if (loads <= 1) VQ_GEMV_XL(1);
     else VQ_GEMV_XL(2);
+  } else if constexpr (WAVES == 8 && KS < 8) {
+    VQ_GEMV_XL(4);
   } else {
     if (loads <= 1) VQ_GEMV_XL(1);
     else if (loads <= 2) VQ_GEMV_XL(2);
@@ -311,6 +316,23 @@ static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
     else VQ_GEMV_XL(8);
   }
 #undef VQ_GEMV_XL
+}
+
+template <int DT, int GROUP, int KS>
+static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
+  if constexpr (KS > 4) {
+    launch_gemv_waves<DT, GROUP, KS, 1, KS>(a, st);
+  } else {
+    // Many rows of x leave LDS (above 16 rows and parts also registers) for fewer than the four
+    // workgroups of four waves that a compute unit can hold: eight waves then share the same x,
+    // unless all workgroups fit at once.  8192 -> n, groups of 128, 4 / 8 waves, us: 16 rows, n =
+    // 16384 23.1 / 25.2, 20480 40.5 / 34.3, 28672 49.9 / 37.0; 8 rows, n = 8192 13.7 / 14.4, 12288
+    // 22.5 / 19.2; groups of 32, 9 rows, 28672 49.2 / 38.6, 7 rows 40.5 / 38.8 but 24576 33.2 / 37.6.
+    const int fit = std::min((int)(GV_LDS / gv_shared(KS, 1, a.m, 4)), a.m * KS > 16 ? 3 : 4);
+    const int64_t groups = ((int64_t)a.n * KS + 63) / 64;
+    if (fit < 4 && groups > (int64_t)fit * vq_internal::persistent_blocks()) launch_gemv_waves<DT, GROUP, KS, 1, 8>(a, st);
+    else launch_gemv_waves<DT, GROUP, KS, 1, 4>(a, st);
+  }
 }
 
 template <int DT, int GROUP>
@@ -322,11 +344,11 @@ static void launch_gemv_group(const GemvArgs& a, hipStream_t st) {
   int ks = 2;
   while (ks < 16 && (int64_t)ks * ((a.n + 15) / 16) < 1600) ks *= 2;
   while (a.m * ks > GV_ROWS) ks /= 2;
-  if (a.m > 16) launch_gemv_part<DT, GROUP, 1, 2>(a, st);
-  else if (ks == 16) launch_gemv_part<DT, GROUP, 16, 1>(a, st);
-  else if (ks == 8) launch_gemv_part<DT, GROUP, 8, 1>(a, st);
-  else if (ks == 4) launch_gemv_part<DT, GROUP, 4, 1>(a, st);
-  else launch_gemv_part<DT, GROUP, 2, 1>(a, st);
+  if (a.m > 16) launch_gemv_waves<DT, GROUP, 1, 2, 4>(a, st);
+  else if (ks == 16) launch_gemv_part<DT, GROUP, 16>(a, st);
+  else if (ks == 8) launch_gemv_part<DT, GROUP, 8>(a, st);
+  else if (ks == 4) launch_gemv_part<DT, GROUP, 4>(a, st);
+  else launch_gemv_part<DT, GROUP, 2>(a, st);
 }
 
 template <int DT>

@@ -184,3 +184,12 @@ def test_products_of_small_values(vq, m, n, k, group):
     assert np.array_equal(npb(scales).view(np.uint16), np.asarray(s).view(np.uint16))
     ex, b = group4.exact(gen.as_numpy_bits(x), "fp16", packed, s, group)
     within(y, ex, b, "fp32")
+
+
+@pytest.mark.parametrize("m,n,k,group,dt,out", [
+    (16, 16500, 1056, 32, "bf16", "bf16"), (12, 25001, 640, 128, "fp16", "fp32"), (9, 24600, 320, 64, "bf16", "fp16"),
+    (16, 16385, 32, 32, "fp16", "bf16"), (8, 8209, 1056, 32, "bf16", "fp32"), (7, 12300, 1280, 128, "fp16", "fp16"),
+    (5, 12500, 2112, 64, "bf16", "bf16"), (8, 8192, 640, 128, "bf16", "bf16"),
+])
+def test_many_channels_with_many_rows(vq, m, n, k, group, dt, out):
+    test_product_within_the_float32_bound(vq, m, n, k, group, dt, out)
