@@ -97,7 +97,7 @@ struct GemvArgs {
 constexpr int GV_SETS = 2;
 constexpr int GV_CHUNK = 4;                         // pieces
 constexpr int GV_ROW = GV_CHUNK * 256 + 16;         // bytes of a row of a chunk of x in LDS
-constexpr int GV_ROWS = 32;                         // rows times parts at most
+constexpr int GV_ROWS = 32;                         // rows times parts at most, up to 16 rows
 
 template <int DT, int GROUP, int KS, int MB, int XL, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(KS == 16 ? 4 : 3))) void k_w4gemv(GemvArgs g) {
@@ -344,8 +344,15 @@ static void launch_gemv_group(const GemvArgs& a, hipStream_t st) {
   int ks = 2;
   while (ks < 16 && (int64_t)ks * ((a.n + 15) / 16) < 1600) ks *= 2;
   while (a.m * ks > GV_ROWS) ks /= 2;
-  if (a.m > 16) launch_gemv_waves<DT, GROUP, 1, 2, 4>(a, st);
-  else if (ks == 16) launch_gemv_part<DT, GROUP, 16>(a, st);
+  if (a.m > 16) {
+    // 32 rows a workgroup: two parts of K and eight waves, where all workgroups fit at once.
+    // 32 rows, us against one part and four waves: 8192 -> 8192 31.7 / 42.1, 16384 -> 2048 56.8 / 77.9,
+    // 64 rows 32.4 / 43.1; 24 rows, 8192 -> 28672 64.8 / 52.8.
+    const int64_t groups = (((int64_t)a.n + 63) / 64) * ((a.m + 31) / 32);
+    const int64_t fit = (int64_t)(GV_LDS / gv_shared(2, 2, std::min(a.m, 32), 8));
+    if (groups <= fit * vq_internal::persistent_blocks()) launch_gemv_waves<DT, GROUP, 2, 2, 8>(a, st);
+    else launch_gemv_waves<DT, GROUP, 1, 2, 4>(a, st);
+  } else if (ks == 16) launch_gemv_part<DT, GROUP, 16>(a, st);
   else if (ks == 8) launch_gemv_part<DT, GROUP, 8>(a, st);
   else if (ks == 4) launch_gemv_part<DT, GROUP, 4>(a, st);
   else launch_gemv_part<DT, GROUP, 2>(a, st);

@@ -193,3 +193,11 @@ def test_products_of_small_values(vq, m, n, k, group):
 ])
 def test_many_channels_with_many_rows(vq, m, n, k, group, dt, out):
     test_product_within_the_float32_bound(vq, m, n, k, group, dt, out)
+
+
+@pytest.mark.parametrize("m,n,k,group,dt,out", [
+    (17, 100, 1056, 32, "bf16", "bf16"), (32, 65, 32, 32, "fp16", "fp32"), (33, 1000, 640, 128, "bf16", "fp16"),
+    (24, 17000, 1088, 64, "bf16", "bf16"), (31, 129, 8320, 64, "fp16", "bf16"), (65, 40, 2080, 32, "bf16", "fp32"),
+])
+def test_more_rows_than_a_tile(vq, m, n, k, group, dt, out):
+    test_product_within_the_float32_bound(vq, m, n, k, group, dt, out)
