@@ -58,6 +58,7 @@ struct GemvArgs {
   void* y;
   int64_t ldx, ldy;
   int m, n, k, group, out_dt;
+  int tile;  // rows of x per workgroup, 16 MB at most
 };
 
 // ---------------------------------------------------------------------------------------
@@ -97,7 +98,7 @@ struct GemvArgs {
 constexpr int GV_SETS = 2;
 constexpr int GV_CHUNK = 4;                         // pieces
 constexpr int GV_ROW = GV_CHUNK * 256 + 16;         // bytes of a row of a chunk of x in LDS
-constexpr int GV_ROWS = 32;                         // rows times parts at most, up to 16 rows
+constexpr int GV_ROWS = 32;                         // rows times parts at most
 
 template <int DT, int GROUP, int KS, int MB, int XL, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(KS == 16 ? 4 : 3))) void k_w4gemv(GemvArgs g) {
@@ -109,8 +110,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(KS =
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rl = lane & 15, kq = lane >> 4;
   const int kw = wave % KS, nw = wave / KS;
-  const int n0 = ((int)blockIdx.x * (WAVES / KS) + nw) * 16, m0 = blockIdx.y * (16 * MB);
-  const int rows = min(16 * MB, g.m - m0);
+  const int n0 = ((int)blockIdx.x * (WAVES / KS) + nw) * 16, m0 = blockIdx.y * g.tile;
+  const int rows = min(g.tile, g.m - m0);
   const int pieces = (g.k + 127) / 128;
   const int p0 = pieces * kw / KS, p1 = pieces * (kw + 1) / KS;
   const int chunks = ((pieces + KS - 1) / KS + GV_CHUNK - 1) / GV_CHUNK;  // of the longest part
@@ -281,7 +282,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(KS =
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int m = m0 + 16 * i + 4 * kq + r;
-      if (m >= g.m) continue;
+      if (m >= m0 + rows) continue;
       const int64_t o = m * g.ldy + n;
       if (g.out_dt == DT_F32) reinterpret_cast<float*>(g.y)[o] = y[i][r];
       else reinterpret_cast<uint16_t*>(g.y)[o] = (uint16_t)((g.out_dt == DT_BF16 ? cvt_pair<DT_BF16>(y[i][r], 0.0f) : cvt_pair<DT_F16>(y[i][r], 0.0f)) & 0xFFFFu);
@@ -296,9 +297,9 @@ static size_t gv_shared(int ks, int mb, int rows, int waves) {
 template <int DT, int GROUP, int KS, int MB, int WAVES>
 static void launch_gemv_waves(const GemvArgs& a, hipStream_t st) {
   constexpr int COLS = 16 * WAVES / KS;
-  const int rows = std::min(a.m, 16 * MB);
+  const int rows = a.tile;
   const size_t shm = gv_shared(KS, MB, rows, WAVES);
-  const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)((a.m + 16 * MB - 1) / (16 * MB)));
+  const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)((a.m + rows - 1) / rows));
   const int loads = (rows * KS + WAVES - 1) / WAVES;  // of x, per thread and chunk
 #define VQ_GEMV_XL(X) hipLaunchKernelGGL((k_w4gemv<DT, GROUP, KS, MB, X, WAVES>), grid, dim3(64 * WAVES), shm, st, a)
   if constexpr (MB == 2) {
@@ -328,31 +329,45 @@ static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
     // unless all workgroups fit at once.  8192 -> n, groups of 128, 4 / 8 waves, us: 16 rows, n =
     // 16384 23.1 / 25.2, 20480 40.5 / 34.3, 28672 49.9 / 37.0; 8 rows, n = 8192 13.7 / 14.4, 12288
     // 22.5 / 19.2; groups of 32, 9 rows, 28672 49.2 / 38.6, 7 rows 40.5 / 38.8 but 24576 33.2 / 37.6.
-    const int fit = std::min((int)(GV_LDS / gv_shared(KS, 1, a.m, 4)), a.m * KS > 16 ? 3 : 4);
-    const int64_t groups = ((int64_t)a.n * KS + 63) / 64;
+    const int fit = std::min((int)(GV_LDS / gv_shared(KS, 1, a.tile, 4)), a.tile * KS > 16 ? 3 : 4);
+    const int64_t groups = ((int64_t)a.n * KS + 63) / 64 * ((a.m + a.tile - 1) / a.tile);
     if (fit < 4 && groups > (int64_t)fit * vq_internal::persistent_blocks()) launch_gemv_waves<DT, GROUP, KS, 1, 8>(a, st);
     else launch_gemv_waves<DT, GROUP, KS, 1, 4>(a, st);
   }
 }
 
 template <int DT, int GROUP>
-static void launch_gemv_group(const GemvArgs& a, hipStream_t st) {
+static void launch_gemv_group(GemvArgs a, hipStream_t st) {
   // Parts of K: waves enough for the whole card, at least two.  One row, us with 2 / 4 / 8 / 16
   // parts: 16384 -> 2048 28.3 / 16.0 / 12.2 / 10.8; 8192 -> 8192 16.0 / 11.2 / 11.6 / 16.2; 4096 ->
   // 14336 9.6 / 10.2 / 11.5 / 20.8; 8192 -> 28672 30.3 / 30.2 / 33.4 / 48.4; seven rows, groups of
   // 32, 8192 -> 28671 40.8 / 53.7.  Many rows of x leave room in LDS for fewer parts.
+  const int64_t blocks = ((int64_t)a.n + 15) / 16;
   int ks = 2;
-  while (ks < 16 && (int64_t)ks * ((a.n + 15) / 16) < 1600) ks *= 2;
-  while (a.m * ks > GV_ROWS) ks /= 2;
-  if (a.m > 16) {
-    // 32 rows a workgroup: two parts of K and eight waves, where all workgroups fit at once.
-    // 32 rows, us against one part and four waves: 8192 -> 8192 31.7 / 42.1, 16384 -> 2048 56.8 / 77.9,
-    // 64 rows 32.4 / 43.1; 24 rows, 8192 -> 28672 64.8 / 52.8.
-    const int64_t groups = (((int64_t)a.n + 63) / 64) * ((a.m + 31) / 32);
-    const int64_t fit = (int64_t)(GV_LDS / gv_shared(2, 2, std::min(a.m, 32), 8));
-    if (groups <= fit * vq_internal::persistent_blocks()) launch_gemv_waves<DT, GROUP, 2, 2, 8>(a, st);
-    else launch_gemv_waves<DT, GROUP, 1, 2, 4>(a, st);
-  } else if (ks == 16) launch_gemv_part<DT, GROUP, 16>(a, st);
+  while (ks < 16 && ks * blocks < 1600) ks *= 2;
+  a.tile = a.m;
+  if (a.m > 4) {
+    // Fewer rows a workgroup leave room for more parts, as long as all waves are there at once
+    // (16 a compute unit; the weights' further readings come from the caches).  Us with tiles of 32 / 16 /
+    // 8 / 4 rows and 1 / 2 / 4 / 8 parts: 32 rows, 16384 -> 2048 77.9 / 36.8 / 22.3 / 32.6, 8192 -> 8192
+    // 42.0 / 25.4 / 40.5 / 76.3, 8192 -> 28672 52.1 / 64.4 / 117; 16 rows, 8192 -> 512 - / 17.2 / 9.9 / 7.5,
+    // 4096 - / 19.8 / 13.9 / 21.2, 4096 -> 12288 - / 13.0 / 16.4 / 33.1.
+    for (int tile = 4; tile <= 16; tile *= 2) {
+      const int parts = GV_ROWS / tile;
+      const int64_t tiles = (a.m + tile - 1) / tile;
+      if (parts > ks || parts * blocks * tiles > 16 * (int64_t)vq_internal::persistent_blocks()) continue;
+      ks = parts;
+      a.tile = (int)((a.m + tiles - 1) / tiles);
+      break;
+    }
+  }
+  if (a.tile > 16) {
+    a.tile = std::min(a.m, 32);
+    launch_gemv_waves<DT, GROUP, 1, 2, 4>(a, st);
+    return;
+  }
+  while (a.tile * ks > GV_ROWS) ks /= 2;
+  if (ks == 16) launch_gemv_part<DT, GROUP, 16>(a, st);
   else if (ks == 8) launch_gemv_part<DT, GROUP, 8>(a, st);
   else if (ks == 4) launch_gemv_part<DT, GROUP, 4>(a, st);
   else launch_gemv_part<DT, GROUP, 2>(a, st);

@@ -425,8 +425,8 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  *   scales     device [n x k/group] of dt
  *   x          device dt [m x k], stride ldx (16-byte aligned, ldx % 8 == 0)
  *   y          device out_dt in {F16, BF16, F32}, [m x n], stride ldy
- * m is any number of rows (0 enqueues nothing), but the weights are read once for every
- * 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x reach
+ * m is any number of rows (0 enqueues nothing), but the weights are read again for every
+ * 4 to 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x reach
  * the outputs of their row as NaN.  One kernel; nothing is allocated.
  * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group, m > 2^20, n > 2^24).
  */

@@ -201,3 +201,12 @@ def test_many_channels_with_many_rows(vq, m, n, k, group, dt, out):
 ])
 def test_more_rows_than_a_tile(vq, m, n, k, group, dt, out):
     test_product_within_the_float32_bound(vq, m, n, k, group, dt, out)
+
+
+@pytest.mark.parametrize("m,n,k,group,dt,out", [
+    (5, 50, 2080, 32, "bf16", "bf16"), (6, 333, 1088, 64, "fp16", "fp32"), (11, 40, 4224, 128, "bf16", "fp16"),
+    (16, 515, 2112, 64, "bf16", "bf16"), (13, 3001, 352, 32, "fp16", "bf16"), (21, 1999, 480, 32, "bf16", "fp32"),
+    (32, 4100, 320, 64, "bf16", "bf16"), (67, 30, 8192, 128, "fp16", "fp16"), (130, 100, 96, 32, "bf16", "bf16"),
+])
+def test_rows_in_smaller_tiles(vq, m, n, k, group, dt, out):
+    test_product_within_the_float32_bound(vq, m, n, k, group, dt, out)
