@@ -65,12 +65,10 @@ struct GemvArgs {
 // The product on the 16 x 16 x 32 matrix instruction: 16 rows of x against 16 output
 // channels, so that up to 16 rows cost what one does.
 //
-// Codes to 16-bit floats: with u = c + 8 (one exclusive or for eight codes) the nibble goes
-// into the top four mantissa bits of 16.0, which makes the operand 16 + u = c + 24 exactly,
-// two of them per shift and and-or.  The excess 24 sum x comes off first: a group's
-// accumulators start from the product of x with a constant -24, which is one more matrix
-// instruction per fragment of x, not per fragment of weights, and lands in the layout that
-// the accumulators have.
+// Codes become exact 16-bit floats before they meet x (see widen).  Leaving them at c + 24, which
+// costs one and-or for two, and taking 24 sum x off the accumulators was faster with
+// bfloat16 rows (below), but rounded a loud channel of x at 24 to 31 times its size even where its
+// code is 0 (error 0.1% of the outputs at 1e5 among unit values) and lost finite rows above 1e37.
 //
 // Layout: a lane loads 16 bytes of a weight row, 32 codes, the 64 lanes 64 bytes of 16
 // rows.  A matrix instruction wants 32 consecutive channels spread over the lanes' four
@@ -89,10 +87,10 @@ struct GemvArgs {
 // was even or slower: it costs registers, and with them waves).  The parts are joined through
 // LDS in a fixed order.
 //
-// Measured, with the launch: 4096 -> 12288, one row, groups of 64, 9.4 us (27 MB); 8192 -> 28672, one row,
-// groups of 128, 30.2 us = 4.0 TB/s; 8192 -> 28671, seven rows, groups of 32, 40.7 us = 3.3 TB/s: the
-// vector units are busy 40% of that time (22 instructions for every 512 codes, 17 with groups of
-// 128), and on average 2.1 waves of a possible 4 are there, as the last workgroups end.
+// Measured, with the launch, bfloat16 / fp16 rows (in brackets with codes left at c + 24): 4096 -> 12288,
+// one row, groups of 64, 10.4 / 9.6 us (9.5 / 9.6); 8192 -> 28672, one row, groups of 128, 34.4 / 31.1 us = 3.5
+// / 3.9 TB/s (30.0 / 29.9); 8192 -> 28671, seven rows, groups of 32, 42.9 / 41.1 us = 3.1 / 3.2 TB/s (40.3 /
+// 40.4); 32 rows, groups of 128, 8192 -> 8192 24.2 / 22.2 us (22.1 / 22.3), 8192 -> 28672 53.0 / 49.9 (51.9 / 51.3).
 // Two blocks of channels a wave (x read from LDS once for both) was slower nearly everywhere
 // (8192 -> 28672 32.0 us): half the waves.
 constexpr int GV_SETS = 2;
@@ -178,21 +176,45 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(KS =
     else
       return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(in8, a), __builtin_bit_cast(in8, b), c, 0, 0, 0);
   };
-  // Eight codes of a dword as c + 24, pairs (t, t + 4).  The constants are kept in registers:
-  // and-or takes one literal at most.
-  unsigned mask = DT == DT_BF16 ? 0x00780078u : 0x03C003C0u, sixteen = DT == DT_BF16 ? 0x41804180u : 0x4C004C00u;
-  asm("" : "+v"(mask), "+v"(sixteen));
+  // Eight codes of a dword as exact 16-bit floats, pairs (t, t + 4); u = c + 8 is one exclusive or for
+  // all.  fp16: u in the top four mantissa bits of 16.0, two of them per shift and and-or, then 24 off both
+  // in one packed subtraction.  bfloat16 has no packed arithmetic: u stays where it lies in the dword, as the
+  // mantissa bits of a float32 whose last of them counts one (2^23 for bits 0-3, 2^19 for bits 4-7, ...), one
+  // and-or and one exact subtraction, and the upper halves of two such floats make a pair.  The
+  // constants are kept in registers: and-or takes no literals.
+  unsigned mask[4], one[4];
+  if constexpr (DT == DT_BF16) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      mask[t] = 0xFu << (4 * t);
+      one[t] = (unsigned)(127 + 23 - 4 * t) << 23;
+      asm("" : "+v"(mask[t]), "+s"(one[t]));
+    }
+  } else {
+    mask[0] = 0x03C003C0u;
+    one[0] = 0x4C004C00u;
+    asm("" : "+v"(mask[0]), "+s"(one[0]));
+  }
   auto widen = [&](unsigned c) {
     const unsigned u = c ^ 0x88888888u;
-    if constexpr (DT == DT_BF16)
-      return v4i{(int)(((u << 3) & mask) | sixteen), (int)(((u >> 1) & mask) | sixteen),
-                 (int)(((u >> 5) & mask) | sixteen), (int)(((u >> 9) & mask) | sixteen)};
-    else
-      return v4i{(int)(((u << 6) & mask) | sixteen), (int)(((u << 2) & mask) | sixteen),
-                 (int)(((u >> 2) & mask) | sixteen), (int)(((u >> 6) & mask) | sixteen)};
+    v4i o;
+    if constexpr (DT == DT_BF16) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float excess = (float)(1 << (23 - 4 * t)) + 8.0f;
+        const float lo = bits_f((u & mask[t]) | one[t]) - excess;
+        const float hi = bits_f(((u >> 16) & mask[t]) | one[t]) - excess;
+        o[t] = (int)__builtin_amdgcn_perm(f_bits(hi), f_bits(lo), 0x07060302u);
+      }
+    } else {
+      typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+      const unsigned at[4] = {u << 6, u << 2, u >> 2, u >> 6};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        o[t] = __builtin_bit_cast(int, __builtin_bit_cast(h2, (at[t] & mask[0]) | one[0]) - h2{(_Float16)24.0f, (_Float16)24.0f});
+    }
+    return o;
   };
-  constexpr int M24 = DT == DT_BF16 ? (int)0xC1C0C1C0u : (int)0xCE00CE00u;
-  const v4i minus24 = {M24, M24, M24, M24};
 
   v4f y[MB];
 #pragma unroll
@@ -222,10 +244,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(KS =
         for (int i = 0; i < MB; ++i) {
           acc[i] = v4f{};
 #pragma unroll
-          for (int j = 0; j < GROUP / 32; ++j) {
-            xf[j][i] = *reinterpret_cast<const v4i*>(xb[i] + 256 * u + 64 * (j0 + j));
-            acc[i] = mma(xf[j][i], minus24, acc[i]);
-          }
+          for (int j = 0; j < GROUP / 32; ++j) xf[j][i] = *reinterpret_cast<const v4i*>(xb[i] + 256 * u + 64 * (j0 + j));
         }
         float s0, s1;
         const int si = u * GPP + j0 / (GROUP / 32);

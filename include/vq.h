@@ -413,11 +413,10 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  *   c[j,k] = clamp(rne(fl32(w * r)), -7, 7); a group with s = 0 (or 1 / s infinite) has
  *            zero codes
  *   y[i,j] = RNE_out(sum_g s[j,g] * sum_{k in g} c[j,k] x[i,k]), products exact, sums in
- *            float32 (in an order fixed by the sizes).  The inner sums run over
- *            (c + 24) x from -24 sum x, so that with G = group
- *            |y - exact| <= (2 G + k / G + 18) 2^-24 * sum_k 56 |s x_k| before the output
- *            rounding: a group's 2 G terms pass through sums of magnitudes of at most
- *            24 sum|x| + 31 sum|x|, and the k / G groups and 16 parts are added
+ *            float32 (in an order fixed by the sizes): with G = group
+ *            |y - exact| <= (2 G + k / G + 18) 2^-24 * sum_k |s c x_k| before the output
+ *            rounding: G additions in a group, counted at 2^-23 each, k / G groups and up
+ *            to 16 parts.  A group's sum of |c x| has to stay inside float32
  *   group      32, 64 or 128; k % group == 0
  *   w          device, dt in {F16, BF16}, [n x k], stride ldw (16-byte aligned, ldw % 8 == 0)
  *   codes      device uint8 [n x k/2], 16-byte aligned: two codes per byte, low nibble =
@@ -426,8 +425,9 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  *   x          device dt [m x k], stride ldx (16-byte aligned, ldx % 8 == 0)
  *   y          device out_dt in {F16, BF16, F32}, [m x n], stride ldy
  * m is any number of rows (0 enqueues nothing), but the weights are read again for every
- * 4 to 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x reach
- * the outputs of their row as NaN.  One kernel; nothing is allocated.
+ * 4 to 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x stay
+ * in their row, where an infinity meets a code as in the formula (a zero code gives NaN).
+ * One kernel; nothing is allocated.
  * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group, m > 2^20, n > 2^24).
  */
 vq_status vq_pack_weights_group(const void* w, vq_dtype dt, int64_t n, int64_t k, int64_t ldw, int group,

@@ -4,11 +4,11 @@
   s = RNE16(fl32(max|w| / 7)) over a group;  r = fl32(1 / s);  c = clamp(rne(fl32(w * r)), -7, 7)
   y = sum_g s_g * sum_{k in g} c_k x_k
 
-The reference product is the exact sum in float64.  The device sums (c + 24) x in float32
-and starts each group from -24 sum x, so a group's error is at most (terms) * 2^-24 times
-the largest sum of magnitudes it passes through, 24 sum|x| + sum|(c + 24) x| <= 56 sum|x|;
-then the groups are scaled and added in float32 (at most K / 32 + 16 additions with the
-joining of the partial sums).
+The reference product is the exact sum in float64.  The device adds the exact products c x in
+float32 and scales a group's sum into the row's: at most G additions in a group, counted at a
+whole step (2^-23) each since the rounding inside a matrix instruction is not specified, then
+K / G scaled additions and up to 16 of the parts of K at half a step, two more for the second order:
+|error| <= (2 G + K / G + 18) 2^-24 sum_k |s c x|, above the float32 underflow.
 """
 from __future__ import annotations
 
@@ -44,8 +44,6 @@ def unpack(packed):
 def exact(x_store, dtype: str, packed, s_store, group: int):
     """(y float64, bound float64): the exact product and the largest error of the device's sums."""
     x = to_f32(x_store, dtype).astype(np.float64)
-    s = np.repeat(to_f32(s_store, dtype).astype(np.float64), group, axis=1)
-    y = x @ (unpack(packed) * s).T
+    w = unpack(packed) * np.repeat(to_f32(s_store, dtype).astype(np.float64), group, axis=1)
     k = x.shape[1]
-    terms = 2 * group + k // group + 18
-    return y, terms * 2.0 ** -24 * 56.0 * (np.abs(x) @ np.abs(s).T)
+    return x @ w.T, (2 * group + k // group + 18) * 2.0 ** -24 * (np.abs(x) @ np.abs(w).T)
