@@ -330,6 +330,13 @@ def vq_qgemm_dequant(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: tor
     return (y, acc) if acc_debug else y
 
 
+def _width(b_bits, kblock):
+    """The width in b_bits, which may carry the piece flag where b is in K pieces."""
+    if b_bits & VQ_W_KBLOCK and not kblock:
+        raise ValueError("b_bits says that b is in K pieces: b must be 3-D")
+    return b_bits & ~VQ_W_KBLOCK
+
+
 def _check_gemm_operands(a, sa, b, sb, b_bits, kp, k0, sa_per_token=True):
     """The GEMM's codes and scales as the kernels read them: A int8 [M x kp] dense; B int8
     [N x kp] (8-bit weights) or uint8 [N x kp/2] (4-bit), or those codes in 64-byte K
@@ -344,6 +351,7 @@ def _check_gemm_operands(a, sa, b, sb, b_bits, kp, k0, sa_per_token=True):
         raise TypeError("b must be a 2-D (row-major) or 3-D (K pieces) CUDA (HIP) tensor of packed weight codes")
     kblock = b.dim() == 3
     n = b.shape[1] if kblock else b.shape[0]
+    b_bits = _width(b_bits, kblock)
     if b_bits in (4, 8):
         row_bytes = kp if b_bits == 8 else kp // 2
         dts = (torch.int8,) if b_bits == 8 else _U8
@@ -866,6 +874,7 @@ def vq_qgemm_experts(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: tor
     n = total // experts
     if total % experts or not n:
         raise ValueError(f"b must hold the same number of rows for each of the {experts} experts")
+    b_bits = _width(b_bits, kblock)
     if b_bits in (4, 8):
         row_bytes = kp if b_bits == 8 else kp // 2
         _dense(b, "b", index, (torch.int8,) if b_bits == 8 else _U8, 0)

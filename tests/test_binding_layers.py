@@ -1,0 +1,82 @@
+"""The binding's checks of device tensors, without a GPU: tensors that have a device, a shape and
+no memory (torch's fake tensors) reach every check, and a call that passes them all would
+reach the launch, which here only takes note."""
+import os
+
+import pytest
+import torch
+from torch._subclasses import FakeTensorMode
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "bit_quantized_linear_vq_amd", "libvq.so")
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libvq.so not built")
+
+
+@pytest.fixture
+def vq(monkeypatch):
+    import bit_quantized_linear_vq_amd as m
+    real = m._lib
+
+    class Lib:
+        launched = []
+
+        def __getattr__(self, name):
+            if name not in m._LAUNCHES:
+                return getattr(real, name)
+            return lambda *a: self.launched.append(name) or 0
+
+    lib = Lib()
+    lib.launched = []
+    monkeypatch.setattr(m, "_lib", lib)
+    monkeypatch.setattr(m, "_getdev", lambda: 0)
+    monkeypatch.setattr(m, "_rawstream", lambda i: 0)
+    monkeypatch.setattr(m, "_stream", lambda t: 0)
+    with FakeTensorMode():
+        yield m
+
+
+def launched(vq):
+    return list(vq._lib.launched)
+
+
+def dev(*shape, dt=torch.float32):
+    return torch.empty(shape, dtype=dt, device="cuda")
+
+
+def experts(vq, bits=8, m=6, e=2, n=32, k=128, **kw):
+    rb = k if bits & 15 == 8 else k // 2
+    wt = torch.int8 if bits & 15 == 8 else torch.uint8
+    a = dict(a=dev(m, k, dt=torch.int8), sa=dev(m), b=dev(e * n, rb, dt=wt), sb=dev(e * n), b_bits=bits,
+             offsets=dev(e + 1, dt=torch.int32), y=dev(m, n, dt=torch.bfloat16))
+    a.update(kw)
+    return vq.vq_qgemm_experts(**a)
+
+
+@pytest.mark.filterwarnings("ignore")
+def test_a_call_that_is_right_reaches_the_launch(vq):
+    experts(vq)
+    experts(vq, 4)
+    experts(vq, b=dev(2, 64, 64, dt=torch.int8))
+    experts(vq, 8 | vq.VQ_W_KBLOCK, b=dev(2, 64, 64, dt=torch.int8))
+    assert launched(vq) == ["vq_qgemm_experts"] * 4
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_the_piece_flag_in_the_width_passes_no_check_by(vq, bits):
+    """With it the library would read row-major codes, or codes of another shape, as pieces."""
+    flag, wt = bits | vq.VQ_W_KBLOCK, torch.int8 if bits == 8 else torch.uint8
+    with pytest.raises(ValueError):
+        experts(vq, flag)
+    with pytest.raises(ValueError):
+        experts(vq, flag, b=dev(1, 64, 64 if bits == 8 else 32, dt=wt))
+    with pytest.raises(TypeError):
+        experts(vq, flag, b=torch.empty(2, 64, 64, dtype=wt))
+    a, sa, sb = dev(6, 128, dt=torch.int8), dev(6), dev(32)
+    with pytest.raises(ValueError):
+        vq.vq_qgemm_dequant(a, sa, dev(32, 16, dt=wt), sb, flag, y=dev(6, 32, dt=torch.bfloat16), ws=False)
+    with pytest.raises(ValueError):
+        vq.vq_qgemm_dequant(a, sa, dev(5, 32, 64, dt=wt), sb, flag, y=dev(6, 32, dt=torch.bfloat16), ws=False)
+    with pytest.raises(TypeError):
+        vq.vq_qgemm_dequant(a, sa, torch.empty(2, 32, 64, dtype=wt), sb, flag, y=dev(6, 32, dt=torch.bfloat16), ws=False)
+    assert not launched(vq)
