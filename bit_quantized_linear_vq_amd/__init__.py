@@ -859,7 +859,7 @@ def vq_qgemm_experts(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: tor
     rows) times expert e's packed weights, dequantized as vq_qgemm_dequant does.
 
     b, sb: one vq_pack_weights of all experts' weights, [E * N x K] (row-major or in K
-    pieces).  Rows of y outside the offsets are not written.  Returns y [T x N]."""
+    pieces).  Codes with an outlier partition (idx=) are refused.  Rows of y outside the offsets are not written.  Returns y [T x N]."""
     if not (isinstance(a, torch.Tensor) and a.is_cuda and a.dim() == 2):
         raise TypeError("a must be a 2-D CUDA (HIP) tensor")
     m, kp = a.shape
@@ -880,8 +880,11 @@ def vq_qgemm_experts(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: tor
         _dense(b, "b", index, (torch.int8,) if b_bits == 8 else _U8, 0)
         if b.shape != (((row_bytes + 63) // 64, total, 64) if kblock else (total, row_bytes)):
             raise ValueError(f"b must be packed {b_bits}-bit codes of [E * N x {kp}] weights")
+    # Exactly: more are those of codes with an outlier partition, two to a row.
     _dense(sa, "sa", index, _F32, m)
     _dense(sb, "sb", index, _F32, total)
+    if sa.numel() != m or sb.numel() != total:
+        raise ValueError(f"sa and sb must hold {m} and {total} scales: the experts take codes of one partition")
     t, r_ptr, y, ldy = _experts_rows(m, rows, index, a.device, y, n, out_dtype)
     _launch("vq_qgemm_experts", index, a.data_ptr(), sa.data_ptr(), b.data_ptr(),
             b_bits | (VQ_W_KBLOCK if kblock else 0), sb.data_ptr(), offsets.data_ptr(), experts, r_ptr, m, t, n, kp,

@@ -439,9 +439,10 @@ vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k
  * Matrix products of several experts in one launch.  Rows are sorted by expert: output
  * row i in [offsets[e], offsets[e + 1]) is row rows[i] of a (row i without `rows`) times
  * expert e's weights.
- *   vq_qgemm_experts       codes and scales as vq_qgemm_dequant takes them (per-token
- *                          scales, single partition); a row's output is that call's, bit
- *                          for bit
+ *   vq_qgemm_experts       codes and scales as vq_qgemm_dequant takes them with k0 = kp
+ *                          (per-token scales, one partition: codes with an outlier
+ *                          partition have two scales a row, which would be read as those of
+ *                          two rows); a row's output is that call's, bit for bit
  *   vq_gemm_dense_experts  16-bit rows and weights as vq_gemm_dense takes them, with its
  *                          error bound
  *   offsets    device int32 [experts + 1], 0 <= offsets[e] <= offsets[e + 1] <= t.  Rows of y

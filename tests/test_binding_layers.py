@@ -80,3 +80,27 @@ def test_the_piece_flag_in_the_width_passes_no_check_by(vq, bits):
     with pytest.raises(TypeError):
         vq.vq_qgemm_dequant(a, sa, torch.empty(2, 32, 64, dtype=wt), sb, flag, y=dev(6, 32, dt=torch.bfloat16), ws=False)
     assert not launched(vq)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(sa=(6, 2)), dict(sa=(12,)), dict(sb=(64, 2)), dict(sb=(128,)), dict(sa=(6, 2), sb=(64, 2)), dict(sa=(5,)), dict(sb=(63,)),
+])
+def test_scales_of_two_partitions_are_refused(vq, kw):
+    """The codes of an outlier partition have two scales a row: the experts take one."""
+    with pytest.raises(ValueError):
+        experts(vq, **{n: dev(*shape) for n, shape in kw.items()})
+    assert not launched(vq)
+
+
+def test_operands_with_an_outlier_partition_do_not_fit_the_experts(vq):
+    """As the quantizers return them: codes [M x kp], scales [M x 2]."""
+    idx, x, w = dev(3, dt=torch.int32), dev(6, 128, dt=torch.bfloat16), dev(64, 128, dt=torch.bfloat16)
+    a, sa = vq.vq_rmsnorm_quant(x, None, 8, idx=idx)
+    b, sb = vq.vq_pack_weights(w, 8, idx=idx)
+    off = dev(3, dt=torch.int32)
+    vq._lib.launched.clear()
+    with pytest.raises(ValueError, match="one partition"):
+        vq.vq_qgemm_experts(a, sa, b, sb, 8, off)
+    with pytest.raises(ValueError, match="one partition"):
+        vq.vq_qgemm_experts(a, dev(6), b, sb, 8, off)
+    assert not launched(vq)
