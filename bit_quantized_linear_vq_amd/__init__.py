@@ -13,6 +13,7 @@ import functools
 import os
 
 import torch
+from torch.overrides import TorchFunctionMode
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvq.so")
@@ -950,6 +951,20 @@ class _Recorder:
         return record
 
 
+class _Holder(TorchFunctionMode):
+    """Keeps every tensor whose address is taken while it is active: the operands, outputs and
+    workspaces of the recorded launches, whoever made them."""
+
+    def __init__(self):
+        super().__init__()
+        self.held = []
+
+    def __torch_function__(self, func, types, args=(), kwargs=None):
+        if func is torch.Tensor.data_ptr:
+            self.held.append(args[0])
+        return func(*args, **(kwargs or {}))
+
+
 def prepare(fn, *args, **kwargs):
     """Validate and marshal a binding call once, for loops that repeat it on the same
     tensors (the binding's checks cost more host time than the kernels of a small layer).
@@ -959,17 +974,19 @@ def prepare(fn, *args, **kwargs):
     not given), and launch() enqueues the recorded launches again, unchanged, on torch's
     current stream of the device at that time (the device of fn's first device-tensor
     argument, else the current device).  fn may also be a caller's function that makes
-    binding calls: all their launches are recorded, in order.  The tensors involved must stay alive and
-    keep their storage and shape (launch() holds references to them; it reads their data
-    anew at each call).  fn must be one of the binding's asynchronous entry points;
+    binding calls: all their launches are recorded, in order.  launch() holds every tensor that a
+    recorded call addresses, also those that fn makes and drops; they must keep their
+    storage and shape (their data is read anew at each call).  fn must be one of the binding's asynchronous entry points;
     prepare() is not thread-safe (it swaps the library handle for the duration of fn).
     """
     global _lib
     real = _lib
     rec = _Recorder(real)
     _lib = rec
+    holder = _Holder()
     try:
-        result = fn(*args, **kwargs)
+        with holder:
+            result = fn(*args, **kwargs)
     finally:
         _lib = real
     if not rec.calls:
@@ -977,7 +994,7 @@ def prepare(fn, *args, **kwargs):
     tensors = [a for a in list(args) + list(kwargs.values()) if isinstance(a, torch.Tensor) and a.is_cuda]
     device = tensors[0].get_device() if tensors else torch.cuda.current_device()
     calls = rec.calls
-    keep = (args, kwargs, result)
+    keep = (args, kwargs, result, holder.held)
 
     def launch():
         st = torch._C._cuda_getCurrentRawStream(device)

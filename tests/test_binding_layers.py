@@ -1,7 +1,9 @@
 """The binding's checks of device tensors, without a GPU: tensors that have a device, a shape and
 no memory (torch's fake tensors) reach every check, and a call that passes them all would
 reach the launch, which here only takes note."""
+import gc
 import os
+import weakref
 
 import pytest
 import torch
@@ -32,6 +34,7 @@ def vq(monkeypatch):
     monkeypatch.setattr(m, "_getdev", lambda: 0)
     monkeypatch.setattr(m, "_rawstream", lambda i: 0)
     monkeypatch.setattr(m, "_stream", lambda t: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0)
     with FakeTensorMode():
         yield m
 
@@ -104,3 +107,29 @@ def test_operands_with_an_outlier_partition_do_not_fit_the_experts(vq):
     with pytest.raises(ValueError, match="one partition"):
         vq.vq_qgemm_experts(a, dev(6), b, sb, 8, off)
     assert not launched(vq)
+
+
+@pytest.mark.filterwarnings("ignore")
+def test_prepared_calls_hold_every_tensor_that_they_address(vq):
+    """A function's own tensors too: what it drops when it returns is still written to by the
+    recorded launches."""
+    w = dev(64, 128, dt=torch.bfloat16)
+    gone = []
+
+    def f(x):
+        c, s, h = vq.vq_rmsnorm_quant(x, None, 8, residual=x[:, :128])
+        n = vq.vq_rmsnorm(x, dev(128).to(torch.bfloat16))
+        b, sb = vq.vq_pack_weights(w, 8)
+        gone.extend(weakref.ref(t) for t in (c, s, h, n, b, sb))
+        return vq.vq_qgemm_experts(c, s, b, sb, 8, dev(3, dt=torch.int32)), vq.vq_gemm_dense_experts(
+            n, w.view(2, 32, 128), dev(3, dt=torch.int32))
+
+    launch, out = vq.prepare(f, dev(6, 128, dt=torch.bfloat16))
+    gc.collect()
+    assert [r() is None for r in gone] == [False] * len(gone)
+    assert not launched(vq) and len(out) == 2
+    launch()
+    assert launched(vq) == ["vq_rmsnorm_quant", "vq_rmsnorm", "vq_pack_weights", "vq_qgemm_experts", "vq_gemm_dense_experts"]
+    del launch, out
+    gc.collect()
+    assert all(r() is None for r in gone)
