@@ -971,12 +971,12 @@ def prepare(fn, *args, **kwargs):
 
     Runs fn(*args, **kwargs) with the library's launches recorded instead of enqueued, and
     returns (launch, result): result is what fn returned (its outputs, allocated now if
-    not given), and launch() enqueues the recorded launches again, unchanged, on torch's
-    current stream of the device at that time (the device of fn's first device-tensor
-    argument, else the current device).  fn may also be a caller's function that makes
-    binding calls: all their launches are recorded, in order.  launch() holds every tensor that a
-    recorded call addresses, also those that fn makes and drops; they must keep their
-    storage and shape (their data is read anew at each call).  fn must be one of the binding's asynchronous entry points;
+    not given), and launch() enqueues the recorded launches again, unchanged, on the device
+    of the tensors that they address (one for all of them), on torch's current stream of that
+    device at that time.  fn must be one of the binding's asynchronous entry points, or a
+    caller's function that makes such calls: all their launches are recorded, in order.
+    launch() holds every tensor that a recorded call addresses, also those that fn makes and
+    drops; they must keep their storage and shape (their data is read anew at each call).
     prepare() is not thread-safe (it swaps the library handle for the duration of fn).
     """
     global _lib
@@ -991,14 +991,25 @@ def prepare(fn, *args, **kwargs):
         _lib = real
     if not rec.calls:
         raise ValueError(f"{getattr(fn, '__name__', fn)} enqueues nothing through the library")
-    tensors = [a for a in list(args) + list(kwargs.values()) if isinstance(a, torch.Tensor) and a.is_cuda]
-    device = tensors[0].get_device() if tensors else torch.cuda.current_device()
+    devices = {t.get_device() for t in holder.held if t.is_cuda}
+    if len(devices) > 1:
+        raise ValueError(f"the calls of one prepared function must use one device, not {sorted(devices)}")
+    device = devices.pop() if devices else torch.cuda.current_device()
     calls = rec.calls
     keep = (args, kwargs, result, holder.held)
 
-    def launch():
+    def run():
         st = torch._C._cuda_getCurrentRawStream(device)
         for name, f, a in calls:
             _check(name, f(*a[:-1], st))
+
+    def launch():
+        if _getdev() == device:
+            return run()
+        prev = torch._C._cuda_exchangeDevice(device)
+        try:
+            run()
+        finally:
+            torch._C._cuda_exchangeDevice(prev)
     launch.keep = keep
     return launch, result

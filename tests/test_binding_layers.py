@@ -133,3 +133,25 @@ def test_prepared_calls_hold_every_tensor_that_they_address(vq):
     del launch, out
     gc.collect()
     assert all(r() is None for r in gone)
+
+
+@pytest.mark.filterwarnings("ignore")
+def test_prepared_calls_run_on_the_device_of_their_tensors(vq, monkeypatch):
+    """As the calls themselves do: with that device current, on its current stream."""
+    current, streams = [0], []
+
+    def exchange(i):
+        prev, current[0] = current[0], i
+        return prev
+    monkeypatch.setattr(vq, "_getdev", lambda: current[0])
+    monkeypatch.setattr(torch._C, "_cuda_exchangeDevice", exchange)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: streams.append((i, current[0])) or 70 + i)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    x = torch.empty(6, 128, dtype=torch.bfloat16, device="cuda:1")
+    launch, y = vq.prepare(lambda: vq.vq_rmsnorm(x, None))  # no tensor among the arguments
+    streams.clear()
+    launch()
+    assert streams == [(1, 1)] and current == [0] and y.get_device() == 1
+    x0 = dev(6, 128, dt=torch.bfloat16)
+    with pytest.raises(ValueError, match="device"):
+        vq.prepare(lambda: (vq.vq_rmsnorm(x, None), vq.vq_rmsnorm(x0, None)))
