@@ -30,13 +30,19 @@ __global__ __launch_bounds__(256) void k_pack_group(const uint16_t* w, int64_t l
     float v[8];
 #pragma unroll
     for (int t = 0; t < 4; ++t) decode2<DT>(raw[t], v[2 * t], v[2 * t + 1]);
-    float m = 0.0f;
+    // An infinity or NaN makes its group's maximum infinite (fmaxf alone would pass a NaN by).
+    float m = 0.0f, z = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) m = fmaxf(m, fabsf(v[t]));
+    for (int t = 0; t < 8; ++t) {
+      m = fmaxf(m, fabsf(v[t]));
+      z += v[t] * 0.0f;
+    }
+    if (!(z == 0.0f)) m = bits_f(0x7F800000u);
     if (!ok) m = 0.0f;
 #pragma unroll
     for (int o = LPG / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    const unsigned s16 = cvt_pair<DT>(m / 7.0f, 0.0f) & 0xFFFFu;
+    const bool bad = !(m < bits_f(0x7F800000u));
+    const unsigned s16 = bad ? (DT == DT_BF16 ? 0x7FC0u : 0x7E00u) : cvt_pair<DT>(m / 7.0f, 0.0f) & 0xFFFFu;
     float s, unused;
     decode2<DT>(s16, s, unused);
     float r = 1.0f / s;
@@ -44,7 +50,7 @@ __global__ __launch_bounds__(256) void k_pack_group(const uint16_t* w, int64_t l
     if (ok) {
       unsigned u[8];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) u[t] = qbyte(v[t], r, 7.0f);
+      for (int t = 0; t < 8; ++t) u[t] = qbyte(bad ? 0.0f : v[t], r, 7.0f);
       *reinterpret_cast<unsigned*>(codes + row * (k / 2) + 4 * p) = pack8_nibbles(u);
       if ((p & (LPG - 1)) == 0) scales[row * (ppr / LPG) + p / LPG] = (uint16_t)s16;
     }

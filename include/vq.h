@@ -411,7 +411,8 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  * bound by the weights' bytes, so the activations stay at 16 bits.
  *   s[j,g] = RNE_dt(fl32(max|w| / 7)) over the group;  r = fl32(1 / s)
  *   c[j,k] = clamp(rne(fl32(w * r)), -7, 7); a group with s = 0 (or 1 / s infinite) has
- *            zero codes
+ *            zero codes; one with an infinity or NaN has zero codes and a NaN scale, so that
+ *            its channel's outputs are NaN
  *   y[i,j] = RNE_out(sum_g s[j,g] * sum_{k in g} c[j,k] x[i,k]), products exact, sums in
  *            float32 (in an order fixed by the sizes): with G = group
  *            |y - exact| <= (2 G + k / G + 18) 2^-24 * sum_k |s c x_k| before the output

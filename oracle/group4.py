@@ -2,6 +2,7 @@
 16-bit rows (test infrastructure only).
 
   s = RNE16(fl32(max|w| / 7)) over a group;  r = fl32(1 / s);  c = clamp(rne(fl32(w * r)), -7, 7)
+  (a group with an infinity or NaN: zero codes, a NaN scale)
   y = sum_g s_g * sum_{k in g} c_k x_k
 
 The reference product is the exact sum in float64.  The device adds the exact products c x in
@@ -23,11 +24,14 @@ def pack(w_store, dtype: str, group: int):
     w = to_f32(w_store, dtype)
     n, k = w.shape
     g = w.reshape(n, k // group, group)
-    s_store = from_f32((np.max(np.abs(g), axis=2) / np.float32(7.0)).astype(np.float32), dtype)
+    bad = ~np.isfinite(g).all(axis=2)
+    g = np.where(bad[:, :, None], np.float32(0), g)
+    s32 = (np.max(np.abs(g), axis=2) / np.float32(7.0)).astype(np.float32)
+    s_store = from_f32(np.where(bad, np.float32("nan"), s32), dtype)
     s = to_f32(s_store, dtype)
-    with np.errstate(divide="ignore", over="ignore"):
+    with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
         r = (np.float32(1.0) / s).astype(np.float32)
-    r = np.where((s > 0) & np.isfinite(r), r, np.float32(0)).astype(np.float32)
+        r = np.where((s > 0) & np.isfinite(r), r, np.float32(0)).astype(np.float32)
     c = np.clip(np.rint((g * r[:, :, None]).astype(np.float32)), -7, 7).astype(np.int8).reshape(n, k)
     return c, pack_int4(c), s_store
 

@@ -73,3 +73,29 @@ def test_an_infinity_meets_its_code(vq, dt):
     with np.errstate(invalid="ignore"):
         want = np.float32(np.inf) * c[:, 9].astype(np.float32)
     assert np.array_equal(y[1], want, equal_nan=True) and np.array_equal(y[2], -want, equal_nan=True)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_weights_that_are_not_finite(vq, dt, group):
+    """Their group has a NaN scale and zero codes, the other groups are as without them, and the
+    channel's outputs say so."""
+    rng = np.random.default_rng(group)
+    n, k = 9, 3 * group
+    w = (rng.standard_normal((n, k)) * 0.02).astype(np.float32)
+    clean = vq.vq_pack_weights_group(gen.to_storage(w, dt).to(DEV), group)[0].cpu().numpy()
+    w[1, 0], w[2, group - 1], w[3, group + 5], w[4, 3 * group - 1] = np.nan, np.inf, -np.inf, np.nan
+    w[5, group:2 * group] = np.nan
+    w[6, 3], w[6, 4] = np.inf, np.nan
+    ws = gen.to_storage(w, dt)
+    codes, scales = vq.vq_pack_weights_group(ws.to(DEV), group)
+    bad = np.zeros((n, 3), dtype=bool)
+    bad[1, 0] = bad[2, 0] = bad[3, 1] = bad[4, 2] = bad[5, 1] = bad[6, 0] = True
+    _, packed, s = group4.pack(gen.as_numpy_bits(ws), dt, group)
+    assert np.array_equal(np.isnan(onum.to_f32(s, dt)), bad)
+    got_c, got_s = codes.cpu().numpy(), onum.to_f32(gen.as_numpy_bits(scales.cpu()), dt)
+    assert np.array_equal(got_c, packed) and np.array_equal(got_s, onum.to_f32(s, dt), equal_nan=True)
+    keep = np.repeat(~bad, group // 2, axis=1)
+    assert np.array_equal(got_c[keep], clean[keep]) and not got_c[~keep].any()
+    y = vq.vq_w4_gemv(torch.ones((2, k), dtype=ws.dtype, device=DEV), codes, scales, torch.float32).cpu().numpy()
+    assert np.array_equal(np.isnan(y), np.broadcast_to(bad.any(1), (2, n)))
