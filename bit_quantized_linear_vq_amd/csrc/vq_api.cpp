@@ -529,8 +529,9 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
 
 namespace {
 bool ok_group(int group) { return group == 32 || group == 64 || group == 128; }
-// Limits of the product's launch grid.
-constexpr int64_t kMaxGemvRows = (int64_t)1 << 20, kMaxGemvCols = (int64_t)1 << 24;
+// Limits of the product's launch grid, and of its 32-bit counts of channels (in pieces of 128, a
+// chunk past the end).
+constexpr int64_t kMaxGemvRows = (int64_t)1 << 20, kMaxGemvCols = (int64_t)1 << 24, kMaxGemvK = (int64_t)1 << 30;
 }  // namespace
 
 vq_status vq_pack_weights_group(const void* w, vq_dtype dt, int64_t n, int64_t k, int64_t ldw, int group,
@@ -549,7 +550,7 @@ vq_status vq_w4_gemv(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k
   if (!is_16bit(dt) || !valid_dt(out_dt)) return VQ_ERR_INVALID_ARG;
   if (m < 0 || n < 1 || k < 1 || m >= kMaxDim || n >= kMaxDim || k >= kMaxDim) return VQ_ERR_INVALID_ARG;
   if (!codes || !scales || (m > 0 && (!x || !y)) || ldx < k || ldy < n) return VQ_ERR_INVALID_ARG;
-  if (!ok_group(group) || m > kMaxGemvRows || n > kMaxGemvCols) return VQ_ERR_UNSUPPORTED;
+  if (!ok_group(group) || m > kMaxGemvRows || n > kMaxGemvCols || k > kMaxGemvK) return VQ_ERR_UNSUPPORTED;
   if (k % group || !aligned16(x) || ldx % 8 || !aligned16(codes) || reinterpret_cast<uintptr_t>(scales) % 2)
     return VQ_ERR_SHAPE;
   if (reinterpret_cast<uintptr_t>(y) % (uintptr_t)elem_size(out_dt)) return VQ_ERR_SHAPE;

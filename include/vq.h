@@ -429,7 +429,8 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  * 4 to 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x stay
  * in their row, where an infinity meets a code as in the formula (a zero code gives NaN).
  * One kernel; nothing is allocated.
- * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group, m > 2^20, n > 2^24).
+ * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group; of the product
+ * also m > 2^20, n > 2^24, k > 2^30).
  */
 vq_status vq_pack_weights_group(const void* w, vq_dtype dt, int64_t n, int64_t k, int64_t ldw, int group,
                                 uint8_t* codes, void* scales, hipStream_t stream);
