@@ -307,7 +307,8 @@ constexpr int A_BYTES = BM * ROW;
 constexpr int LA = A_BYTES / (NT * 16);  // direct loads per wave and stage (2)
 }  // namespace xp
 
-__device__ const float x_zero = 0.0f, x_one = 1.0f;
+// Row scales of an index outside a and of 16-bit rows.  No row's own scale is -0.
+__device__ const float x_none = -0.0f, x_one = 1.0f;
 
 template <int KIND, int OUT_DT>
 __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_experts_pp(XArgs g) {
@@ -445,12 +446,12 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     for (int i = 0; i < LB; ++i) gb[i] = g.b + x.e * g.b_expert + (int64_t)min(x.n0 + rb[i], g.n - 1) * g.ldb + cb[i];
     boff = 0;
   };
-  // Row scales (0 for an index outside a; 1 for 16-bit rows) and column scales, by direct
+  // Row scales (x_none for an index outside a; 1 for 16-bit rows) and column scales, by direct
   // loads ahead of the tile's first stage.
   auto load_scales = [&](const Tile& x, int buf) {
     if (wave < 4) {
       const bool ok = (unsigned)is < (unsigned)g.m_a;
-      const float* src = !ok ? &x_zero : INT ? g.sa + is : &x_one;
+      const float* src = !ok ? &x_none : INT ? g.sa + is : &x_one;
       dma4(src, &s_sa[buf][64 * wave]);
     } else {
       const float* src = INT ? g.sb + (int64_t)x.e * g.n + min(x.n0 + rs, g.n - 1) : &x_one;
@@ -623,6 +624,8 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       const int ml = 64 * mb + 32 * wm + rl;
       const int m = c.r0 + ml;
       const float sa0 = s_sa[buf][ml];
+      // Zeros for an index outside a, also where a column's scale or a row of a is not finite.
+      const bool none = f_bits(sa0) == 0x80000000u, some_none = __any(none);
       const bool shift = odd && (((int64_t)(reinterpret_cast<uintptr_t>(g.y) >> 1) + m * g.ldy) & 1);
       unsigned before = 0;  // the eight columns before this lane's: the last two
 #pragma unroll
@@ -640,13 +643,17 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
               const float t0 = sa0 * sb_r[nb][q][r];
               out[r] = (float)a0 * t0;
             } else {
-              out[r] = sa0 != 0.0f ? acc[mb][nb][4 * q + r] : 0.0f;
+              out[r] = acc[mb][nb][4 * q + r];
             }
           }
           if constexpr (HALF_OUT) {
             pk[2 * q] = cvt_pair<OUT_DT>(out[0], out[1]);
             pk[2 * q + 1] = cvt_pair<OUT_DT>(out[2], out[3]);
           } else {
+            if (some_none) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) out[r] = none ? 0.0f : out[r];
+            }
             float* dst = reinterpret_cast<float*>(g.y) + (int64_t)m * g.ldy + n;
             if (ml < c.rows && n + 4 <= g.n) {
               *reinterpret_cast<v4f_any*>(dst) = v4f{out[0], out[1], out[2], out[3]};
@@ -660,7 +667,8 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
           for (int pr = 0; pr < 2; ++pr) {
             const auto s0 = __builtin_amdgcn_permlane32_swap(pk[4 * pr], pk[4 * pr + 2], false, false);
             const auto s1 = __builtin_amdgcn_permlane32_swap(pk[4 * pr + 1], pk[4 * pr + 3], false, false);
-            const u4v w = {s0[0], s1[0], s0[1], s1[1]};
+            u4v w = {s0[0], s1[0], s0[1], s1[1]};
+            if (some_none) w = none ? u4v{0u, 0u, 0u, 0u} : w;
             const int no = c.n0 + wn * WTN + nb * 32 + 16 * pr + 8 * kc;
             h_t* dst = reinterpret_cast<h_t*>(g.y) + (int64_t)m * g.ldy + no;
             u4v wide = w;
