@@ -99,3 +99,48 @@ def test_weights_that_are_not_finite(vq, dt, group):
     assert np.array_equal(got_c[keep], clean[keep]) and not got_c[~keep].any()
     y = vq.vq_w4_gemv(torch.ones((2, k), dtype=ws.dtype, device=DEV), codes, scales, torch.float32).cpu().numpy()
     assert np.array_equal(np.isnan(y), np.broadcast_to(bad.any(1), (2, n)))
+
+
+# (rows, outputs, K, group): together every number of parts of K (1 to 16), of waves, of rows a
+# workgroup and of loads of x a thread, K that ends inside a chunk of 512 or a piece of 128, parts of
+# unequal length and parts of none.
+EXACT = [
+    (1, 1, 16416, 32), (1, 2048, 4128, 32), (1, 300, 32, 32), (2, 515, 8256, 64), (1, 4100, 4128, 32), (2, 4100, 2208, 32),
+    (3, 100, 16416, 32), (4, 515, 8320, 128), (100, 17, 4128, 32), (6, 40, 96, 32), (11, 2048, 8224, 32), (16, 300, 16416, 32),
+    (1, 8209, 1056, 32), (2, 12300, 1088, 64), (4, 8209, 2080, 32), (5, 4100, 4128, 32), (8, 4100, 1184, 32),
+    (65, 515, 2112, 64), (5, 12300, 1056, 32), (8, 8209, 1152, 128), (16, 4100, 2080, 32),
+    (1, 20001, 1056, 32), (3, 16385, 1152, 128), (7, 16385, 1056, 32), (8, 20001, 608, 32), (9, 8209, 2080, 32),
+    (13, 12300, 1216, 64), (12, 25001, 1056, 32), (16, 25001, 640, 128), (64, 4100, 1088, 64),
+    (17, 16385, 1056, 32), (31, 20001, 576, 64), (32, 28671, 544, 32), (65, 8209, 1184, 32),
+]
+
+
+def whole_numbers(m, n, k, group, dt, seed=0):
+    """x of whole numbers up to 7, any code, scales that are powers of two: every partial sum is a
+    multiple of 1/4 below 7 * 8 * 2 * K < 2^22, so that float32 holds it exactly in any order."""
+    assert 7 * 8 * 2 * k < 2 ** 22
+    rng = np.random.default_rng([m, n, k, seed])
+    x = gen.to_storage(rng.integers(-7, 8, (m, k)).astype(np.float32), dt)
+    packed = rng.integers(0, 256, (n, k // 2), dtype=np.uint8)
+    s = gen.to_storage(np.exp2(rng.integers(-2, 2, (n, k // group))).astype(np.float32), dt)
+    w = group4.unpack(packed).astype(np.float32) * np.repeat(onum.to_f32(gen.as_numpy_bits(s), dt), group, axis=1)
+    return x, packed, s, onum.to_f32(gen.as_numpy_bits(x), dt).astype(np.float64) @ w.astype(np.float64).T
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n,k,group", EXACT)
+def test_products_of_whole_numbers_are_exact(vq, m, n, k, group, dt):
+    x, packed, s, want = whole_numbers(m, n, k, group, dt)
+    y = vq.vq_w4_gemv(x.to(DEV), torch.from_numpy(packed).to(DEV), s.to(DEV), torch.float32)
+    assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp16"])
+@pytest.mark.parametrize("m,n,k,group", [(1, 4100, 4128, 32), (7, 100, 1056, 32), (20, 515, 640, 128)])
+def test_exact_products_are_rounded_once(vq, m, n, k, group, out):
+    x, packed, s, want = whole_numbers(m, n, k, group, "bf16")
+    y = vq.vq_w4_gemv(x.to(DEV), torch.from_numpy(packed).to(DEV), s.to(DEV), torch.bfloat16 if out == "bf16" else torch.float16)
+    with np.errstate(over="ignore"):
+        w = onum.from_f32(want.astype(np.float32), out)
+    assert np.array_equal(gen.as_numpy_bits(y.cpu()).view(np.uint16) & 0x7FFF, w.view(np.uint16) & 0x7FFF)
+    assert np.array_equal(np.sign(onum.to_f32(gen.as_numpy_bits(y.cpu()), out)), np.sign(want))
