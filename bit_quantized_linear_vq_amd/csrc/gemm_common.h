@@ -96,6 +96,18 @@ __device__ __forceinline__ void store4_f32(void* y, int64_t off, const float v[4
   }
 }
 
+// 16 packed 4-bit codes (low nibble = even k) as int8 values 16 c, in order.
+__device__ __forceinline__ v4i unpack_int4x16(u2v w) {
+  const unsigned h0 = w.x & 0xF0F0F0F0u, l0 = (w.x << 4) & 0xF0F0F0F0u;
+  const unsigned h1 = w.y & 0xF0F0F0F0u, l1 = (w.y << 4) & 0xF0F0F0F0u;
+  v4i r;
+  r.x = (int)__builtin_amdgcn_perm(h0, l0, 0x05010400u);
+  r.y = (int)__builtin_amdgcn_perm(h0, l0, 0x07030602u);
+  r.z = (int)__builtin_amdgcn_perm(h1, l1, 0x05010400u);
+  r.w = (int)__builtin_amdgcn_perm(h1, l1, 0x07030602u);
+  return r;
+}
+
 // Work item w of a persistent GEMM with the remainder split: items [0, dp_items) are
 // whole tiles, the rest are `split` consecutive K ranges of each remaining tile.  Written
 // with selects only: with an if/else that assigns the fields on both sides, the compiler

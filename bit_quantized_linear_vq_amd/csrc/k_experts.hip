@@ -83,17 +83,6 @@ __device__ __forceinline__ bool find_tile(const XArgs& g, int bm, int tile, RowT
   return false;
 }
 
-__device__ __forceinline__ v4i unpack4(u2v w) {
-  const unsigned h0 = w.x & 0xF0F0F0F0u, l0 = (w.x << 4) & 0xF0F0F0F0u;
-  const unsigned h1 = w.y & 0xF0F0F0F0u, l1 = (w.y << 4) & 0xF0F0F0F0u;
-  v4i r;
-  r.x = (int)__builtin_amdgcn_perm(h0, l0, 0x05010400u);
-  r.y = (int)__builtin_amdgcn_perm(h0, l0, 0x07030602u);
-  r.z = (int)__builtin_amdgcn_perm(h1, l1, 0x05010400u);
-  r.w = (int)__builtin_amdgcn_perm(h1, l1, 0x07030602u);
-  return r;
-}
-
 // ---------------------------------------------------------------------------------------
 // Few rows per expert (decoding): a product is bound by the weights' bytes, and each is
 // needed by one tile only.  A workgroup owns 16 rows of outputs and 32 columns for each of
@@ -173,7 +162,7 @@ __global__ __launch_bounds__(256) void k_experts_few(XArgs g, int tiles_n) {
         if constexpr (KIND == X_I4) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(unpack4(h ? u2v{(unsigned)w.z, (unsigned)w.w} : u2v{(unsigned)w.x, (unsigned)w.y}), fa[set][u][h], acc[b], 0, 0, 0);
+            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(unpack_int4x16(h ? u2v{(unsigned)w.z, (unsigned)w.w} : u2v{(unsigned)w.x, (unsigned)w.y}), fa[set][u][h], acc[b], 0, 0, 0);
         } else if constexpr (KIND == X_I8) {
           acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, fa[set][u][0], acc[b], 0, 0, 0);
         } else if constexpr (KIND == X_F16) {
@@ -522,7 +511,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #pragma unroll
         for (int nb = 0; nb < NBLK; ++nb) {
           v4i b;
-          if constexpr (KIND == X_I4) b = unpack4(fB[h][nb]);
+          if constexpr (KIND == X_I4) b = unpack_int4x16(fB[h][nb]);
           else b = fB[h][nb];
 #pragma unroll
           for (int mb = 0; mb < NM; ++mb) {

@@ -105,17 +105,6 @@ __device__ __forceinline__ int64_t wofs(const GArgs& g, int c) {
   else return c;
 }
 
-__device__ __forceinline__ v4i unpack_int4x16(u2v w) {
-  const unsigned h0 = w.x & 0xF0F0F0F0u, l0 = (w.x << 4) & 0xF0F0F0F0u;
-  const unsigned h1 = w.y & 0xF0F0F0F0u, l1 = (w.y << 4) & 0xF0F0F0F0u;
-  v4i r;
-  r.x = (int)__builtin_amdgcn_perm(h0, l0, 0x05010400u);
-  r.y = (int)__builtin_amdgcn_perm(h0, l0, 0x07030602u);
-  r.z = (int)__builtin_amdgcn_perm(h1, l1, 0x05010400u);
-  r.w = (int)__builtin_amdgcn_perm(h1, l1, 0x07030602u);
-  return r;
-}
-
 template <int BBITS, int OUT_DT, bool DUAL, int H, bool KB>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_qgemm(GArgs g) {
   static_assert(!DUAL || H == 2 || (H == 4 && BBITS == 4),
