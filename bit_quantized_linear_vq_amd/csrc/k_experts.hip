@@ -281,10 +281,12 @@ static hipError_t launch_few_kind(const XArgs& a, int out_dt, hipStream_t st) {
 // since the time of a short tile is that of its weights (64 rows, 8192 -> 16384: 84 us whole,
 // 54 in four).
 //
-// Measured: 17776 rows over 8 experts, 1920 -> 5760, 8-bit, 238 us = 1.65 POP/s; 6001 over 4,
-// 12288 -> 1920, 4-bit, 167 us = 1.69; 8190 over 8, 2048 -> 5759, 16-bit, 265 us = 0.73 PFLOP/s (235
-// for 5760, 185 for one expert: 1.05).  The matrix units' power sets the rate of whole tiles:
-// dealing the last tiles out evenly by their measured cost changed nothing.  4124 rows over 32
+// Measured: 17776 rows over 8 experts, 1920 -> 5760, 8-bit, 234 us = 1.68 POP/s; 6001 over 4,
+// 12288 -> 1920, 4-bit, 162 us = 1.74; 8190 over 8, 2048 -> 5759, 16-bit, 243 us = 0.80 PFLOP/s (237
+// for 5760; 191 for one expert: 1.01, whose 736 tiles are 2.9 rounds of 256, where the eight experts'
+// 830 to 850 are 3.3 and the last round's pieces each walk all of K).  With 8-bit and 4-bit codes the
+// matrix units' power sets the rate of whole tiles: dealing the last tiles out evenly by their
+// measured cost changed nothing.  4124 rows over 32
 // experts, 2048 -> 2048, 8-bit: 54 us, where the weights alone take 27: a first round of 256 tiles
 // at 4 TB/s and a second one that is bound by the latency of its stages.
 namespace xp {
@@ -699,7 +701,7 @@ __global__ __launch_bounds__(xp::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 template <int KIND>
 static hipError_t launch_pp_kind(XArgs a, int out_dt, hipStream_t st) {
   const int64_t tiles = (a.t / xp::BM + (a.experts < a.t ? a.experts : a.t)) * (int64_t)((a.n + xp::BN - 1) / xp::BN);
-  a.max_items = (int)tiles;  // at most 2^30 (the entry point's limits)
+  a.max_items = (int)tiles;  // at most (2^18 + 2^10) * 2^12 (the entry point's limits)
   const int pb = vq_internal::persistent_blocks();
   const dim3 grid((unsigned)std::min<int64_t>(4 * tiles, pb));  // a tile may be cut in four
   const size_t shm = (size_t)a.experts * 16;  // at most 16 KB beside the 132 KB of the ring and scales
@@ -721,7 +723,9 @@ static hipError_t launch_kind(const XArgs& a, int out_dt, hipStream_t st) {
   // rows from which the other one wins grow a little more slowly than their number falls:
   // 64 tiles (8 experts, 4096 -> 2048), 16 / 32 rows each, 19.1 / 29.2 against 21.4 / 21.5,
   // 14.3 / 21.0 against 25.0 / 25.1, 39.0 / 58.6 against 54.1 / 54.2; 16 tiles (2 experts), 64
-  // rows each, 18.1 against 23.2, 13.2 against 27.6, 32.6 against 41.0.
+  // rows each, 18.1 against 23.2, 13.2 against 27.6, 32.6 against 41.0.  The rule is a power law through
+  // three numbers of tiles and takes the slower kernel at two of these points: 16 tiles, 8-bit, 64 rows
+  // each (it turns at 48), and 64 tiles, 4-bit, 32 rows each (at 28).
   const int64_t used = std::min<int64_t>(a.experts, a.t);
   const int64_t cus = vq_internal::persistent_blocks();
   const int64_t tiles = std::min<int64_t>(used * ((a.n + xp::BN - 1) / xp::BN), cus);

@@ -18,8 +18,10 @@
 // that up to 2048 elements a row needs one wave and no barrier; with few, one piece, for the
 // latency.
 //
-// Measured: 17776 x 1920 with the residual, to codes 46.2 us = 5.2 TB/s, to 16 bits 47.4 us = 5.8 TB/s; 4113 x
-// 4096 to 16 bits 27.0 us (21.6 where buffers are used again), 4113 x 4095 29.0 us; one row of 1920 3.3 us.  A large copy reaches 5.0-5.4 TB/s.
+// Measured, back to back over three sets of buffers: 17776 x 1920 with the residual, to codes 46.9 us = 5.1
+// TB/s (alone in a trace 46.4-52, median 47.2), to 16 bits 45.5 us = 6.0 TB/s (50.8 over eight sets: the
+// last-level cache holds the rest); 4113 x 4096 to 16 bits 27.2 us (21.4 over one set), 4113 x 4095 28.6 us;
+// one row of 1920 4.5 us, 3.1 in a trace.  A large copy reaches 5.0-5.4 TB/s.
 #include <algorithm>
 
 #include "dev_common.h"
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
       }
     }
   }
-  const double inv_k = (double)a.k;
+  const double kd = (double)a.k;
 
   int buf = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < a.rows; row0 += (int64_t)gridDim.x * rpb, buf ^= 1) {
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
           raw[j][i] = cvt_pair<DT>(x0 + r0, x1 + r1);
         }
       }
-      // Eight squares, exact in float32; the pieces past the row's end repeat its first one.
+      // Eight squares, each exact in float64; the pieces past the row's end repeat its first one.
       double p = 0.0;
       const int before = END == END_OVERLAP ? elem(j) - at(j) : 0;  // counted by the piece before
 #pragma unroll
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
       ss = 0.0;
       for (int w = 0; w < wpr; ++w) ss += s_sum[buf][rib * wpr + w];
     }
-    const float rstd = (float)(1.0 / sqrt(ss / inv_k + a.eps));
+    const float rstd = (float)(1.0 / sqrt(ss / kd + a.eps));
 
     if (a.h && row_ok) {
       uint16_t* hr = a.h + row * a.ldh;

@@ -96,9 +96,12 @@ struct GemvArgs {
 // Measured, with the launch, bfloat16 / fp16 rows (in brackets with codes left at c + 24): 4096 -> 12288,
 // one row, groups of 64, 10.4 / 9.6 us (9.5 / 9.6); 8192 -> 28672, one row, groups of 128, 34.4 / 31.1 us = 3.5
 // / 3.9 TB/s (30.0 / 29.9); 8192 -> 28671, seven rows, groups of 32, 42.9 / 41.1 us = 3.1 / 3.2 TB/s (40.3 /
-// 40.4); 32 rows, groups of 128, 8192 -> 8192 24.2 / 22.2 us (22.1 / 22.3), 8192 -> 28672 53.0 / 49.9 (51.9 / 51.3).
+// 40.4); 32 rows, groups of 128, 8192 -> 8192 24.2 / 22.2 us (22.1 / 22.3), 8192 -> 28672 53.0 / 49.9 (51.9 /
+// 51.3).  For every 512 codes a wave has 35 / 25 vector instructions with groups of 32, 29 / 20 with 128: the
+// vector units are busy 55% / 40% of the seven rows' time, 53% / 39% of the one row's, and on average 2.2
+// waves of a possible 4 are there, as the last workgroups end.
 // Two blocks of channels a wave (x read from LDS once for both) was slower nearly everywhere
-// (8192 -> 28672 32.0 us): half the waves.
+// (8192 -> 28672 32.0 against 30.2 us, codes at c + 24): half the waves.
 constexpr int GV_SETS = 2;
 constexpr int GV_CHUNK = 4;                         // pieces
 constexpr int GV_ROW = GV_CHUNK * 256 + 16;         // bytes of a row of a chunk of x in LDS
@@ -351,9 +354,9 @@ static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
   } else {
     // Many rows of x leave LDS (above 16 rows and parts also registers) for fewer than the four
     // workgroups of four waves that a compute unit can hold: eight waves then share the same x,
-    // unless all workgroups fit at once.  8192 -> n, groups of 128, 4 / 8 waves, us: 16 rows, n =
-    // 16384 23.1 / 25.2, 20480 40.5 / 34.3, 28672 49.9 / 37.0; 8 rows, n = 8192 13.7 / 14.4, 12288
-    // 22.5 / 19.2; groups of 32, 9 rows, 28672 49.2 / 38.6, 7 rows 40.5 / 38.8 but 24576 33.2 / 37.6.
+    // unless all workgroups fit at once.  8192 -> n, bfloat16, groups of 128, 4 / 8 waves, us: 16 rows, n =
+    // 16384 24.6 / 27.7, 20480 44.0 / 38.6, 28672 52.5 / 41.0; 8 rows, n = 8192 14.7 / 15.6, 12288
+    // 24.3 / 21.2; groups of 32, 9 rows, 28672 54.2 / 43.8, 7 rows 42.9 / 43.1 but 24576 35.9 / 42.7.
     const int fit = std::min((int)(GV_LDS / gv_shared(KS, 1, a.tile, 4)), a.tile * KS > 16 ? 3 : 4);
     const int64_t groups = ((int64_t)a.n * KS + 63) / 64 * ((a.m + a.tile - 1) / a.tile);
     if (fit < 4 && groups > (int64_t)fit * vq_internal::persistent_blocks()) launch_gemv_waves<DT, GROUP, KS, 1, 8>(a, st);
@@ -363,10 +366,11 @@ static void launch_gemv_part(const GemvArgs& a, hipStream_t st) {
 
 template <int DT, int GROUP>
 static void launch_gemv_group(GemvArgs a, hipStream_t st) {
-  // Parts of K: waves enough for the whole card, at least two.  One row, us with 2 / 4 / 8 / 16
-  // parts: 16384 -> 2048 28.3 / 16.0 / 12.2 / 10.8; 8192 -> 8192 16.0 / 11.2 / 11.6 / 16.2; 4096 ->
-  // 14336 9.6 / 10.2 / 11.5 / 20.8; 8192 -> 28672 30.3 / 30.2 / 33.4 / 48.4; seven rows, groups of
-  // 32, 8192 -> 28671 40.8 / 53.7.  Many rows of x leave room in LDS for fewer parts.
+  // Parts of K: waves enough for the whole card, at least two.  One bfloat16 row, us with 2 / 4 / 8 / 16
+  // parts: 16384 -> 2048 30.1 / 17.1 / 13.2 / 11.7; 8192 -> 8192 17.0 / 12.0 / 12.7 / 16.5; 4096 ->
+  // 14336 11.2 / 11.6 / 11.3 / 20.2; 8192 -> 28672 34.9 / 32.6 / 35.4 / 50.2 (fp16 31.0 / 29.5 / 33.9 / 46.2:
+  // the rule's two give up 5 to 7% there); seven rows, groups of 32, 8192 -> 28671 42.9 / 47.3.  Many rows of
+  // x leave room in LDS for fewer parts.
   const int64_t blocks = ((int64_t)a.n + 15) / 16;
   int ks = 2;
   while (ks < 16 && ks * blocks < 1600) ks *= 2;
@@ -374,9 +378,9 @@ static void launch_gemv_group(GemvArgs a, hipStream_t st) {
   if (a.m > 4) {
     // Fewer rows a workgroup leave room for more parts, as long as all waves are there at once
     // (16 a compute unit; the weights' further readings come from the caches).  Us with tiles of 32 / 16 /
-    // 8 / 4 rows and 1 / 2 / 4 / 8 parts: 32 rows, 16384 -> 2048 77.9 / 36.8 / 22.3 / 32.6, 8192 -> 8192
-    // 42.0 / 25.4 / 40.5 / 76.3, 8192 -> 28672 52.1 / 64.4 / 117; 16 rows, 8192 -> 512 - / 17.2 / 9.9 / 7.5,
-    // 4096 - / 19.8 / 13.9 / 21.2, 4096 -> 12288 - / 13.0 / 16.4 / 33.1.
+    // 8 / 4 rows and 1 / 2 / 4 / 8 parts, bfloat16: 32 rows, 16384 -> 2048 83.9 / 40.7 / 24.6 / 38.1, 8192 ->
+    // 8192 43.6 / 25.5 / 38.8 / 71.9, 8192 -> 28672 52.9 / 73.0 / 129 / 242; 16 rows, 8192 -> 512 - / 19.0 / 11.0 /
+    // 8.2, 4096 - / 21.7 / 14.8 / 22.5, 4096 -> 12288 - / 14.2 / 17.7 / 34.8.
     for (int tile = 4; tile <= 16; tile *= 2) {
       const int parts = GV_ROWS / tile;
       const int64_t tiles = (a.m + tile - 1) / tile;

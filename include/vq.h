@@ -390,7 +390,8 @@ vq_status vq_gemm_dense(const void* x, const void* w, vq_dtype dt, int64_t m, in
  *              (an outlier index outside [0, k) gives code 0); gran VQ_PER_TOKEN or
  *              VQ_PER_TENSOR_STATIC
  * m = 0 enqueues nothing.  An infinity or NaN in a row makes that row's dynamic scale NaN
- * (its codes are then unspecified); one in the weight does so to every row.
+ * (its codes are then unspecified); one in the weight does so to every row.  With eps = 0 a
+ * row whose mean square is 0 has no norm: its rstd is infinite, and its outputs are NaN.
  * vq_rmsnorm takes any k up to 32768, any stride and any element-aligned address;
  * vq_rmsnorm_quant has the alignment rules of vq_quant_act, for x, res and h.
  * Launches one kernel; nothing is allocated.  Errors: INVALID_ARG, SHAPE, UNSUPPORTED
@@ -426,7 +427,7 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
  *   x          device dt [m x k], stride ldx (16-byte aligned, ldx % 8 == 0)
  *   y          device out_dt in {F16, BF16, F32}, [m x n], stride ldy
  * m is any number of rows (0 enqueues nothing), but the weights are read again for every
- * 4 to 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x stay
+ * 3 to 32 of them: past that vq_qgemm_dequant is the faster product.  Infinities and NaN in x stay
  * in their row, where an infinity meets a code as in the formula (a zero code gives NaN).
  * One kernel; nothing is allocated.
  * Errors: INVALID_ARG, SHAPE (k % group, alignment), UNSUPPORTED (group; of the product
