@@ -37,6 +37,7 @@ EXPORTS = (
     "vq_mx_gemm",
     "vq_mx_gemm_workspace_bytes", "vq_gemm_dense",
     "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts", "vq_gemm_dense_experts",
+    "vq_gated_norm", "vq_gated_norm_quant",
     "vq_calib_hist_bins", "vq_calib_static_scale", "vq_control_workspace_elems", "vq_step_control",
     "vq_status_string", "vq_last_hip_error", "vq_version",
 )
@@ -94,6 +95,9 @@ def _load():
         "vq_w4_gemv": (I, [P, I, I64, I64, I64, I64, P, P, I, P, I, I64, P]),
         "vq_qgemm_experts": (I, [P, P, P, I, P, P, I64, P, I64, I64, I64, I64, P, I, I64, P]),
         "vq_gemm_dense_experts": (I, [P, P, I, P, I64, P, I64, I64, I64, I64, I64, I64, I64, P, I, I64, P]),
+        "vq_gated_norm": (I, [P, P, I, I64, I64, I64, I64, I, P, I, D, P, I, P, I, D, P, I64, P, I64, P]),
+        "vq_gated_norm_quant": (I, [P, P, I, I64, I64, I64, I64, I, P, I, D, P, I, P, I, D, I, P, I, P, I32, P, P, P, P,
+                                    I64, P]),
         "vq_calib_hist_bins": (I64, []),
         "vq_calib_static_scale": (I, [P, I, I64, I64, I64, I, P, I32, P, P, P, P, P, P, P]),
         "vq_status_string": (ctypes.c_char_p, [I]),
@@ -920,6 +924,160 @@ def vq_gemm_dense_experts(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tenso
     return y
 
 
+# ------------------------------------------------------------------ gated norm
+
+VQ_NORM_NONE, VQ_NORM_RMS, VQ_NORM_LAYER = 0, 1, 2
+_NORM = {"rms": VQ_NORM_RMS, "layer": VQ_NORM_LAYER}
+_POST = {None: VQ_NORM_NONE, "none": VQ_NORM_NONE, **_NORM}
+
+
+class Modulation(ctypes.Structure):
+    """vq_modulation: rows of gate, scale and shift, and which of them each row takes."""
+    _fields_ = [("gate", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p),
+                ("ldg", ctypes.c_int64), ("ldsc", ctypes.c_int64), ("ldsh", ctypes.c_int64),
+                ("index", ctypes.c_void_p), ("sets", ctypes.c_int64), ("dt", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+def _modulation(gate, scale, shift, index, m, k, dt, device_index):
+    """The vq_modulation of tensors [sets x k], all of one shape, and type dt or float32; None without any."""
+    ptrs, lds, first = [], [], None
+    for t, name in ((gate, "gate"), (scale, "mod_scale"), (shift, "mod_shift")):
+        if t is None:
+            ptrs.append(None)
+            lds.append(k)
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device_index:
+            raise TypeError(f"{name} must be a CUDA (HIP) tensor on device {device_index}")
+        if first is None:
+            first = t
+            if t.dtype is not dt and t.dtype is not torch.float32:
+                raise TypeError(f"{name} must have dtype {dt} or torch.float32, not {t.dtype}")
+            if t.dim() != 2 or t.shape[1] != k or t.shape[0] < 1:
+                raise ValueError(f"{name} must be [sets x {k}]")
+        elif t.dtype is not first.dtype or t.shape != first.shape:
+            raise ValueError("gate, mod_scale and mod_shift must have one shape and dtype")
+        ld, unit = t.stride()
+        sets = t.shape[0]
+        if (k > 1 and unit != 1) or (sets > 1 and ld < k):
+            raise ValueError(f"{name} must have unit stride along its rows and a pitch of at least a row")
+        ptrs.append(t.data_ptr())
+        lds.append(ld if sets > 1 else k)
+    if first is None:
+        if index is not None:
+            raise ValueError("index goes with a gate, mod_scale or mod_shift")
+        return None
+    sets = first.shape[0]
+    i_ptr = None
+    if index is not None:
+        _dense(index, "index", device_index, _I32, m)
+        if index.numel() != m:
+            raise ValueError(f"index must hold {m} elements")
+        i_ptr = index.data_ptr()
+    elif m % sets:
+        raise ValueError(f"{m} rows do not split evenly over {sets} sets: pass index")
+    return Modulation(*ptrs, *lds, i_ptr, sets, _DT[first.dtype], 0)
+
+
+def _gated_operands(branch, residual, post, post_weight, branch_scale, gate, scale, shift, index, norm, weight, eps,
+                    sum_out):
+    ldh = _rows16(residual, "residual")
+    m, k = residual.shape
+    dt, dev = residual.dtype, residual.get_device()
+    post, norm = _POST.get(post, -1), _NORM.get(norm, -1)
+    if post < 0 or norm < 0:
+        raise ValueError("norm must be 'rms' or 'layer', post one of them or None")
+    w = []
+    for t, name in ((post_weight, "post_weight"), (weight, "weight")):
+        if t is None:
+            w.append((None, _DT[dt]))
+            continue
+        _dense(t, name, dev, (dt, torch.float32), k)
+        if t.numel() != k:
+            raise ValueError(f"{name} must hold {k} elements")
+        w.append((t.data_ptr(), _DT[t.dtype]))
+    y_ptr, ldy, s_ptr, lds = None, k, None, k
+    if branch is None:
+        if post != VQ_NORM_NONE or post_weight is not None or gate is not None or sum_out is not None:
+            raise ValueError("post, post_weight, gate and sum_out go with a branch")
+        sum_out = residual
+    else:
+        ldy = _rows16(branch, "branch", dev, dt)
+        if branch.shape != residual.shape:
+            raise ValueError("branch must have residual's shape")
+        if post == VQ_NORM_NONE and post_weight is not None:
+            raise ValueError("post_weight goes with post")
+        y_ptr = branch.data_ptr()
+        if sum_out is None:
+            sum_out = torch.empty(m, k, dtype=dt, device=residual.device)
+        else:
+            lds = _rows16(sum_out, "sum_out", dev, dt)
+            if sum_out.shape != residual.shape:
+                raise ValueError("sum_out must have residual's shape")
+        s_ptr = sum_out.data_ptr()
+    mod = _modulation(gate, scale, shift, index, m, k, dt, dev)
+    head = (y_ptr, residual.data_ptr(), _DT[dt], m, k, ldy, ldh, post, *w[0], branch_scale,
+            None if mod is None else ctypes.byref(mod), norm, *w[1], eps)
+    return m, k, dev, head, sum_out, s_ptr, lds
+
+
+def vq_gated_norm(branch: torch.Tensor | None, residual: torch.Tensor, weight: torch.Tensor | None = None,
+                  eps: float = 1e-6, norm: str = "rms", gate=None, branch_scale: float = 1.0, post: str | None = None,
+                  post_weight=None, mod_scale=None, mod_shift=None, index=None, y=None, sum_out=None):
+    """Between two blocks: s = residual + gate * branch_scale * post(branch), and the norm of s
+    times weight, times 1 + mod_scale, plus mod_shift.
+
+    norm, post: "rms" or "layer" (post None: the branch as it is).  gate, mod_scale and
+    mod_shift [sets x K], rows of any pitch: row i of M takes set index[i] (int32 [M]), or the
+    sets split the rows evenly.  branch None: only the norm, of the residual itself.
+    Returns (y, s), s in sum_out (it may be residual or branch)."""
+    m, k, dev, head, s, s_ptr, lds = _gated_operands(branch, residual, post, post_weight, branch_scale, gate,
+                                                     mod_scale, mod_shift, index, norm, weight, eps, sum_out)
+    if y is None:
+        y, ldn = torch.empty(m, k, dtype=residual.dtype, device=residual.device), k
+    else:
+        ldn = _rows16(y, "y", dev, residual.dtype)
+        if y.shape != residual.shape:
+            raise ValueError("y must have residual's shape")
+    _launch("vq_gated_norm", dev, *head, y.data_ptr(), ldn, s_ptr, lds)
+    return y, s
+
+
+def vq_gated_norm_quant(branch: torch.Tensor | None, residual: torch.Tensor, bits: int,
+                        weight: torch.Tensor | None = None, eps: float = 1e-6, norm: str = "rms", gate=None,
+                        branch_scale: float = 1.0, post: str | None = None, post_weight=None, mod_scale=None,
+                        mod_shift=None, index=None, gran: str = "token", idx: torch.Tensor | None = None,
+                        static_scale: torch.Tensor | None = None, bits_dev: torch.Tensor | None = None, codes=None,
+                        scales=None, sum_out=None):
+    """vq_gated_norm's rows as activation codes, quantized as vq_quant_act does (gran "token" or
+    "static").  Returns (codes int8 [M x kp], scales, s)."""
+    m, k, dev, head, s, s_ptr, lds = _gated_operands(branch, residual, post, post_weight, branch_scale, gate,
+                                                     mod_scale, mod_shift, index, norm, weight, eps, sum_out)
+    n_out = 0
+    if idx is not None:
+        n_out = int(idx.numel())
+        _dense(idx, "idx", dev, _I32, n_out)
+    parts = 2 if n_out else 1
+    if static_scale is not None:
+        _dense(static_scale, "static_scale", dev, _F32, parts)
+    if bits_dev is not None:
+        _dense(bits_dev, "bits_dev", dev, _I32, 1)
+    kp = vq_packed_k(k, n_out) if n_out else k
+    g = _GRAN.get(gran, -1)
+    if codes is None:
+        codes = torch.empty(m, kp, dtype=torch.int8, device=residual.device)
+    else:
+        _dense(codes, "codes", dev, (torch.int8,), m * kp)
+    if scales is None:
+        shape = ((m, 2) if n_out else (m,)) if g == VQ_PER_TOKEN else (parts,)
+        scales = torch.empty(*shape, dtype=torch.float32, device=residual.device)
+    else:
+        _dense(scales, "scales", dev, _F32, (m if g == VQ_PER_TOKEN else 1) * parts)
+    _launch("vq_gated_norm_quant", dev, *head, bits, _ptr(bits_dev), g, _ptr(idx), n_out, _ptr(static_scale),
+            codes.data_ptr(), scales.data_ptr(), s_ptr, lds)
+    return codes, scales, s
+
+
 # ------------------------------------------------------------------ prepared calls
 
 # Entry points that only enqueue work on a stream (their last argument).
@@ -928,7 +1086,7 @@ _LAUNCHES = frozenset((
     "vq_route_rel_l1", "vq_quant_residual", "vq_qgemm_dequant_residual", "vq_mx_quant", "vq_mx_quant_rotated",
     "vq_mx_gemm", "vq_gemm_dense", "vq_calib_static_scale", "vq_step_control",
     "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts",
-    "vq_gemm_dense_experts",
+    "vq_gemm_dense_experts", "vq_gated_norm", "vq_gated_norm_quant",
 ))
 
 

@@ -26,12 +26,10 @@
 
 #include "dev_common.h"
 #include "gemm_common.h"
+#include "rows_common.h"
 #include "vq_internal.h"
 
 namespace vqk {
-
-typedef u4v u4v_el __attribute__((aligned(2)));
-typedef v4f v4f_el __attribute__((aligned(4)));
 
 struct NormArgs {
   const uint16_t* x;
@@ -50,31 +48,6 @@ struct NormArgs {
   int k, kp, w_f32, qbits, n_out, p1;
 };
 
-// Wave-wide sum in float64: four steps of register moves inside the rows of 16 lanes, then the
-// four rows from scalar registers.
-template <int CTRL>
-__device__ __forceinline__ double dpp_d(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
-}
-__device__ __forceinline__ double lane_d(double v, int l) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
-  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
-}
-__device__ __forceinline__ double wave_sum_dpp(double v) {
-  v += dpp_d<0xB1>(v);   // quad_perm [1,0,3,2]
-  v += dpp_d<0x4E>(v);   // quad_perm [2,3,0,1]
-  v += dpp_d<0x141>(v);  // row_half_mirror
-  v += dpp_d<0x140>(v);  // row_mirror
-  return (lane_d(v, 0) + lane_d(v, 16)) + (lane_d(v, 32) + lane_d(v, 48));
-}
-
-// Eight elements at any element's address; TINY: the row has only cnt < 8; NT: past the cache.
-//
 // What goes past the cache.  The sum, always: nobody reads it before the product has run (4113 x 4096
 // to 16 bits 23.3 -> 21.6 us with buffers in use again, 8000 x 5760 to codes 69.7 -> 66.0; even also
 // where the next call's residual is this one's sum).  x and the residual, read once, where the call's
@@ -82,31 +55,7 @@ __device__ __forceinline__ double wave_sum_dpp(double v) {
 // product that reads the codes, 1920 -> 5760, 254 -> 245; but what the layer before left in that cache
 // should be found there (4113 x 4096 21.6, past it 26.0), and outlier channels are read twice.  Never what
 // the product reads next: codes sent past it made 64 rows of 4096 with their product 19.6 -> 22.2 us.
-template <bool TINY, bool NT>
-__device__ __forceinline__ u4v load8(const uint16_t* p, int cnt) {
-  if constexpr (!TINY && NT) return __builtin_nontemporal_load(reinterpret_cast<const u4v_el*>(p));
-  if constexpr (!TINY) return *reinterpret_cast<const u4v_el*>(p);
-  u4v v = {0u, 0u, 0u, 0u};
-  for (int i = 0; i < 8; ++i)
-    if (i < cnt) v[i >> 1] |= (unsigned)p[i] << (16 * (i & 1));
-  return v;
-}
-template <bool TINY, bool NT>
-__device__ __forceinline__ void store8(uint16_t* p, const u4v& v, int cnt) {
-  if constexpr (!TINY && NT) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u4v_el*>(p));
-  } else if constexpr (!TINY) {
-    *reinterpret_cast<u4v_el*>(p) = v;
-  } else {
-    for (int i = 0; i < 8; ++i)
-      if (i < cnt) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-  }
-}
-
-// How K ends: a multiple of 8; a last piece that starts early enough to end with the row, its
-// first elements counted by their own piece; or fewer than 8 elements in all.
-enum : int { END_WHOLE = 0, END_OVERLAP = 1, END_TINY = 2 };
-
+//
 // QUANT: codes and scales instead of y.  PAST: x and the residual past the cache.  T threads a row.
 template <int DT, bool RES, bool QUANT, bool DUAL, int END, int NP, bool PAST = false>
 __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a, int T) {
@@ -383,7 +332,7 @@ static void launch_norm_np(const NormArgs& a, int np, int grid, int block, int T
     case 1: hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 1>), dim3(grid), dim3(block), 0, st, a, T); break;
     case 2: hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 2>), dim3(grid), dim3(block), 0, st, a, T); break;
     default:
-      // Above three quarters of the 256 MiB last-level cache: load8.
+      // Above three quarters of the 256 MiB last-level cache: see above the kernel.
       if (!DUAL && a.rows * a.k * (2 + 2 * RES + 2 * (a.h != nullptr) + (QUANT ? 1 : 2)) > ((int64_t)192 << 20))
         hipLaunchKernelGGL((k_rmsnorm<DT, RES, QUANT, DUAL, END, 4, !DUAL>), dim3(grid), dim3(block), 0, st, a, T);
       else

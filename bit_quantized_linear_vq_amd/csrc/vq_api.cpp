@@ -525,6 +525,128 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
   return hip_status(vq_internal::launch_norm(p, stream));
 }
 
+// ------------------------------------------------------------------ gated norm
+
+namespace {
+static_assert(sizeof(vq_modulation) == 72 && offsetof(vq_modulation, sets) == 56 && offsetof(vq_modulation, dt) == 64,
+              "vq_modulation layout is part of the ABI");
+
+// The gate's, scale's and shift's rows over m rows of k elements of type dt.
+vq_status check_modulation(const vq_modulation* mod, vq_dtype dt, int64_t m, int64_t k, vq_internal::ModParams& p) {
+  p = vq_internal::ModParams{};
+  p.sets = 1;
+  if (!mod || (!mod->gate && !mod->scale && !mod->shift)) return VQ_OK;
+  if (mod->dt != (int)dt && mod->dt != VQ_F32) return VQ_ERR_INVALID_ARG;
+  if (mod->sets < 1 || mod->sets >= kMaxDim) return VQ_ERR_INVALID_ARG;
+  if ((mod->gate && mod->ldg < k) || (mod->scale && mod->ldsc < k) || (mod->shift && mod->ldsh < k))
+    return VQ_ERR_INVALID_ARG;
+  const uintptr_t el = mod->dt == VQ_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(mod->gate) % el || reinterpret_cast<uintptr_t>(mod->scale) % el ||
+      reinterpret_cast<uintptr_t>(mod->shift) % el || reinterpret_cast<uintptr_t>(mod->index) % 4 ||
+      (!mod->index && m % mod->sets))
+    return VQ_ERR_SHAPE;
+  p.gate = mod->gate;
+  p.scale = mod->scale;
+  p.shift = mod->shift;
+  p.ldg = mod->ldg;
+  p.ldsc = mod->ldsc;
+  p.ldsh = mod->ldsh;
+  p.index = mod->index;
+  p.sets = mod->sets;
+  p.f32 = mod->dt == VQ_F32;
+  return VQ_OK;
+}
+
+vq_status check_gated(const void* y, const void* h, vq_dtype dt, int64_t m, int64_t k, int64_t ldy, int64_t ldh,
+                      vq_norm post, const void* post_weight, vq_dtype post_w_dt, double branch_scale,
+                      const vq_modulation* mod, vq_norm norm, const void* weight, vq_dtype w_dt, double eps,
+                      const void* sum, int64_t lds, vq_internal::GatedNormParams& p) {
+  if (m < 0 || k < 1 || m >= kMaxDim || k >= kMaxDim || !is_16bit(dt)) return VQ_ERR_INVALID_ARG;
+  if ((weight && w_dt != dt && w_dt != VQ_F32) || (post_weight && post_w_dt != dt && post_w_dt != VQ_F32))
+    return VQ_ERR_INVALID_ARG;
+  if (norm != VQ_NORM_RMS && norm != VQ_NORM_LAYER) return VQ_ERR_INVALID_ARG;
+  if (post != VQ_NORM_NONE && post != VQ_NORM_RMS && post != VQ_NORM_LAYER) return VQ_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.0 || !std::isfinite((float)branch_scale)) return VQ_ERR_INVALID_ARG;
+  if (m > 0 && (!h || (y && !sum))) return VQ_ERR_INVALID_ARG;
+  if (m > 0 && !y && (sum || post != VQ_NORM_NONE || (mod && mod->gate))) return VQ_ERR_INVALID_ARG;
+  if (post == VQ_NORM_NONE && post_weight) return VQ_ERR_INVALID_ARG;
+  if (ldh < k || (y && ldy < k) || (sum && lds < k)) return VQ_ERR_INVALID_ARG;
+  if (k > vq_internal::norm_max_k()) return VQ_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(y) % 2 || reinterpret_cast<uintptr_t>(h) % 2 || reinterpret_cast<uintptr_t>(sum) % 2 ||
+      reinterpret_cast<uintptr_t>(weight) % (w_dt == VQ_F32 ? 4 : 2) ||
+      reinterpret_cast<uintptr_t>(post_weight) % (post_w_dt == VQ_F32 ? 4 : 2))
+    return VQ_ERR_SHAPE;
+  vq_status s = check_modulation(mod, dt, m, k, p.mod);
+  if (s != VQ_OK) return s;
+  p.y = y;
+  p.h = h;
+  p.dtype = (int)dt;
+  p.rows = m;
+  p.k = k;
+  p.ldy = ldy;
+  p.ldh = ldh;
+  p.post = (int)post;
+  p.norm = (int)norm;
+  p.pw = post_weight;
+  p.w = weight;
+  p.pw_f32 = post_w_dt == VQ_F32;
+  p.w_f32 = w_dt == VQ_F32;
+  p.alpha = (float)branch_scale;
+  p.eps = eps;
+  p.s = const_cast<void*>(sum);
+  p.lds = lds;
+  return VQ_OK;
+}
+}  // namespace
+
+vq_status vq_gated_norm(const void* y, const void* h, vq_dtype dt, int64_t m, int64_t k, int64_t ldy, int64_t ldh,
+                        vq_norm post, const void* post_weight, vq_dtype post_w_dt, double branch_scale,
+                        const vq_modulation* mod, vq_norm norm, const void* weight, vq_dtype w_dt, double eps,
+                        void* n, int64_t ldn, void* sum, int64_t lds, hipStream_t stream) {
+  vq_internal::GatedNormParams p{};
+  vq_status s = check_gated(y, h, dt, m, k, ldy, ldh, post, post_weight, post_w_dt, branch_scale, mod, norm, weight,
+                            w_dt, eps, sum, lds, p);
+  if (s != VQ_OK) return s;
+  if ((m > 0 && !n) || ldn < k) return VQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(n) % 2) return VQ_ERR_SHAPE;
+  if (m == 0) return VQ_OK;
+  p.n = n;
+  p.ldn = ldn;
+  return hip_status(vq_internal::launch_gated_norm(p, stream));
+}
+
+vq_status vq_gated_norm_quant(const void* y, const void* h, vq_dtype dt, int64_t m, int64_t k, int64_t ldy,
+                              int64_t ldh, vq_norm post, const void* post_weight, vq_dtype post_w_dt,
+                              double branch_scale, const vq_modulation* mod, vq_norm norm, const void* weight,
+                              vq_dtype w_dt, double eps, int bits, const int32_t* bits_dev, vq_gran gran,
+                              const int32_t* idx_dev, int32_t n_out, const float* static_scale_dev, int8_t* codes,
+                              float* scales, void* sum, int64_t lds, hipStream_t stream) {
+  vq_internal::GatedNormParams p{};
+  vq_status s = check_gated(y, h, dt, m, k, ldy, ldh, post, post_weight, post_w_dt, branch_scale, mod, norm, weight,
+                            w_dt, eps, sum, lds, p);
+  if (s != VQ_OK) return s;
+  if (m > 0 && (!codes || !scales)) return VQ_ERR_INVALID_ARG;
+  if (n_out < 0 || (n_out > 0 && !idx_dev)) return VQ_ERR_INVALID_ARG;
+  if (gran != VQ_PER_TENSOR && gran != VQ_PER_TOKEN && gran != VQ_PER_TENSOR_STATIC) return VQ_ERR_INVALID_ARG;
+  if (gran == VQ_PER_TENSOR_STATIC && !static_scale_dev) return VQ_ERR_INVALID_ARG;
+  if (gran == VQ_PER_TENSOR || !ok_bits(bits)) return VQ_ERR_UNSUPPORTED;
+  if (n_out > VQ_MAX_OUTLIERS || n_out >= k) return VQ_ERR_UNSUPPORTED;
+  if (k % VQ_K_ALIGN) return VQ_ERR_SHAPE;
+  if (!aligned16(h) || ldh % 8 || !aligned16(codes)) return VQ_ERR_SHAPE;
+  if (y && (!aligned16(y) || ldy % 8 || !aligned16(sum) || lds % 8)) return VQ_ERR_SHAPE;
+  if (m == 0) return VQ_OK;
+  p.codes = codes;
+  p.scales = scales;
+  p.bits = bits;
+  p.bits_dev = bits_dev;
+  p.idx = idx_dev;
+  p.n_out = n_out;
+  p.p1 = (int)part_len(n_out);
+  p.kp = k + part_len(n_out);
+  p.static_scale = gran == VQ_PER_TENSOR_STATIC ? static_scale_dev : nullptr;
+  return hip_status(vq_internal::launch_gated_norm(p, stream));
+}
+
 // ------------------------------------------------------------------ group-scaled 4-bit weights
 
 namespace {

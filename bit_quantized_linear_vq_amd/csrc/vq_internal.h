@@ -118,6 +118,43 @@ struct NormParams {
 int norm_max_k();
 hipError_t launch_norm(const NormParams& p, hipStream_t st);
 
+// Rows of modulation (vq_modulation): sets >= 1, and without an index rows % sets == 0.
+struct ModParams {
+  const void* gate;
+  const void* scale;
+  const void* shift;
+  int64_t ldg, ldsc, ldsh;
+  const int32_t* index;
+  int64_t sets;
+  int f32;  // in float32 instead of the rows' type
+};
+struct GatedNormParams {
+  const void* y;  // or nullptr
+  const void* h;
+  int dtype;  // 0 f16, 1 bf16
+  int64_t rows, k, ldy, ldh;
+  int post, norm;  // vq_norm
+  const void* pw;
+  const void* w;
+  int pw_f32, w_f32;
+  float alpha;
+  ModParams mod;
+  double eps;
+  void* s;
+  int64_t lds;
+  void* n;  // 16-bit output, or nullptr with codes
+  int64_t ldn;
+  int8_t* codes;
+  float* scales;
+  int bits;
+  const int32_t* bits_dev;
+  const int32_t* idx;
+  int n_out, p1;
+  int64_t kp;
+  const float* static_scale;
+};
+hipError_t launch_gated_norm(const GatedNormParams& p, hipStream_t st);
+
 hipError_t launch_pack_group(const void* w, int dtype, int64_t n, int64_t k, int64_t ldw, int group, uint8_t* codes,
                              void* scales, hipStream_t st);
 struct W4GemvParams {

@@ -407,6 +407,65 @@ vq_status vq_rmsnorm_quant(const void* x, const void* res, vq_dtype dt, int64_t 
                            hipStream_t stream);
 
 /*
+ * Norms before and after a block, fused with its gate and residual scale: what stands
+ * between the last product of one block and the first of the next.
+ *   u = y                                                     post VQ_NORM_NONE
+ *   u = fl32(fl32(fl32(y - mean_y) * rstd_y) * post_weight)   the branch's own norm
+ *   s = RNE_dt(fl32(h + fl32(u * fl32(gate * branch_scale)))) kept for the residual stream
+ *   v = fl32(fl32(fl32(s - mean_s) * rstd_s) * weight)
+ *   v = fl32(fl32(v * fl32(1 + scale)) + shift)
+ * mean is fl32(sum x / k) for VQ_NORM_LAYER and 0 for VQ_NORM_RMS, rstd = fl32(1 / sqrt(
+ * sum x^2 / k - (sum x / k)^2 + eps)) (without the mean for VQ_NORM_RMS), both from float64
+ * sums.  vq_gated_norm stores n = RNE_dt(v); vq_gated_norm_quant stores the codes and scales
+ * of v, exactly as vq_quant_act derives them from its x.
+ *   y          device, dt in {F16, BF16}, [m x k], stride ldy, or NULL: no branch, s = h (and
+ *              then no sum, no post norm and no gate)
+ *   h          device dt [m x k], stride ldh: the residual stream
+ *   post_weight, weight   device [k] of post_w_dt, w_dt (dt or F32), or NULL for ones
+ *   branch_scale   finite, rounded to float32
+ *   mod        host, read during the call, or NULL: no gate (1), scale (0) and shift (0)
+ *   eps        finite, >= 0, of both norms
+ *   sum        device dt [m x k], stride lds: receives s.  It may be h or y itself (same pointer
+ *              and stride); no other overlap of inputs and outputs.  NULL without a branch
+ *   n          device dt [m x k], stride ldn
+ *   bits, bits_dev, gran, idx_dev, n_out, static_scale_dev, codes, scales: as for vq_rmsnorm_quant
+ * The rows of a vq_modulation: gate, scale and shift are each [sets x k] of dt (strides ldg,
+ * ldsc, ldsh; parts of one wider tensor, say) or NULL, and row i of the operands takes set
+ * index[i], or set i / (m / sets) without an index (m % sets == 0).  A row whose index lies
+ * outside [0, sets) has no branch (s = h exactly), no scale and no shift.
+ * m = 0 enqueues nothing.  An infinity or NaN among a row's values v makes its dynamic scales
+ * NaN (the codes are then unspecified).  With eps = 0 a row without deviation has an infinite
+ * rstd, and NaN outputs.
+ * vq_gated_norm takes any k up to 32768, any stride and any element-aligned address;
+ * vq_gated_norm_quant has the alignment rules of vq_quant_act, for y, h and sum.
+ * Launches one kernel; nothing is allocated.  Errors: INVALID_ARG, SHAPE, UNSUPPORTED
+ * (k > 32768, gran VQ_PER_TENSOR, bits, n_out as for vq_quant_act).
+ */
+typedef enum vq_norm { VQ_NORM_NONE = 0, VQ_NORM_RMS = 1, VQ_NORM_LAYER = 2 } vq_norm;
+
+typedef struct vq_modulation {
+  const void* gate;
+  const void* scale;
+  const void* shift;
+  int64_t ldg, ldsc, ldsh;
+  const int32_t* index;
+  int64_t sets;
+  int32_t dt; /* vq_dtype: the operands' or VQ_F32 */
+  int32_t reserved;
+} vq_modulation;
+
+vq_status vq_gated_norm(const void* y, const void* h, vq_dtype dt, int64_t m, int64_t k, int64_t ldy, int64_t ldh,
+                        vq_norm post, const void* post_weight, vq_dtype post_w_dt, double branch_scale,
+                        const vq_modulation* mod, vq_norm norm, const void* weight, vq_dtype w_dt, double eps,
+                        void* n, int64_t ldn, void* sum, int64_t lds, hipStream_t stream);
+vq_status vq_gated_norm_quant(const void* y, const void* h, vq_dtype dt, int64_t m, int64_t k, int64_t ldy,
+                              int64_t ldh, vq_norm post, const void* post_weight, vq_dtype post_w_dt,
+                              double branch_scale, const vq_modulation* mod, vq_norm norm, const void* weight,
+                              vq_dtype w_dt, double eps, int bits, const int32_t* bits_dev, vq_gran gran,
+                              const int32_t* idx_dev, int32_t n_out, const float* static_scale_dev, int8_t* codes,
+                              float* scales, void* sum, int64_t lds, hipStream_t stream);
+
+/*
  * 4-bit weights with a scale for each group of `group` consecutive input channels, and
  * their product with a few unquantized rows: the layer's form for single tokens, which is
  * bound by the weights' bytes, so the activations stay at 16 bits.

@@ -37,7 +37,9 @@ Steps and the passages they follow:
 * ``norm``      root-mean-square norm with the residual's addition, as 16-bit rows or codes.
 * ``group4``    4-bit weights with group scales and their product with a few 16-bit rows.
 * ``experts``   products of several experts over rows sorted by expert.
+* ``gated``     norms before and after a block with its gate and residual scale.
 """
 from . import (  # noqa: F401
     numerics, detect, quantizer, fwht, gemm, route, linear, decompose, mx, calib, control, dense, norm, group4, experts,
+    gated,
 )

@@ -1,0 +1,85 @@
+"""C-ABI checks, without a GPU, of the operators between the layers of a block: invalid arguments
+get the documented status before any HIP call, and calls with no rows return without one."""
+import ctypes
+import os
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "bit_quantized_linear_vq_amd", "libvq.so")
+
+# The calls pass a fake device address to entry points that must reject them: only where no
+# GPU could be reached by one that does not.
+pytestmark = [
+    pytest.mark.skipif(not os.path.exists(LIB), reason="libvq.so not built"),
+    pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="a GPU is present: fake device addresses must not reach it"),
+]
+
+OK, INVALID, SHAPE, UNSUP, HIP = range(5)
+F16, BF16, F32 = 0, 1, 2
+FAKE, ODD, BYTE = 0x10000, 0x10008, 0x10001
+NULL = None
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def vq():
+    import bit_quantized_linear_vq_amd as m
+    return m
+
+
+GATED = dict(y=FAKE, h=FAKE, dt=BF16, m=4, k=128, ldy=128, ldh=128, post=1, pw=FAKE, pwdt=F32, alpha=1.0, gate=FAKE,
+             scale=FAKE, shift=FAKE, ldg=128, ldsc=128, ldsh=128, index=NULL, sets=2, mdt=F32, norm=2, w=FAKE, wdt=BF16,
+             eps=1e-6, n=FAKE, ldn=128, s=FAKE, lds=128, mod=True)
+
+
+def head(vq, a):
+    mod = vq.Modulation(a["gate"], a["scale"], a["shift"], a["ldg"], a["ldsc"], a["ldsh"], a["index"], a["sets"], a["mdt"], 0)
+    return (a["y"], a["h"], a["dt"], a["m"], a["k"], a["ldy"], a["ldh"], a["post"], a["pw"], a["pwdt"], a["alpha"],
+            ctypes.byref(mod) if a["mod"] else None, a["norm"], a["w"], a["wdt"], a["eps"])
+
+
+def gated(vq, **kw):
+    a = {**GATED, **kw}
+    return vq._lib.vq_gated_norm(*head(vq, a), a["n"], a["ldn"], a["s"], a["lds"], NULL)
+
+
+NO_BRANCH = dict(y=NULL, s=NULL, post=0, pw=NULL, gate=NULL)
+BAD_GATED = [
+    (dict(h=NULL), INVALID), (dict(s=NULL), INVALID), (dict(dt=F32), INVALID), (dict(m=-1), INVALID), (dict(k=0), INVALID),
+    (dict(ldy=127), INVALID), (dict(ldh=64), INVALID), (dict(lds=127), INVALID), (dict(pwdt=F16), INVALID),
+    (dict(wdt=F16), INVALID), (dict(norm=0), INVALID), (dict(norm=3), INVALID), (dict(post=5), INVALID),
+    (dict(post=0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=NAN), INVALID), (dict(alpha=INF), INVALID),
+    (dict(alpha=NAN), INVALID), (dict(alpha=1e300), INVALID), (dict(mdt=F16), INVALID), (dict(sets=0), INVALID),
+    (dict(sets=-2), INVALID), (dict(ldg=127), INVALID), (dict(ldsc=127), INVALID), (dict(ldsh=0), INVALID),
+    ({**NO_BRANCH, "s": FAKE}, INVALID), ({**NO_BRANCH, "post": 1}, INVALID), ({**NO_BRANCH, "gate": FAKE}, INVALID),
+    ({**NO_BRANCH, "pw": FAKE}, INVALID),
+    (dict(sets=3), SHAPE), (dict(gate=0x10002), SHAPE), (dict(scale=BYTE, mdt=BF16), SHAPE), (dict(shift=0x10003), SHAPE),
+    (dict(index=0x10002), SHAPE), (dict(h=BYTE), SHAPE), (dict(y=BYTE), SHAPE), (dict(s=BYTE), SHAPE),
+    (dict(w=BYTE), SHAPE), (dict(pw=0x10002), SHAPE),
+]
+
+
+@pytest.mark.parametrize("kw,want", BAD_GATED + [
+    (dict(n=NULL), INVALID), (dict(ldn=100), INVALID), (dict(n=BYTE), SHAPE),
+    (dict(k=32769, ldy=32769, ldh=32769, ldn=32769, lds=32769), UNSUP),
+    (dict(m=0), OK), (dict(m=0, y=NULL, h=NULL, n=NULL, s=NULL, mod=False, post=0, pw=NULL), OK),
+])
+def test_gated_norm_validation(vq, kw, want):
+    assert gated(vq, **kw) == want
+
+
+def gatedq(vq, **kw):
+    a = {**GATED, **dict(bits=8, bits_dev=NULL, gran=1, idx=NULL, n_out=0, st=NULL, codes=FAKE, scales=FAKE), **kw}
+    return vq._lib.vq_gated_norm_quant(*head(vq, a), a["bits"], a["bits_dev"], a["gran"], a["idx"], a["n_out"], a["st"],
+                                       a["codes"], a["scales"], a["s"], a["lds"], NULL)
+
+
+@pytest.mark.parametrize("kw,want", BAD_GATED + [
+    (dict(codes=NULL), INVALID), (dict(scales=NULL), INVALID), (dict(n_out=-1), INVALID), (dict(n_out=2), INVALID),
+    (dict(gran=5), INVALID), (dict(gran=2), INVALID), (dict(gran=0), UNSUP), (dict(bits=5), UNSUP),
+    (dict(idx=FAKE, n_out=128), UNSUP), (dict(k=100), SHAPE), (dict(h=ODD), SHAPE), (dict(y=ODD), SHAPE), (dict(s=ODD), SHAPE),
+    (dict(codes=ODD), SHAPE), (dict(ldy=130), SHAPE), (dict(ldh=132), SHAPE), (dict(lds=129), SHAPE), (dict(m=0), OK),
+])
+def test_gated_norm_quant_validation(vq, kw, want):
+    assert gatedq(vq, **kw) == want
