@@ -37,7 +37,7 @@ EXPORTS = (
     "vq_mx_gemm",
     "vq_mx_gemm_workspace_bytes", "vq_gemm_dense",
     "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts", "vq_gemm_dense_experts",
-    "vq_gated_norm", "vq_gated_norm_quant",
+    "vq_gated_norm", "vq_gated_norm_quant", "vq_route_experts_workspace_elems", "vq_route_experts", "vq_combine_experts",
     "vq_calib_hist_bins", "vq_calib_static_scale", "vq_control_workspace_elems", "vq_step_control",
     "vq_status_string", "vq_last_hip_error", "vq_version",
 )
@@ -98,6 +98,9 @@ def _load():
         "vq_gated_norm": (I, [P, P, I, I64, I64, I64, I64, I, P, I, D, P, I, P, I, D, P, I64, P, I64, P]),
         "vq_gated_norm_quant": (I, [P, P, I, I64, I64, I64, I64, I, P, I, D, P, I, P, I, D, I, P, I, P, I32, P, P, P, P,
                                     I64, P]),
+        "vq_route_experts_workspace_elems": (I64, [I64, I64]),
+        "vq_route_experts": (I, [P, I, I64, I64, I64, I, P, I, I, I, I, I, D, P, P, P, P, P, P, P]),
+        "vq_combine_experts": (I, [P, I, I64, I64, P, P, I64, I64, I, P, I64, P, P, I, I64, P]),
         "vq_calib_hist_bins": (I64, []),
         "vq_calib_static_scale": (I, [P, I, I64, I64, I64, I, P, I32, P, P, P, P, P, P, P]),
         "vq_status_string": (ctypes.c_char_p, [I]),
@@ -1078,6 +1081,112 @@ def vq_gated_norm_quant(branch: torch.Tensor | None, residual: torch.Tensor, bit
     return codes, scales, s
 
 
+# ------------------------------------------------------------------ routing to experts
+
+VQ_SCORE_SOFTMAX, VQ_SCORE_SIGMOID = 0, 1
+_SCORE = {"softmax": VQ_SCORE_SOFTMAX, "sigmoid": VQ_SCORE_SIGMOID}
+_ANY = (torch.float16, torch.bfloat16, torch.float32)
+
+
+def _rows_any(t, name, index, dtypes):
+    """_rows16 for other types: a 2-D device tensor with unit stride along its rows.  Returns the pitch."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or (index is not None and t.get_device() != index):
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor{'' if index is None else f' on device {index}'}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    m, k = t.shape
+    ld, unit = t.stride()
+    if (k > 1 and unit != 1) or (m > 1 and ld < k):
+        raise ValueError(f"{name} must have unit stride along its rows and a pitch of at least a row")
+    return ld if m > 1 else k
+
+
+@functools.lru_cache(maxsize=1024)
+def vq_route_experts_workspace_elems(m: int, experts: int) -> int:
+    """Int32 elements of the scratch that vq_route_experts needs for m rows."""
+    return int(_lib.vq_route_experts_workspace_elems(m, experts))
+
+
+def vq_route_experts(scores: torch.Tensor, top: int, score: str = "softmax", bias=None, groups: int = 1,
+                     top_groups: int | None = None, group_best: int = 1, renorm: bool = True, scale: float = 1.0,
+                     offsets=None, rows=None, weights=None, experts=None, place=None, ws=None):
+    """The router's scores [M x E] to the rows sorted by expert: `top` experts for each token.
+
+    score: "softmax" or "sigmoid".  bias (float32 [E]) is added for the choice only.  groups,
+    top_groups, group_best: only the experts of the top_groups groups (default all) whose best one
+    or two sum highest.  Scores of -inf close an expert to a token.  Returns (offsets int32 [E + 1],
+    rows int32 [M * top], weights float32 [M x top], experts int32 [M x top], place int32 [M x top]):
+    offsets and rows as the experts' products take them, place and weights as vq_combine_experts does."""
+    ldx = _rows_any(scores, "scores", None, _ANY)
+    m, e = scores.shape
+    dev, device = scores.get_device(), scores.device
+    top = int(top)
+    if score not in _SCORE:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if bias is not None:
+        _dense(bias, "bias", dev, _F32, e)
+        if bias.numel() != e:
+            raise ValueError(f"bias must hold {e} elements")
+    if not 1 <= top <= e:
+        raise ValueError(f"top must be from 1 to {e}")
+    outs = []
+    for t, name, dt, shape in ((offsets, "offsets", torch.int32, (e + 1,)), (rows, "rows", torch.int32, (m * top,)),
+                               (weights, "weights", torch.float32, (m, top)), (experts, "experts", torch.int32, (m, top)),
+                               (place, "place", torch.int32, (m, top))):
+        if t is None:
+            t = torch.empty(shape, dtype=dt, device=device)
+        else:
+            _dense(t, name, dev, (dt,), 0)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        outs.append(t)
+    need = vq_route_experts_workspace_elems(m, e)
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.int32, device=device)
+    else:
+        _dense(ws, "ws", dev, _I32, need)
+    _launch("vq_route_experts", dev, scores.data_ptr(), _DT[scores.dtype], m, e, ldx, _SCORE[score], _ptr(bias), groups,
+            groups if top_groups is None else top_groups, group_best, top, int(bool(renorm)), scale,
+            *[t.data_ptr() for t in outs], ws.data_ptr())
+    return tuple(outs)
+
+
+def vq_combine_experts(y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, residual=None, gate=None, index=None,
+                       out_dtype=None, out=None):
+    """The experts' rows y [T x N] back to their tokens: residual + gate * sum_j weights[:, j] * y[place[:, j]].
+
+    place (int32) and weights (float32) [M x top] as vq_route_experts returns them; gate [sets x N] and
+    index as vq_gated_norm takes them.  out_dtype defaults to the residual's, or y's; out may be the
+    residual.  Returns out [M x N]."""
+    ldy = _rows_any(y, "y", None, _ANY)
+    t, n = y.shape
+    dev = y.get_device()
+    _dense(place, "place", dev, _I32, 0)
+    _dense(weights, "weights", dev, _F32, 0)
+    if place.dim() != 2 or place.shape != weights.shape or not place.shape[1]:
+        raise ValueError("place and weights must both be [M x top]")
+    m, top = place.shape
+    ldr = n
+    if residual is not None:
+        ldr = _rows_any(residual, "residual", dev, _ANY)
+        if residual.shape != (m, n):
+            raise ValueError(f"residual must be [{m} x {n}]")
+    if out is None:
+        out, ldo = torch.empty(m, n, dtype=out_dtype or (y if residual is None else residual).dtype, device=y.device), n
+    else:
+        ldo = _rows_any(out, "out", dev, _ANY)
+        if out.shape != (m, n):
+            raise ValueError(f"out must be [{m} x {n}]")
+    if out.dtype not in _ANY or (residual is not None and residual.dtype is not out.dtype):
+        raise TypeError("out must have the residual's dtype")
+    mod = _modulation(gate, None, None, index, m, n, y.dtype if y.dtype in _HALF else out.dtype, dev)
+    _launch("vq_combine_experts", dev, y.data_ptr(), _DT[y.dtype], t, ldy, place.data_ptr(), weights.data_ptr(), m, n, top,
+            _ptr(residual), ldr, None if mod is None else ctypes.byref(mod), out.data_ptr(), _DT[out.dtype], ldo)
+    return out
+
+
 # ------------------------------------------------------------------ prepared calls
 
 # Entry points that only enqueue work on a stream (their last argument).
@@ -1087,6 +1196,7 @@ _LAUNCHES = frozenset((
     "vq_mx_gemm", "vq_gemm_dense", "vq_calib_static_scale", "vq_step_control",
     "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts",
     "vq_gemm_dense_experts", "vq_gated_norm", "vq_gated_norm_quant",
+    "vq_route_experts", "vq_combine_experts",
 ))
 
 

@@ -768,6 +768,89 @@ vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const
   return hip_status(vq_internal::launch_experts(p, stream));
 }
 
+// ------------------------------------------------------------------ routing to experts
+
+namespace {
+constexpr int kMaxTop = 32, kMaxGroups = 64;
+bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+}  // namespace
+
+int64_t vq_route_experts_workspace_elems(int64_t m, int64_t experts) {
+  if (m < 0 || m > kMaxExpertRows || experts < 1 || experts > kMaxExperts) return 0;
+  return std::max<int64_t>(1, vq_internal::route_experts_blocks(m) * experts);
+}
+
+vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t experts, int64_t ldx, vq_score score,
+                           const float* bias, int groups, int top_groups, int group_best, int top, int renorm,
+                           double scale, int32_t* offsets, int32_t* rows, float* weights, int32_t* chosen,
+                           int32_t* place, int32_t* ws, hipStream_t stream) {
+  if (!valid_dt(dt) || m < 0 || experts < 1 || ldx < experts || top < 1) return VQ_ERR_INVALID_ARG;
+  if (score != VQ_SCORE_SOFTMAX && score != VQ_SCORE_SIGMOID) return VQ_ERR_INVALID_ARG;
+  if (!offsets || !ws || (m > 0 && (!x || !rows || !weights || !chosen || !place))) return VQ_ERR_INVALID_ARG;
+  if (groups < 1 || experts % groups || top_groups < 1 || top_groups > groups) return VQ_ERR_INVALID_ARG;
+  if (group_best < 1 || group_best > 2 || group_best > experts / groups) return VQ_ERR_INVALID_ARG;
+  if (top > experts / groups * top_groups || !std::isfinite((float)scale)) return VQ_ERR_INVALID_ARG;
+  if (experts > kMaxExperts || top > kMaxTop || groups > kMaxGroups || m > kMaxExpertRows / top)
+    return VQ_ERR_UNSUPPORTED;
+  if (misaligned(x, elem_size(dt)) || misaligned(bias, 4) || misaligned(offsets, 4) || misaligned(rows, 4) ||
+      misaligned(weights, 4) || misaligned(chosen, 4) || misaligned(place, 4) || misaligned(ws, 4))
+    return VQ_ERR_SHAPE;
+  vq_internal::RouteExpertsParams p{};
+  p.x = x;
+  p.dtype = (int)dt;
+  p.bias = bias;
+  p.ldx = ldx;
+  p.rows = m;
+  p.experts = (int)experts;
+  p.top = top;
+  p.groups = groups;
+  p.keep = top_groups;
+  p.best = group_best;
+  p.softmax = score == VQ_SCORE_SOFTMAX;
+  p.renorm = renorm != 0;
+  p.scale = (float)scale;
+  p.offsets = offsets;
+  p.row_of = rows;
+  p.weights = weights;
+  p.chosen = chosen;
+  p.place = place;
+  p.counts = ws;
+  return hip_status(vq_internal::launch_route_experts(p, stream));
+}
+
+vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64_t ldy, const int32_t* place,
+                             const float* weights, int64_t m, int64_t n, int top, const void* res, int64_t ldr,
+                             const vq_modulation* mod, void* out, vq_dtype out_dt, int64_t ldo, hipStream_t stream) {
+  if (!valid_dt(y_dt) || !valid_dt(out_dt)) return VQ_ERR_INVALID_ARG;
+  if (m < 0 || n < 1 || top < 1 || y_rows < 0 || ldy < n || ldo < n || (res && ldr < n)) return VQ_ERR_INVALID_ARG;
+  if (m > 0 && (!place || !weights || !out || (y_rows > 0 && !y))) return VQ_ERR_INVALID_ARG;
+  if (mod && (mod->scale || mod->shift)) return VQ_ERR_INVALID_ARG;
+  if (is_16bit(y_dt) && is_16bit(out_dt) && y_dt != out_dt) return VQ_ERR_UNSUPPORTED;
+  if (top > kMaxTop || n > kMaxExpertCols || m > kMaxExpertRows || y_rows > kMaxExpertRows) return VQ_ERR_UNSUPPORTED;
+  if (misaligned(y, elem_size(y_dt)) || misaligned(res, elem_size(out_dt)) || misaligned(out, elem_size(out_dt)) ||
+      misaligned(place, 4) || misaligned(weights, 4))
+    return VQ_ERR_SHAPE;
+  vq_internal::CombineParams p{};
+  vq_status s = check_modulation(mod, is_16bit(y_dt) ? y_dt : out_dt, m, n, p.mod);
+  if (s != VQ_OK) return s;
+  if (m == 0) return VQ_OK;
+  p.y = y;
+  p.y_dt = (int)y_dt;
+  p.y_rows = y_rows;
+  p.ldy = ldy;
+  p.place = place;
+  p.weights = weights;
+  p.rows = m;
+  p.n = n;
+  p.top = top;
+  p.res = res;
+  p.ldr = ldr;
+  p.out = out;
+  p.out_dt = (int)out_dt;
+  p.ldo = ldo;
+  return hip_status(vq_internal::launch_combine(p, stream));
+}
+
 // ------------------------------------------------------------------ calibration
 
 int64_t vq_calib_hist_bins(void) { return vq_internal::calib_hist_bins(); }

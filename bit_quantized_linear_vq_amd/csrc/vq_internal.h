@@ -155,6 +155,39 @@ struct GatedNormParams {
 };
 hipError_t launch_gated_norm(const GatedNormParams& p, hipStream_t st);
 
+struct RouteExpertsParams {
+  const void* x;
+  int dtype;
+  const float* bias;  // or nullptr
+  int64_t ldx, rows;
+  int experts, top, groups, keep, best, softmax, renorm;
+  float scale;
+  int32_t* offsets;
+  int32_t* row_of;
+  float* weights;
+  int32_t* chosen;
+  int32_t* place;
+  int32_t* counts;  // route_experts_blocks(rows) * experts
+};
+int64_t route_experts_blocks(int64_t rows);
+hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st);
+struct CombineParams {
+  const void* y;
+  int y_dt;
+  int64_t y_rows, ldy;
+  const int32_t* place;
+  const float* weights;
+  int64_t rows, n;
+  int top;
+  const void* res;  // or nullptr, of out_dt
+  int64_t ldr;
+  ModParams mod;  // its gate
+  void* out;
+  int out_dt;
+  int64_t ldo;
+};
+hipError_t launch_combine(const CombineParams& p, hipStream_t st);
+
 hipError_t launch_pack_group(const void* w, int dtype, int64_t n, int64_t k, int64_t ldw, int group, uint8_t* codes,
                              void* scales, hipStream_t st);
 struct W4GemvParams {

@@ -535,6 +535,64 @@ vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const
                                 hipStream_t stream);
 
 /*
+ * Routing to experts: from the router's scores to what the experts' products take (rows
+ * sorted by expert) and what vq_combine_experts takes (each choice's place and weight).
+ *   p[i,e] = softmax over e of x[i,e], or 1 / (1 + exp(-x[i,e]))
+ *   c[i,e] = p[i,e] + bias[e], which only the choice goes by; without a bias the choice goes by
+ *            x[i,e] itself (the order of p, also where p rounds to the same number)
+ *   groups   experts in `groups` equal, consecutive groups: those top_groups whose group_best (1
+ *            or 2) largest c (p, for two without a bias) sum highest are kept, the others' experts not
+ *            chosen
+ *   chosen[i,0..top)  the experts of the largest c, descending
+ *   weights[i,j] = p[i,chosen] / (renorm ? sum_j p[i,chosen] : 1) * scale  (0 where that sum is 0)
+ * Ties go to the lower index, among groups and experts alike.  Everything is computed in
+ * float64 and the weights rounded once to float32.  An expert whose score or bias is -infinity is
+ * closed to the token: never chosen, with p = 0.  Where fewer than top experts are open the
+ * remaining choices are expert -1, place -1 and weight 0.  A row with a NaN score or c, or (softmax)
+ * an infinite score, is not routed: -1 throughout, and NaN weights.
+ *   x          device, dt in {F16, BF16, F32}, [m x experts], stride ldx
+ *   bias       device float [experts] or NULL
+ *   offsets    device int32 [experts + 1]: expert e's choices are at [offsets[e], offsets[e + 1])
+ *   rows       device int32 [m * top]: the token of each sorted choice, in an expert by ascending
+ *              token; -1 from offsets[experts] on
+ *   weights    device float [m x top];  chosen, place: device int32 [m x top] (place: where the
+ *              choice is in the sorted order)
+ *   ws         device int32 scratch of vq_route_experts_workspace_elems(m, experts) elements; calls
+ *              that may run at the same time need one each
+ * m = 0 writes zero offsets.  Places are the same in every call (no order of atomics enters).
+ * Nothing is allocated and the host reads nothing, so a call may be captured.
+ * Errors: INVALID_ARG (also top > experts of the kept groups, experts % groups, group_best > a
+ * group's experts), UNSUPPORTED (experts > 1024, top > 32, groups > 64, m * top > 2^26).
+ */
+typedef enum vq_score { VQ_SCORE_SOFTMAX = 0, VQ_SCORE_SIGMOID = 1 } vq_score;
+int64_t vq_route_experts_workspace_elems(int64_t m, int64_t experts);
+vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t experts, int64_t ldx, vq_score score,
+                           const float* bias, int groups, int top_groups, int group_best, int top, int renorm,
+                           double scale, int32_t* offsets, int32_t* rows, float* weights, int32_t* chosen,
+                           int32_t* place, int32_t* ws, hipStream_t stream);
+
+/*
+ * The experts' rows back to their tokens:
+ *   out[i] = RNE_out(fl32(res[i] + fl32(gate[i] * sum_j weights[i,j] * y[place[i,j]])))
+ * the products and the sum in float32, in the order of j; without res or gate their step is left
+ * out.  A place outside [0, y_rows) reads nothing and adds weight * 0 (a NaN weight shows, an absent
+ * choice of weight 0 does not).
+ *   y          device, y_dt in {F16, BF16, F32}, [y_rows x n], stride ldy
+ *   place, weights   device int32 and float [m x top], as vq_route_experts writes them
+ *   res        device out_dt [m x n], stride ldr, or NULL
+ *   mod        host or NULL: its gate [sets x n], F32 or of the 16-bit type among y_dt and out_dt, as
+ *              for vq_gated_norm (scale and shift NULL); a row outside the sets is res[i], or 0
+ *   out        device out_dt [m x n], stride ldo: y_dt or F32, any if y_dt is F32.  It may be res
+ *              itself (same pointer and stride)
+ * Any n, strides and element-aligned addresses.  m = 0 enqueues nothing.  One kernel; nothing is
+ * allocated.  Errors: INVALID_ARG, SHAPE (alignment, m % sets), UNSUPPORTED (top > 32, n > 2^20,
+ * m or y_rows > 2^26, y_dt and out_dt two 16-bit types).
+ */
+vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64_t ldy, const int32_t* place,
+                             const float* weights, int64_t m, int64_t n, int top, const void* res, int64_t ldr,
+                             const vq_modulation* mod, void* out, vq_dtype out_dt, int64_t ldo, hipStream_t stream);
+
+/*
  * Static per-tensor activation scale by clipping-percentile search (Q-ARVD, Technical
  * details: per-tensor activations with a clipping percentile and a scale learned during
  * reconstruction).  One pass builds the histogram of |x| over its 32768 16-bit magnitude

@@ -38,8 +38,9 @@ Steps and the passages they follow:
 * ``group4``    4-bit weights with group scales and their product with a few 16-bit rows.
 * ``experts``   products of several experts over rows sorted by expert.
 * ``gated``     norms before and after a block with its gate and residual scale.
+* ``router``    routing to experts by their scores, and the experts' rows back to their tokens.
 """
 from . import (  # noqa: F401
     numerics, detect, quantizer, fwht, gemm, route, linear, decompose, mx, calib, control, dense, norm, group4, experts,
-    gated,
+    gated, router,
 )

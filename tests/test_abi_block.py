@@ -83,3 +83,57 @@ def gatedq(vq, **kw):
 ])
 def test_gated_norm_quant_validation(vq, kw, want):
     assert gatedq(vq, **kw) == want
+
+
+def route(vq, **kw):
+    a = {**dict(x=FAKE, dt=F32, m=4, e=16, ldx=16, score=0, bias=FAKE, groups=4, keep=2, best=2, top=3, renorm=1, scale=1.0,
+                off=FAKE, rows=FAKE, w=FAKE, ch=FAKE, place=FAKE, ws=FAKE), **kw}
+    return vq._lib.vq_route_experts(a["x"], a["dt"], a["m"], a["e"], a["ldx"], a["score"], a["bias"], a["groups"], a["keep"],
+                                    a["best"], a["top"], a["renorm"], a["scale"], a["off"], a["rows"], a["w"], a["ch"],
+                                    a["place"], a["ws"], NULL)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=NULL), INVALID), (dict(dt=7), INVALID), (dict(m=-1), INVALID), (dict(e=0), INVALID), (dict(ldx=15), INVALID),
+    (dict(score=2), INVALID), (dict(score=-1), INVALID), (dict(off=NULL), INVALID), (dict(rows=NULL), INVALID),
+    (dict(w=NULL), INVALID), (dict(ch=NULL), INVALID), (dict(place=NULL), INVALID), (dict(ws=NULL), INVALID),
+    (dict(groups=0), INVALID), (dict(groups=3), INVALID), (dict(keep=0), INVALID), (dict(keep=5), INVALID),
+    (dict(best=0), INVALID), (dict(best=3), INVALID), (dict(groups=16, keep=8), INVALID), (dict(top=0), INVALID),
+    (dict(top=9), INVALID), (dict(scale=INF), INVALID), (dict(scale=NAN), INVALID),
+    (dict(e=1028, ldx=1028), UNSUP), (dict(e=256, ldx=256, top=33), UNSUP), (dict(e=512, ldx=512, groups=128), UNSUP),
+    (dict(m=1 << 25), UNSUP), (dict(m=1 << 62), UNSUP),
+    (dict(x=0x10002), SHAPE), (dict(bias=0x10002), SHAPE), (dict(off=0x10002), SHAPE), (dict(rows=BYTE), SHAPE),
+    (dict(w=0x10002), SHAPE), (dict(ch=0x10002), SHAPE), (dict(place=0x10003), SHAPE), (dict(ws=0x10002), SHAPE),
+])
+def test_route_validation(vq, kw, want):
+    assert route(vq, **kw) == want
+
+
+def test_route_workspace(vq):
+    n = vq._lib.vq_route_experts_workspace_elems
+    assert n(-1, 8) == n(8, 0) == n(8, 1025) == n((1 << 26) + 1, 8) == 0
+    assert n(0, 8) > 0 and n(1, 1) > 0 and n(1 << 26, 1024) >= 1024
+
+
+def combine(vq, **kw):
+    a = {**dict(y=FAKE, ydt=BF16, rows=8, ldy=64, place=FAKE, w=FAKE, m=4, n=64, top=2, res=FAKE, ldr=64, out=FAKE, odt=BF16,
+                ldo=64, mod=True, gate=FAKE, scale=NULL, shift=NULL, ldg=64, ldsc=64, ldsh=64, index=NULL, sets=2, mdt=F32), **kw}
+    mod = vq.Modulation(a["gate"], a["scale"], a["shift"], a["ldg"], a["ldsc"], a["ldsh"], a["index"], a["sets"], a["mdt"], 0)
+    return vq._lib.vq_combine_experts(a["y"], a["ydt"], a["rows"], a["ldy"], a["place"], a["w"], a["m"], a["n"], a["top"],
+                                      a["res"], a["ldr"], ctypes.byref(mod) if a["mod"] else None, a["out"], a["odt"],
+                                      a["ldo"], NULL)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(y=NULL), INVALID), (dict(ydt=3), INVALID), (dict(odt=5), INVALID), (dict(rows=-1), INVALID), (dict(ldy=63), INVALID),
+    (dict(place=NULL), INVALID), (dict(w=NULL), INVALID), (dict(m=-1), INVALID), (dict(n=0), INVALID), (dict(top=0), INVALID),
+    (dict(ldr=63), INVALID), (dict(out=NULL), INVALID), (dict(ldo=10), INVALID), (dict(scale=FAKE), INVALID),
+    (dict(shift=FAKE), INVALID), (dict(mdt=F16), INVALID), (dict(sets=0), INVALID), (dict(ldg=63), INVALID),
+    (dict(odt=F16), UNSUP), (dict(top=33), UNSUP), (dict(m=(1 << 26) + 1), UNSUP), (dict(rows=(1 << 26) + 1), UNSUP),
+    (dict(n=(1 << 20) + 1, ldy=1 << 21, ldr=1 << 21, ldo=1 << 21), UNSUP),
+    (dict(sets=3), SHAPE), (dict(y=BYTE), SHAPE), (dict(res=BYTE), SHAPE), (dict(out=0x10002, odt=F32), SHAPE),
+    (dict(place=0x10002), SHAPE), (dict(w=0x10002), SHAPE), (dict(gate=0x10002), SHAPE),
+    (dict(m=0), OK), (dict(m=0, y=NULL, place=NULL, w=NULL, out=NULL, res=NULL, mod=False), OK),
+])
+def test_combine_validation(vq, kw, want):
+    assert combine(vq, **kw) == want

@@ -102,3 +102,59 @@ def test_gated_quant_refusals(vq, error, kw):
 def test_gated_norm_refuses_another_output(vq):
     refused(vq, ValueError, gated, vq, y=dev(6, 127, dt=B))
     refused(vq, TypeError, gated, vq, y=dev(6, 128, dt=H))
+
+
+def route(vq, **kw):
+    a = dict(scores=dev(6, 16), top=2, offsets=dev(17, dt=I32), rows=dev(12, dt=I32), weights=dev(6, 2), experts=dev(6, 2, dt=I32),
+             place=dev(6, 2, dt=I32), ws=dev(64, dt=I32))
+    a.update(kw)
+    return vq.vq_route_experts(**a)
+
+
+def test_route_calls_that_are_right_reach_the_launch(vq):
+    route(vq)
+    route(vq, scores=dev(6, 16, dt=H), score="sigmoid", bias=dev(16), groups=4, top_groups=2, group_best=2)
+    route(vq, scores=dev(6, 20)[:, :16])
+    assert vq._lib.launched == ["vq_route_experts"] * 3
+
+
+@pytest.mark.parametrize("error,kw", [
+    (TypeError, lambda: dict(scores=torch.empty(6, 16))), (TypeError, lambda: dict(scores=dev(6, 16, dt=I32))),
+    (ValueError, lambda: dict(scores=dev(96))), (ValueError, lambda: dict(scores=dev(16, 6).t())),
+    (ValueError, lambda: dict(score="max")), (ValueError, lambda: dict(top=0)), (ValueError, lambda: dict(top=17)),
+    (ValueError, lambda: dict(bias=dev(15))), (ValueError, lambda: dict(bias=dev(17))), (TypeError, lambda: dict(bias=dev(16, dt=H))),
+    (ValueError, lambda: dict(offsets=dev(16, dt=I32))), (TypeError, lambda: dict(offsets=dev(17))),
+    (ValueError, lambda: dict(rows=dev(6, 2, dt=I32))), (ValueError, lambda: dict(weights=dev(2, 6))),
+    (ValueError, lambda: dict(weights=dev(2, 6).t())), (TypeError, lambda: dict(experts=dev(6, 2))),
+    (TypeError, lambda: dict(place=torch.empty(6, 2, dtype=I32))), (ValueError, lambda: dict(ws=dev(15, dt=I32))),
+])
+def test_route_refusals(vq, error, kw):
+    refused(vq, error, route, vq, **kw())
+
+
+def combine(vq, **kw):
+    a = dict(y=dev(12, 64, dt=B), place=dev(6, 2, dt=I32), weights=dev(6, 2), out=dev(6, 64, dt=B))
+    a.update(kw)
+    return vq.vq_combine_experts(**a)
+
+
+def test_combine_calls_that_are_right_reach_the_launch(vq):
+    combine(vq)
+    combine(vq, residual=dev(6, 64, dt=B), gate=dev(3, 64))
+    combine(vq, y=dev(12, 64), gate=dev(4, 64, dt=B), index=dev(6, dt=I32))
+    combine(vq, y=dev(0, 64, dt=B))
+    assert vq._lib.launched == ["vq_combine_experts"] * 4
+
+
+@pytest.mark.parametrize("error,kw", [
+    (TypeError, lambda: dict(y=dev(12, 64, dt=I32))), (ValueError, lambda: dict(y=dev(12 * 64, dt=B))),
+    (TypeError, lambda: dict(place=dev(6, 2))), (ValueError, lambda: dict(place=dev(6, 3, dt=I32))),
+    (ValueError, lambda: dict(place=dev(12, dt=I32), weights=dev(12))), (TypeError, lambda: dict(weights=dev(6, 2, dt=B))),
+    (ValueError, lambda: dict(place=dev(6, 0, dt=I32), weights=dev(6, 0))),
+    (ValueError, lambda: dict(residual=dev(6, 63, dt=B))), (TypeError, lambda: dict(residual=dev(6, 64))),
+    (ValueError, lambda: dict(out=dev(5, 64, dt=B))), (TypeError, lambda: dict(out=dev(6, 64, dt=torch.int16))),
+    (ValueError, lambda: dict(gate=dev(4, 64))), (ValueError, lambda: dict(index=dev(6, dt=I32))),
+    (TypeError, lambda: dict(gate=dev(2, 64, dt=H))), (TypeError, lambda: dict(out=torch.empty(6, 64, dtype=B))),
+])
+def test_combine_refusals(vq, error, kw):
+    refused(vq, error, combine, vq, **kw())

@@ -2,7 +2,7 @@
 of the definitions, and planted mistakes that the comparisons catch."""
 import numpy as np
 
-from oracle import gated, norm
+from oracle import gated, norm, router
 from oracle import numerics as onum
 
 
@@ -75,3 +75,72 @@ def test_planted_mistakes_are_caught():
     ]
     for ws, wv in wrong:
         assert not (np.array_equal(ws, s) and np.array_equal(wv, v))
+
+
+def test_routing_by_hand():
+    x = np.array([[0.0, 2.0, 1.0, 2.0], [-np.inf, 5.0, -np.inf, -np.inf], [-np.inf] * 4, [1.0, np.nan, 0.0, 0.0]])
+    off, rows, w, ch, place = router.route(x, 2)
+    assert ch.tolist() == [[1, 3], [1, -1], [-1, -1], [-1, -1]]  # the tie goes to the lower index
+    assert off.tolist() == [0, 0, 2, 2, 3] and rows.tolist() == [0, 1, 0] + [-1] * 5
+    assert place.tolist() == [[0, 2], [1, -1], [-1, -1], [-1, -1]]
+    assert w[:3].tolist() == [[0.5, 0.5], [1.0, 0.0], [0.0, 0.0]] and np.isnan(w[3]).all()
+    p = np.exp([0.0, 2.0, 1.0, 2.0])
+    assert np.allclose(router.route(x, 2, renorm=False, scale=2.0)[2][0], 2 * p[1] / p.sum(), rtol=1e-15)
+
+
+def test_a_bias_moves_the_choice_and_not_the_weight():
+    x = np.array([[0.0, 1.0, 2.0]])
+    ch, w = router.choose(x[0], 1, "sigmoid", bias=[0.9, 0.0, -0.1])
+    assert ch == [0] and w == [1.0]
+    ch, w = router.choose(x[0], 1, "sigmoid", bias=[0.9, 0.0, -0.1], renorm=False)
+    assert w == [0.5]
+    assert router.choose(x[0], 3, "sigmoid", bias=[0.0, -np.inf, 0.0])[0] == [2, 0, -1]
+
+
+def test_groups_by_one_and_by_two():
+    x = np.log(np.array([0.30, 0.02, 0.20, 0.18, 0.25, 0.05]))
+    assert router.choose(x, 2, groups=3, keep=1)[0] == [0, 1]  # the best single expert is in group 0
+    assert router.choose(x, 2, groups=3, keep=1, best=2)[0] == [2, 3]  # the best pair in group 1
+    assert router.choose(x, 3, groups=3, keep=2, best=2)[0] == [0, 2, 3]
+    # the pairs' sums: 0.32, 0.38, 0.30; with the third group closed but for one expert still third
+    x[4] = -np.inf
+    assert router.choose(x, 3, groups=3, keep=3, best=2)[0] == [0, 2, 3]
+
+
+def test_choice_by_the_scores_where_p_rounds_to_one():
+    assert router.choose([40.0, 50.0, 45.0], 2, "sigmoid")[0] == [1, 2]
+    assert router.choose([-2000.0, 0.0, -1500.0], 2)[0] == [1, 2]
+
+
+def test_routing_mistakes_are_caught():
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((9, 8))
+    b = 0.3 * rng.standard_normal(8)
+    right = router.route(x, 3, bias=b, groups=4, keep=2, best=2)
+    for how in (dict(), dict(bias=b), dict(bias=b, groups=4, keep=2), dict(bias=b, groups=2, keep=1, best=2),
+                dict(bias=-b, groups=4, keep=2, best=2), dict(bias=b, groups=4, keep=2, best=2, score="sigmoid")):
+        wrong = router.route(x, 3, **how)
+        assert not (np.array_equal(right[3], wrong[3]) and np.array_equal(right[2], wrong[2]))
+
+
+def test_combining_by_hand():
+    y = np.array([[1, 2], [10, 20], [np.nan, np.nan]], np.float32)
+    place = np.array([[1, 0], [-1, 0], [-1, -1], [1, 5]], np.int32)
+    w = np.array([[0.5, 2], [0, 1], [0, 0], [1, np.nan]], np.float32)
+    v = router.combine(y, place, w)
+    assert v[:3].tolist() == [[7, 14], [1, 2], [0, 0]] and np.isnan(v[3]).all()
+    res = np.ones((4, 2), np.float32)
+    v = router.combine(y, place, w, res, np.array([[2, -1], [0, 0]], np.float32), np.array([0, 0, 1, 2]))
+    assert v.tolist() == [[15, -13], [3, -1], [1, 1], [1, 1]]
+
+
+def test_a_product_over_experts_and_back_is_the_weighted_sum_of_its_experts():
+    rng = np.random.default_rng(7)
+    x, wt = rng.standard_normal((6, 4)).astype(np.float32), rng.standard_normal((5, 3, 4)).astype(np.float32)
+    off, rows, w, ch, place = router.route(rng.standard_normal((6, 5)), 2)
+    y = np.zeros((12, 3), np.float32)
+    for e in range(5):
+        y[off[e]:off[e + 1]] = x[rows[off[e]:off[e + 1]]] @ wt[e].T
+    v = router.combine(y, place, w.astype(np.float32))
+    for t in range(6):
+        assert np.allclose(v[t], sum(w[t, j] * (wt[ch[t, j]] @ x[t]) for j in range(2)), rtol=1e-5, atol=1e-6)
