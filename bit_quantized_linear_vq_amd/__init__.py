@@ -38,6 +38,7 @@ EXPORTS = (
     "vq_mx_gemm_workspace_bytes", "vq_gemm_dense",
     "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts", "vq_gemm_dense_experts",
     "vq_gated_norm", "vq_gated_norm_quant", "vq_route_experts_workspace_elems", "vq_route_experts", "vq_combine_experts",
+    "vq_lowrank_workspace_elems", "vq_lowrank_add",
     "vq_calib_hist_bins", "vq_calib_static_scale", "vq_control_workspace_elems", "vq_step_control",
     "vq_status_string", "vq_last_hip_error", "vq_version",
 )
@@ -101,6 +102,8 @@ def _load():
         "vq_route_experts_workspace_elems": (I64, [I64, I64]),
         "vq_route_experts": (I, [P, I, I64, I64, I64, I, P, I, I, I, I, I, D, P, P, P, P, P, P, P]),
         "vq_combine_experts": (I, [P, I, I64, I64, P, P, I64, I64, I, P, I64, P, P, I, I64, P]),
+        "vq_lowrank_workspace_elems": (I64, [I64, I64, I64, I64]),
+        "vq_lowrank_add": (I, [P, I, I64, I64, I64, I64, P, P, I64, I64, P, P, P, I64, P, I, I64, P, P]),
         "vq_calib_hist_bins": (I64, []),
         "vq_calib_static_scale": (I, [P, I, I64, I64, I64, I, P, I32, P, P, P, P, P, P, P]),
         "vq_status_string": (ctypes.c_char_p, [I]),
@@ -715,7 +718,7 @@ def _rows16(t, name, index=None, dtype=None):
         raise ValueError(f"{name} must be 2-D")
     m, k = t.shape
     ld, unit = t.stride()
-    if (k > 1 and unit != 1) or (m > 1 and ld < k):
+    if (k > 1 and unit != 1 and m) or (m > 1 and ld < k):
         raise ValueError(f"{name} must have unit stride along its rows and a pitch of at least a row")
     return ld if m > 1 else k
 
@@ -1098,7 +1101,7 @@ def _rows_any(t, name, index, dtypes):
         raise ValueError(f"{name} must be 2-D")
     m, k = t.shape
     ld, unit = t.stride()
-    if (k > 1 and unit != 1) or (m > 1 and ld < k):
+    if (k > 1 and unit != 1 and m) or (m > 1 and ld < k):
         raise ValueError(f"{name} must have unit stride along its rows and a pitch of at least a row")
     return ld if m > 1 else k
 
@@ -1187,6 +1190,61 @@ def vq_combine_experts(y: torch.Tensor, place: torch.Tensor, weights: torch.Tens
     return out
 
 
+# ------------------------------------------------------------------ low-rank adapters
+
+@functools.lru_cache(maxsize=1024)
+def vq_lowrank_workspace_elems(m: int, adapters: int, rank: int, k: int) -> int:
+    """Float32 elements of the scratch that vq_lowrank_add needs for m rows."""
+    return int(_lib.vq_lowrank_workspace_elems(m, adapters, rank, k))
+
+
+def vq_lowrank_add(base: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: torch.Tensor, index: torch.Tensor,
+                   scales: torch.Tensor | None = None, out=None, ws=None):
+    """base + scales[a] * (x . down[a]^T) . up[a]^T with each row's own adapter a = index[row] (outside
+    [0, L): none, the row is base's).
+
+    x [M x K]: the input of the projection whose output base [M x N] is; down [L x R x K], up
+    [L x N x R] of x's type; index int32 [M]; scales float32 [L].  base and out: x's type or float32;
+    out may be base.  Returns out [M x N]."""
+    ldx = _rows16(x, "x")
+    m, k = x.shape
+    dt, dev = x.dtype, x.get_device()
+    ldb = _rows_any(base, "base", dev, (dt, torch.float32))
+    n = base.shape[1]
+    if base.shape[0] != m:
+        raise ValueError(f"base must have x's {m} rows")
+    _dense(down, "down", dev, (dt,), 0)
+    _dense(up, "up", dev, (dt,), 0)
+    if down.dim() != 3 or down.shape[2] != k:
+        raise ValueError(f"down must be [L x R x {k}]")
+    adapters, rank, _ = down.shape
+    if up.shape != (adapters, n, rank):
+        raise ValueError(f"up must be [{adapters} x {n} x {rank}]")
+    _dense(index, "index", dev, _I32, m)
+    if index.numel() != m:
+        raise ValueError(f"index must hold {m} elements")
+    s_ptr = None
+    if scales is not None:
+        _dense(scales, "scales", dev, _F32, adapters)
+        if scales.numel() != adapters:
+            raise ValueError(f"scales must hold {adapters} elements")
+        s_ptr = scales.data_ptr()
+    if out is None:
+        out, ldo = torch.empty(m, n, dtype=base.dtype, device=base.device), n
+    else:
+        ldo = _rows_any(out, "out", dev, (base.dtype,))
+        if out.shape != base.shape:
+            raise ValueError("out must have base's shape")
+    need = vq_lowrank_workspace_elems(m, adapters, rank, k)
+    if ws is None:
+        ws = torch.empty(max(need, 1), dtype=torch.float32, device=x.device)
+    else:
+        _dense(ws, "ws", dev, _F32, need)
+    _launch("vq_lowrank_add", dev, x.data_ptr(), _DT[dt], m, n, k, ldx, down.data_ptr(), up.data_ptr(), adapters, rank,
+            index.data_ptr(), s_ptr, base.data_ptr(), ldb, out.data_ptr(), _DT[out.dtype], ldo, ws.data_ptr())
+    return out
+
+
 # ------------------------------------------------------------------ prepared calls
 
 # Entry points that only enqueue work on a stream (their last argument).
@@ -1196,7 +1254,7 @@ _LAUNCHES = frozenset((
     "vq_mx_gemm", "vq_gemm_dense", "vq_calib_static_scale", "vq_step_control",
     "vq_rmsnorm", "vq_rmsnorm_quant", "vq_pack_weights_group", "vq_w4_gemv", "vq_qgemm_experts",
     "vq_gemm_dense_experts", "vq_gated_norm", "vq_gated_norm_quant",
-    "vq_route_experts", "vq_combine_experts",
+    "vq_route_experts", "vq_combine_experts", "vq_lowrank_add",
 ))
 
 

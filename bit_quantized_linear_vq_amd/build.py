@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libvq.so")
 
 SOURCES = ["k_quant.hip", "k_hadamard.hip", "k_qgemm.hip", "k_detect_route.hip", "k_decompose.hip", "k_mx.hip",
            "k_calib.hip", "k_dense.hip", "k_norm.hip", "k_gated_norm.hip",
-           "k_w4gemv.hip", "k_experts.hip", "k_route_experts.hip", "vq_api.cpp"]
+           "k_w4gemv.hip", "k_experts.hip", "k_route_experts.hip", "k_lowrank.hip", "vq_api.cpp"]
 
 ARCH = os.environ.get("VQ_OFFLOAD_ARCH", "gfx950")
 

@@ -851,6 +851,59 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
   return hip_status(vq_internal::launch_combine(p, stream));
 }
 
+// ------------------------------------------------------------------ low-rank adapters
+
+namespace {
+constexpr int64_t kMaxAdapters = (int64_t)1 << 20, kMaxRank = 128, kMaxLowrankDim = (int64_t)1 << 24;
+bool lowrank_sizes(int64_t m, int64_t adapters, int64_t rank, int64_t k) {
+  return m >= 0 && m < kMaxDim && adapters >= 1 && adapters <= kMaxAdapters && rank >= 8 && rank <= kMaxRank &&
+         rank % 8 == 0 && k >= 1 && k <= kMaxLowrankDim;
+}
+}  // namespace
+
+int64_t vq_lowrank_workspace_elems(int64_t m, int64_t adapters, int64_t rank, int64_t k) {
+  return lowrank_sizes(m, adapters, rank, k) ? vq_internal::lowrank_workspace_elems(m, adapters, rank, k) : 0;
+}
+
+vq_status vq_lowrank_add(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k, int64_t ldx, const void* down,
+                         const void* up, int64_t adapters, int64_t rank, const int32_t* index, const float* scale,
+                         const void* base, int64_t ldb, void* out, vq_dtype out_dt, int64_t ldo, float* ws,
+                         hipStream_t stream) {
+  if (!is_16bit(dt) || (out_dt != dt && out_dt != VQ_F32)) return VQ_ERR_INVALID_ARG;
+  if (m < 0 || n < 1 || k < 1 || adapters < 1 || rank < 1 || m >= kMaxDim || n >= kMaxDim || k >= kMaxDim)
+    return VQ_ERR_INVALID_ARG;
+  if (ldx < k || ldb < n || ldo < n) return VQ_ERR_INVALID_ARG;
+  if (!down || !up || !ws || (m > 0 && (!x || !index || !base || !out))) return VQ_ERR_INVALID_ARG;
+  if (rank > kMaxRank || adapters > kMaxAdapters || n > kMaxLowrankDim || k > kMaxLowrankDim) return VQ_ERR_UNSUPPORTED;
+  if (rank % 8 || k % VQ_K_ALIGN || ldx % 8 || !aligned16(x) || !aligned16(down) || !aligned16(up) || !aligned16(ws))
+    return VQ_ERR_SHAPE;
+  if (misaligned(index, 4) || misaligned(scale, 4) || misaligned(base, elem_size(out_dt)) ||
+      misaligned(out, elem_size(out_dt)))
+    return VQ_ERR_SHAPE;
+  if (m == 0) return VQ_OK;
+  if (vq_internal::lowrank_groups(m, adapters, rank, k, n) > ((int64_t)1 << 30)) return VQ_ERR_UNSUPPORTED;
+  vq_internal::LowrankParams p{};
+  p.x = x;
+  p.dtype = (int)dt;
+  p.rows = m;
+  p.n = n;
+  p.k = k;
+  p.ldx = ldx;
+  p.down = down;
+  p.up = up;
+  p.adapters = adapters;
+  p.rank = rank;
+  p.index = index;
+  p.scale = scale;
+  p.base = base;
+  p.out = out;
+  p.out_dt = (int)out_dt;
+  p.ldb = ldb;
+  p.ldo = ldo;
+  p.t = ws;
+  return hip_status(vq_internal::launch_lowrank(p, stream));
+}
+
 // ------------------------------------------------------------------ calibration
 
 int64_t vq_calib_hist_bins(void) { return vq_internal::calib_hist_bins(); }

@@ -188,6 +188,26 @@ struct CombineParams {
 };
 hipError_t launch_combine(const CombineParams& p, hipStream_t st);
 
+struct LowrankParams {
+  const void* x;
+  int dtype;  // 0 f16, 1 bf16
+  int64_t rows, n, k, ldx;
+  const void* down;
+  const void* up;
+  int64_t adapters, rank;
+  const int32_t* index;
+  const float* scale;  // or nullptr
+  const void* base;
+  void* out;
+  int out_dt;
+  int64_t ldb, ldo;
+  float* t;
+};
+int64_t lowrank_workspace_elems(int64_t rows, int64_t adapters, int64_t rank, int64_t k);
+// Workgroups of the larger of its two launches, at most.
+int64_t lowrank_groups(int64_t rows, int64_t adapters, int64_t rank, int64_t k, int64_t n);
+hipError_t launch_lowrank(const LowrankParams& p, hipStream_t st);
+
 hipError_t launch_pack_group(const void* w, int dtype, int64_t n, int64_t k, int64_t ldw, int group, uint8_t* codes,
                              void* scales, hipStream_t st);
 struct W4GemvParams {

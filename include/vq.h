@@ -593,6 +593,40 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
                              const vq_modulation* mod, void* out, vq_dtype out_dt, int64_t ldo, hipStream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside a projection that they share: row i's request
+ * uses adapter a = index[i],
+ *   out[i] = RNE_out(fl32(base[i] + scale[a] * (x[i] . down[a]^T) . up[a]^T))
+ * and a row whose index lies outside [0, adapters) has none: out[i] = base[i], bit for bit.
+ * base is the shared projection's output (vq_qgemm_dequant, vq_gemm_dense, vq_w4_gemv ..).
+ *   t = x[i] . down[a]^T: products exact, sums in float32, times scale rounded to float32; it
+ *   enters the second product as two 16-bit pieces, sums in float32.  With K = k, R = rank, T the
+ *   largest |t| of the row and S = sum_j |t_j| |up_j|:
+ *     |out - exact| <= scale (2 K + 10) 2^-24 sum_j (sum_k |x_k down_jk|) |up_j|
+ *                      + (4 R + 4) 2^-24 S + 2^-16 S (F16: 2^-22 S + 2^-38 T sum_j |up_j|)
+ *   before the addition of base and the output's rounding
+ *   x          device, dt in {F16, BF16}, [m x k], stride ldx (16-byte aligned, ldx % 8 == 0)
+ *   down       device dt [adapters x rank x k];  up: device dt [adapters x n x rank] (16-byte aligned)
+ *   index      device int32 [m], in any order; rows of one adapter next to each other are fastest:
+ *              a tile of 16 to 64 rows reads every adapter that occurs in it
+ *   scale      device float [adapters], or NULL for ones
+ *   base, out  device out_dt (dt or F32), [m x n], strides ldb, ldo; out may be base itself (same
+ *              pointer and stride)
+ *   ws         device float scratch of vq_lowrank_workspace_elems(m, adapters, rank, k) elements, 16-byte
+ *              aligned; calls that may run at the same time need one each
+ * rank is 8 to 128, a multiple of 8 (a smaller adapter is padded with zeros); k % 64 == 0; any n.
+ * An infinity or NaN in a row of x or in an adapter shows in that row or that adapter's rows alone.
+ * m = 0 enqueues nothing.  Two kernels; nothing is allocated and the host does not read the index,
+ * so a call may be captured in a graph and replayed with another index.
+ * Errors: INVALID_ARG, SHAPE (k % 64, rank % 8, alignment), UNSUPPORTED (rank > 128, adapters > 2^20,
+ * n or k > 2^24, more than 2^30 tiles).
+ */
+int64_t vq_lowrank_workspace_elems(int64_t m, int64_t adapters, int64_t rank, int64_t k);
+vq_status vq_lowrank_add(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k, int64_t ldx, const void* down,
+                         const void* up, int64_t adapters, int64_t rank, const int32_t* index, const float* scale,
+                         const void* base, int64_t ldb, void* out, vq_dtype out_dt, int64_t ldo, float* ws,
+                         hipStream_t stream);
+
+/*
  * Static per-tensor activation scale by clipping-percentile search (Q-ARVD, Technical
  * details: per-tensor activations with a clipping percentile and a scale learned during
  * reconstruction).  One pass builds the histogram of |x| over its 32768 16-bit magnitude

@@ -39,8 +39,9 @@ Steps and the passages they follow:
 * ``experts``   products of several experts over rows sorted by expert.
 * ``gated``     norms before and after a block with its gate and residual scale.
 * ``router``    routing to experts by their scores, and the experts' rows back to their tokens.
+* ``lowrank``   low-rank adapters of many requests beside a shared projection.
 """
 from . import (  # noqa: F401
     numerics, detect, quantizer, fwht, gemm, route, linear, decompose, mx, calib, control, dense, norm, group4, experts,
-    gated, router,
+    gated, router, lowrank,
 )

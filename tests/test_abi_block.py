@@ -137,3 +137,34 @@ def combine(vq, **kw):
 ])
 def test_combine_validation(vq, kw, want):
     assert combine(vq, **kw) == want
+
+
+def lowrank(vq, **kw):
+    a = {**dict(x=FAKE, dt=BF16, m=4, n=32, k=128, ldx=128, down=FAKE, up=FAKE, ad=3, r=16, index=FAKE, scale=FAKE, base=FAKE,
+                ldb=32, out=FAKE, odt=BF16, ldo=32, ws=FAKE), **kw}
+    return vq._lib.vq_lowrank_add(a["x"], a["dt"], a["m"], a["n"], a["k"], a["ldx"], a["down"], a["up"], a["ad"], a["r"],
+                                  a["index"], a["scale"], a["base"], a["ldb"], a["out"], a["odt"], a["ldo"], a["ws"], NULL)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=NULL), INVALID), (dict(dt=F32), INVALID), (dict(odt=F16), INVALID), (dict(odt=9), INVALID), (dict(m=-1), INVALID),
+    (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(ldx=64), INVALID), (dict(ldb=31), INVALID), (dict(ldo=0), INVALID),
+    (dict(down=NULL), INVALID), (dict(up=NULL), INVALID), (dict(ad=0), INVALID), (dict(r=0), INVALID), (dict(index=NULL), INVALID),
+    (dict(base=NULL), INVALID), (dict(out=NULL), INVALID), (dict(ws=NULL), INVALID),
+    (dict(r=136), UNSUP), (dict(ad=(1 << 20) + 1), UNSUP), (dict(n=(1 << 24) + 1, ldb=1 << 25, ldo=1 << 25), UNSUP),
+    (dict(k=(1 << 24) + 64, ldx=1 << 25), UNSUP), (dict(m=(1 << 31) - 1, n=1 << 20, ldb=1 << 20, ldo=1 << 20), UNSUP),
+    (dict(r=12), SHAPE), (dict(k=96, ldx=96), SHAPE), (dict(ldx=132), SHAPE), (dict(x=ODD), SHAPE), (dict(down=ODD), SHAPE),
+    (dict(up=ODD), SHAPE), (dict(ws=ODD), SHAPE), (dict(index=0x10002), SHAPE), (dict(scale=0x10002), SHAPE),
+    (dict(base=BYTE), SHAPE), (dict(out=0x10002, odt=F32), SHAPE),
+    (dict(m=0), OK), (dict(m=0, x=NULL, index=NULL, base=NULL, out=NULL), OK),
+])
+def test_lowrank_validation(vq, kw, want):
+    assert lowrank(vq, **kw) == want
+
+
+def test_lowrank_workspace(vq):
+    n = vq._lib.vq_lowrank_workspace_elems
+    assert n(-1, 1, 8, 64) == n(1, 0, 8, 64) == n(1, 1, 12, 64) == n(1, 1, 136, 64) == n(1, 1, 8, 0) == 0
+    for m in (0, 1, 17, 5000, 1 << 20):
+        for r in (8, 128):
+            assert n(m, 4, r, 4096) >= max(m, 1) * r

@@ -2,7 +2,7 @@
 of the definitions, and planted mistakes that the comparisons catch."""
 import numpy as np
 
-from oracle import gated, norm, router
+from oracle import gated, lowrank, norm, router
 from oracle import numerics as onum
 
 
@@ -144,3 +144,37 @@ def test_a_product_over_experts_and_back_is_the_weighted_sum_of_its_experts():
     v = router.combine(y, place, w.astype(np.float32))
     for t in range(6):
         assert np.allclose(v[t], sum(w[t, j] * (wt[ch[t, j]] @ x[t]) for j in range(2)), rtol=1e-5, atol=1e-6)
+
+
+def test_adapters_by_hand():
+    x = np.array([[1.0, 2.0], [3.0, 4.0], [5.0, 6.0]])
+    down = np.array([[[1.0, 0.0]], [[0.0, 1.0]]])
+    up = np.array([[[1.0], [10.0]], [[2.0], [-1.0]]])
+    delta, bound = lowrank.exact(x, down, up, [1, -1, 0], [2.0, 0.5])
+    assert delta.tolist() == [[2.0, -1.0], [0.0, 0.0], [10.0, 100.0]]
+    assert (bound[1] == 0).all() and (bound[[0, 2]] > 0).all() and (bound < 1e-2).all()
+
+
+def test_adapters_equal_the_merged_weights():
+    """x . (W + s up . down)^T is the projection with the adapter's product merged into its weights."""
+    rng = np.random.default_rng(8)
+    x, w = rng.standard_normal((5, 16)), rng.standard_normal((7, 16))
+    down, up, s = rng.standard_normal((3, 4, 16)), rng.standard_normal((3, 7, 4)), np.array([0.5, 2.0, -1.0])
+    index = np.array([0, 2, 3, 1, 0])
+    delta, _ = lowrank.exact(x, down, up, index, s)
+    for i, a in enumerate(index):
+        merged = w if a > 2 else w + s[a] * up[a] @ down[a]
+        assert np.allclose(x[i] @ w.T + delta[i], x[i] @ merged.T, rtol=1e-12, atol=1e-12)
+
+
+def test_adapter_mistakes_are_outside_the_bound():
+    rng = np.random.default_rng(9)
+    x, down, up = rng.standard_normal((6, 64)), rng.standard_normal((3, 8, 64)) / 8, rng.standard_normal((3, 20, 8))
+    index, s = np.array([0, 1, 2, 0, 1, 2]), np.array([0.5, 1.5, 1.0])
+    for dt in ("bf16", "fp16"):
+        d, b = lowrank.exact(x, down, up, index, s, dt)
+        t16 = np.stack([x[i] @ down[a].T for i, a in enumerate(index)]).astype(np.float16).astype(np.float64)
+        wrong = [lowrank.exact(x, down, up, (index + 1) % 3, s, dt)[0], lowrank.exact(x, down, up, index, None, dt)[0],
+                 np.stack([s[a] * t16[i] @ up[a].T for i, a in enumerate(index)])]  # t rounded once, to 16 bits
+        for w in wrong:
+            assert (np.abs(w - d) > b).any()
