@@ -158,3 +158,42 @@ def test_combine_calls_that_are_right_reach_the_launch(vq):
 ])
 def test_combine_refusals(vq, error, kw):
     refused(vq, error, combine, vq, **kw())
+
+
+def lowrank(vq, **kw):
+    a = dict(base=dev(6, 48, dt=B), x=dev(6, 128, dt=B), down=dev(3, 16, 128, dt=B), up=dev(3, 48, 16, dt=B), index=dev(6, dt=I32),
+             scales=dev(3), out=dev(6, 48, dt=B), ws=dev(4096))
+    a.update(kw)
+    return vq.vq_lowrank_add(**a)
+
+
+def test_lowrank_calls_that_are_right_reach_the_launch(vq):
+    lowrank(vq)
+    lowrank(vq, base=dev(6, 48), out=dev(6, 50)[:, :48], scales=None)
+    lowrank(vq, x=dev(0, 128, dt=B), base=dev(0, 48, dt=B), out=dev(0, 48, dt=B), index=dev(0, dt=I32))
+    assert vq._lib.launched == ["vq_lowrank_add"] * 3
+
+
+@pytest.mark.parametrize("error,kw", [
+    (TypeError, lambda: dict(x=dev(6, 128))), (ValueError, lambda: dict(x=dev(128, 6, dt=B).t())),
+    (TypeError, lambda: dict(base=dev(6, 48, dt=H))), (ValueError, lambda: dict(base=dev(5, 48, dt=B))),
+    (TypeError, lambda: dict(down=dev(3, 16, 128, dt=H))), (ValueError, lambda: dict(down=dev(3, 16, 64, dt=B))),
+    (ValueError, lambda: dict(down=dev(48, 128, dt=B))), (ValueError, lambda: dict(up=dev(3, 16, 48, dt=B))),
+    (ValueError, lambda: dict(up=dev(2, 48, 16, dt=B))), (ValueError, lambda: dict(up=dev(3, 16, 48, dt=B).transpose(1, 2))),
+    (TypeError, lambda: dict(index=dev(6, dt=torch.int64))), (ValueError, lambda: dict(index=dev(5, dt=I32))),
+    (ValueError, lambda: dict(index=dev(7, dt=I32))), (TypeError, lambda: dict(index=torch.zeros(6, dtype=I32))),
+    (ValueError, lambda: dict(scales=dev(2))), (ValueError, lambda: dict(scales=dev(4))), (TypeError, lambda: dict(scales=dev(3, dt=B))),
+    (TypeError, lambda: dict(out=dev(6, 48))), (ValueError, lambda: dict(out=dev(6, 47, dt=B))),
+    (ValueError, lambda: dict(ws=dev(8))), (TypeError, lambda: dict(ws=dev(4096, dt=B))),
+])
+def test_lowrank_refusals(vq, error, kw):
+    refused(vq, error, lowrank, vq, **kw())
+
+
+def test_operands_without_rows_may_have_any_strides(vq):
+    """torch gives a tensor without elements strides that say nothing."""
+    x = torch.empty_strided((0, 128), (1, 7), dtype=B, device="cuda")
+    lowrank(vq, x=x, base=dev(0, 48, dt=B), out=dev(0, 48, dt=B), index=dev(0, dt=I32))
+    gated(vq, branch=x, residual=x, y=x, sum_out=x)
+    route(vq, scores=torch.empty_strided((0, 16), (1, 3), device="cuda"), rows=None, weights=None, experts=None, place=None)
+    assert len(vq._lib.launched) == 3
