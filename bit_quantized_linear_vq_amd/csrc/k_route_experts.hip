@@ -11,6 +11,7 @@
 //   k_route_place   offsets, and each choice's place: rows before it in its expert's segment, by
 //                   ascending token and choice.  Counts are whole numbers, so the order of their sums does not
 //                   matter, and places are the same in every call.
+//   k_route_few     both for up to 64 rows
 #include <algorithm>
 #include <type_traits>
 
@@ -33,294 +34,448 @@ struct RouteArgs {
   float* weights;   // [rows, top]
   int32_t* chosen;  // [rows, top]
   int32_t* place;   // [rows, top]
-  int32_t* counts;  // [blocks, experts]
+  int32_t* counts;  // [blocks, count_pitch], 16-byte aligned
 };
 
-constexpr int ROUTE_ROWS = 64;   // rows of a block of k_route_select
-constexpr double NONE = -__builtin_huge_val();
+constexpr int FEW_ROWS = 64;      // the most that one launch does
+constexpr int PLACE_TILE = 2048;  // choices that a workgroup places at a time: as many as 64 rows can have
 
-// The larger key, of equal ones that of the lower index, over LPR lanes (all of them get it).
-template <int LPR>
-__device__ __forceinline__ void best_of(double& key, int& at) {
-#pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) {
-    const double k2 = __shfl_xor(key, o, 64);
-    const int a2 = __shfl_xor(at, o, 64);
-    const bool take = k2 > key || (k2 == key && a2 < at);
-    key = take ? k2 : key;
-    at = take ? a2 : at;
+// All lanes of a row (LPR of them) get the same; register moves inside 16 lanes.
+template <typename K, int CTRL>
+__device__ __forceinline__ K moved(K v) {
+  if constexpr (sizeof(K) == 8) return dpp_d<CTRL>(v);
+  else return __builtin_bit_cast(K, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+template <int LPR, typename F>
+__device__ __forceinline__ void over_row(F&& step) {
+  step(std::integral_constant<int, 0xB1>{});   // quad_perm [1,0,3,2]
+  step(std::integral_constant<int, 0x4E>{});   // quad_perm [2,3,0,1]
+  step(std::integral_constant<int, 0x141>{});  // row_half_mirror
+  step(std::integral_constant<int, 0x140>{});  // row_mirror
+  if constexpr (LPR == 64) {
+    step(std::integral_constant<int, -16>{});
+    step(std::integral_constant<int, -32>{});
   }
 }
-template <int LPR>
-__device__ __forceinline__ double sum_of(double v) {
-#pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) v += __shfl_xor(v, o, 64);
+template <int CTRL, typename K>
+__device__ __forceinline__ K other(K v) {
+  if constexpr (CTRL < 0) return __shfl_xor(v, -CTRL, 64);
+  else return moved<K, CTRL>(v);
+}
+template <typename K>
+__device__ __forceinline__ K larger(K a, K b) {
+  return a > b ? a : b;
+}
+template <typename K>
+__device__ __forceinline__ K smaller(K a, K b) {
+  return a > b ? b : a;
+}
+template <int LPR, typename K>
+__device__ __forceinline__ K sum_of(K v) {
+  over_row<LPR>([&](auto c) { v += other<decltype(c)::value>(v); });
+  return v;
+}
+template <int LPR, typename K>
+__device__ __forceinline__ K max_of(K v) {
+  over_row<LPR>([&](auto c) { v = larger(other<decltype(c)::value>(v), v); });
   return v;
 }
 template <int LPR>
-__device__ __forceinline__ double max_of(double v) {
-#pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) v = fmax(v, __shfl_xor(v, o, 64));
+__device__ __forceinline__ int min_of(int v) {
+  over_row<LPR>([&](auto c) { v = min(v, other<decltype(c)::value>(v)); });
   return v;
 }
+// The row's lanes of a ballot, from bit 0.
 template <int LPR>
-__device__ __forceinline__ bool any_of(bool b) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ uint64_t row_ballot(bool b) {
   const uint64_t m = __ballot(b);
-  return LPR == 64 ? m != 0 : ((m >> (lane & ~(LPR - 1))) & ((1ull << (LPR & 63)) - 1)) != 0;
+  if constexpr (LPR == 64) return m;
+  else return (m >> (threadIdx.x & 63 & ~(LPR - 1))) & ((1ull << LPR) - 1);
 }
 
-// LPR lanes own a row, lane l the experts l + LPR i.
-template <int DT, int LPR, int VPT>
-__global__ __launch_bounds__(256) void k_route_select(RouteArgs a) {
-  extern __shared__ int s_count[];
-  for (int e = threadIdx.x; e < a.experts; e += 256) s_count[e] = 0;
-  __syncthreads();
-  const int l = threadIdx.x % LPR;
-  for (int r = threadIdx.x / LPR; r < ROUTE_ROWS; r += 256 / LPR) {
-    const int64_t row = (int64_t)blockIdx.x * ROUTE_ROWS + r;
-    if (__builtin_amdgcn_readfirstlane((int)(row < a.rows)) == 0) break;  // the wave's first row, then all
-    const bool row_ok = row < a.rows;
-    const int64_t rr = row_ok ? row : a.rows - 1;
-    double x[VPT], key[VPT];
-    double top = NONE;
-    bool bad = false;
+// e^x in float64: 2^n e^r with n = rne(x / ln 2), |r| <= ln 2 / 2, and e^r by its series to r^13
+// (the rest is below 2^-57 of it).  A third of the instructions of the library's function.
+__device__ __forceinline__ double exp_d(double x) {
+  x = fmin(fmax(x, -800.0), 800.0);  // beyond: 0 and infinity, as the true value rounds
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  // ln 2 = 190530846196 / 2^38 and a rest: n times the first is exact
+  double r = __builtin_fma(n, 190530846196.0 * -0x1p-38, x);
+  r = __builtin_fma(n, -1.64659495828970823e-12, r);
+  double p = 1.0 / 6227020800.0;
+  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+
+// What the choice goes by.  BY_SCORE: the scores themselves, exact in float32.  BY_P: p (+ bias), in
+// float64 for every expert.
+enum : int { BY_SCORE = 0, BY_P = 1 };
+
+// A row's choices: lane l of its LPR holds choices l and l + LPR (of experts l + LPR i, in the loop).
+// Returned: their experts (-1: none) and weights.
+template <int DT, int LPR, int VPT, int BY>
+__device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row, int l, int ch[2], float wt[2]) {
+  typedef typename std::conditional<BY == BY_P, double, float>::type K;
+  constexpr K NONE = -(K)__builtin_huge_val();
+  K key[VPT];
+  float top = -__builtin_huge_valf();
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int e = l + LPR * i;
+    const float x = e < a.experts ? load1<DT>(a.x, row * a.ldx + e) : -__builtin_huge_valf();
+    bad |= x != x || (a.softmax && x == __builtin_huge_valf());
+    top = x > top ? x : top;
+    key[i] = (K)x;
+  }
+  // Of a softmax that is divided by the sum of its chosen, the whole sum is not needed.
+  double base = 0.0, denom = 1.0;  // denom: its reciprocal in the end
+  if (a.softmax) {
+    top = max_of<LPR>(top);
+    base = top > -__builtin_huge_valf() ? (double)top : 0.0;
+    if (BY == BY_P || !a.renorm) {
+      denom = 0.0;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (l + LPR * i < a.experts) denom += exp_d((double)key[i] - base);
+      denom = sum_of<LPR>(denom);
+      denom = denom > 0.0 ? 1.0 / denom : 1.0;
+    }
+  }
+  auto p_of = [&](double x) { return a.softmax ? exp_d(x - base) * denom : 1.0 / (1.0 + exp_d(-x)); };
+  if constexpr (BY == BY_P) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int e = l + LPR * i;
-      x[i] = e < a.experts ? (double)load1<DT>(a.x, rr * a.ldx + e) : NONE;
-      bad |= x[i] != x[i] || (a.softmax && x[i] == -NONE);
-      top = fmax(top, x[i]);
-    }
-    // p in x's place
-    double denom = 1.0;
-    if (a.softmax) {
-      top = max_of<LPR>(top);
-      const double base = top == NONE ? 0.0 : top;
-      denom = 0.0;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        key[i] = x[i];
-        x[i] = exp(x[i] - base);
-        denom += x[i];
-      }
-      denom = sum_of<LPR>(denom);
-      denom = denom > 0.0 ? denom : 1.0;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) x[i] = x[i] / denom;
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        key[i] = x[i];
-        x[i] = 1.0 / (1.0 + exp(-x[i]));
-      }
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int e = l + LPR * i;
-        if (e < a.experts) {
-          const double k = x[i] + (double)a.bias[e];
-          key[i] = key[i] == NONE ? NONE : k;
-          bad |= key[i] != key[i];
-        }
-      }
-    }
-    bad = any_of<LPR>(bad);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) key[i] = bad ? NONE : key[i];
-    if (a.groups > 1) {
-      // Group after group its mark, then the groups that stay, then the others' keys away.
-      const int size = a.experts / a.groups;
-      const bool by_p = a.best == 2 && !a.bias;
-      double mark = NONE;  // lane g of the row holds group g's, g + LPR the next one ..
-      double marks[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) marks[j] = NONE;
-      for (int g = 0; g < a.groups; ++g) {
-        double k1 = NONE;
-        int at = 1 << 30;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int e = l + LPR * i;
-          if (e / size != g || e >= a.experts) continue;
-          const double k = by_p && key[i] != NONE ? x[i] : key[i];
-          if (k > k1) {
-            k1 = k;
-            at = e;
-          }
-        }
-        best_of<LPR>(k1, at);
-        mark = k1;
-        if (a.best == 2 && size > 1) {
-          double k2 = NONE;
-#pragma unroll
-          for (int i = 0; i < VPT; ++i) {
-            const int e = l + LPR * i;
-            if (e / size != g || e >= a.experts || e == at) continue;
-            const double k = by_p && key[i] != NONE ? x[i] : key[i];
-            k2 = fmax(k2, k);
-          }
-          k2 = max_of<LPR>(k2);
-          mark += k2 == NONE ? 0.0 : k2;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (g == l + LPR * j) marks[j] = mark;
-      }
-      uint64_t kept = 0;
-      for (int n = 0; n < a.keep; ++n) {
-        double k1 = NONE;
-        int at = 1 << 30;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int g = l + LPR * j;
-          if (g < a.groups && !((kept >> g) & 1) && (marks[j] > k1 || at == 1 << 30)) {
-            k1 = marks[j];
-            at = g;
-          }
-        }
-        best_of<LPR>(k1, at);
-        kept |= 1ull << at;
-      }
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int e = l + LPR * i;
-        if (e < a.experts && !((kept >> (e / size)) & 1)) key[i] = NONE;
-      }
-    }
-    // Choice after choice; lane j of the row keeps choice j (and j + LPR).
-    double w[2] = {0.0, 0.0}, total = 0.0;
-    int ch[2] = {-1, -1};
-    for (int n = 0; n < a.top; ++n) {
-      double k1 = NONE;
-      int at = 1 << 30;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (key[i] > k1) {
-          k1 = key[i];
-          at = l + LPR * i;
-        }
-      best_of<LPR>(k1, at);
-      if (k1 == NONE) break;  // the same in all lanes of the row
-      double p = 0.0;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (at == l + LPR * i) {
-          p = x[i];
-          key[i] = NONE;
-        }
-      p = sum_of<LPR>(p);
-      total += p;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (n == l + LPR * j) {
-          w[j] = p;
-          ch[j] = at;
-        }
-    }
-    if (row_ok) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = l + LPR * j;
-        if (n >= a.top) continue;
-        double v = a.renorm ? (total > 0.0 ? w[j] / total : 0.0) : w[j];
-        if (bad) v = __builtin_nan("");
-        a.weights[row * a.top + n] = (float)(v * (double)a.scale);
-        a.chosen[row * a.top + n] = ch[j];
-        if (ch[j] >= 0) atomicAdd(&s_count[ch[j]], 1);
-      }
+      if (e >= a.experts || key[i] == NONE) continue;
+      // (by p without a bias the groups go by p, the choice in them by the scores: key stays)
+      if (a.bias) key[i] = p_of(key[i]) + (double)a.bias[e];
+      bad |= key[i] != key[i];
     }
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += 256) a.counts[(int64_t)blockIdx.x * a.experts + e] = s_count[e];
+  bad = row_ballot<LPR>(bad) != 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) key[i] = bad ? NONE : key[i];
+  if (a.groups > 1) {
+    const int size = a.experts / a.groups;
+    const float inv = 1.0f / (float)size;
+    // of at most 1024 experts: half a member off a whole number is more than float32's error
+    auto group_of = [&](int i) { return (int)(((float)(l + LPR * i) + 0.5f) * inv); };
+    K p[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      p[i] = key[i];
+      if constexpr (BY == BY_P)
+        if (!a.bias && key[i] != NONE) p[i] = p_of(key[i]);
+    }
+    constexpr int SLOTS = 64 / LPR;
+    K marks[SLOTS];
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) marks[j] = NONE;
+    // Four groups at a time: their reductions do not wait for each other.
+    for (int g0 = 0; g0 < a.groups; g0 += 4) {
+      K m1[4], m2[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) m1[u] = m2[u] = NONE;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int gi = group_of(i) - g0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const K k = gi == u ? p[i] : NONE;
+          if (BY == BY_P) m2[u] = larger(smaller(k, m1[u]), m2[u]);
+          m1[u] = larger(k, m1[u]);
+        }
+      }
+      over_row<LPR>([&](auto c) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const K o1 = other<decltype(c)::value>(m1[u]);
+          if constexpr (BY == BY_P) m2[u] = larger(smaller(o1, m1[u]), larger(other<decltype(c)::value>(m2[u]), m2[u]));
+          m1[u] = larger(o1, m1[u]);
+        }
+      });
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (a.best == 2 && m2[u] != NONE) m1[u] += m2[u];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) marks[j] = g0 + u == l + LPR * j ? m1[u] : marks[j];
+      }
+    }
+    // A group stays if fewer than `keep` are above it (or level with it and before it).
+    int above[SLOTS] = {};
+    const int lane0 = threadIdx.x & 63 & ~(LPR - 1);
+#pragma unroll 4
+    for (int h = 0; h < a.groups; ++h) {
+      K m = marks[0];
+#pragma unroll
+      for (int j = 1; j < SLOTS; ++j) m = h / LPR == j ? marks[j] : m;
+      m = __shfl(m, lane0 + h % LPR, 64);
+#pragma unroll
+      for (int j = 0; j < SLOTS; ++j) above[j] += m > marks[j] || (m == marks[j] && h < l + LPR * j);
+    }
+    uint64_t kept = 0;
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) kept |= row_ballot<LPR>(above[j] < a.keep) << (LPR * j & 63);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (!((kept >> (group_of(i) & 63)) & 1)) key[i] = NONE;
+  }
+  ch[0] = ch[1] = -1;
+  for (int n = 0; n < a.top; ++n) {
+    K k1 = key[0];
+#pragma unroll
+    for (int i = 1; i < VPT; ++i) k1 = key[i] > k1 ? key[i] : k1;
+    k1 = max_of<LPR>(k1);
+    if (k1 == NONE) break;  // the same in all lanes of the row
+    int at = 1 << 30;
+#pragma unroll
+    for (int i = VPT - 1; i >= 0; --i) at = key[i] == k1 ? l + LPR * i : at;
+    at = min_of<LPR>(at);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) key[i] = at == l + LPR * i ? NONE : key[i];
+    ch[0] = n == l ? at : ch[0];
+    ch[1] = n == l + LPR ? at : ch[1];
+  }
+  double w[2], total = 0.0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    w[j] = 0.0;
+    if (ch[j] >= 0) w[j] = p_of((double)load1<DT>(a.x, row * a.ldx + ch[j]));
+    total += w[j];
+  }
+  if (a.renorm) {
+    total = sum_of<LPR>(total);
+    const double by = total > 0.0 ? total : 1.0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) w[j] = w[j] / by;
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) wt[j] = bad ? bits_f(0x7FC00000u) : (float)(w[j] * (double)a.scale);
 }
 
-// A block places the choices of `span` blocks of k_route_select: its waves take consecutive pieces of
-// them, count their experts, and go through them 64 at a time.
-__global__ __launch_bounds__(1024) void k_route_place(RouteArgs a, int blocks, int span) {
-  extern __shared__ int s_mem[];
-  const int E = a.experts;
-  int* s_base = s_mem;          // [E]: where this block's first choice of an expert goes
-  int* s_off = s_mem + E;       // [E + 1]
-  int* s_wave = s_off + E + 1;  // [waves][E]
-  const int waves = blockDim.x >> 6;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b0 = blockIdx.x * span;
-  for (int e = tid; e < E; e += blockDim.x) {
-    int before = 0, all = 0;
-    for (int b = 0; b < blocks; ++b) {
-      const int c = a.counts[(int64_t)b * E + e];
-      before += b < b0 ? c : 0;
-      all += c;
-    }
-    s_base[e] = before;
-    s_off[e] = all;
-  }
-  for (int i = tid; i < waves * E; i += blockDim.x) s_wave[i] = 0;
-  __syncthreads();
-  if (wave == 0) {
-    int run = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      const int e = e0 + lane;
-      const int c = e < E ? s_off[e] : 0;
-      int inc = c;
+// Weights and choices of a row, stored; its choices counted in LDS.
+template <int LPR>
+__device__ __forceinline__ void store_row(const RouteArgs& a, int64_t row, int l, const int ch[2], const float wt[2],
+                                          int* s_count) {
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(inc, o, 64);
-        if (lane >= o) inc += u;
-      }
-      if (e < E) s_off[e] = run + inc - c;
-      run += __shfl(inc, 63, 64);
+  for (int j = 0; j < 2; ++j) {
+    const int n = l + LPR * j;
+    if (n >= a.top) continue;
+    a.weights[row * a.top + n] = wt[j];
+    a.chosen[row * a.top + n] = ch[j];
+    if (ch[j] >= 0) atomicAdd(&s_count[ch[j]], 1);
+  }
+}
+
+// Counts of a block are a row of 4-aligned length.
+__device__ __forceinline__ int count_pitch(int experts) { return (experts + 3) & ~3; }
+
+template <int DT, int LPR, int VPT, int BY>
+__global__ __launch_bounds__(1024) void k_route_select(RouteArgs a, int rows) {
+  extern __shared__ int s_count[];
+  const int pitch = count_pitch(a.experts);
+  for (int e = threadIdx.x; e < pitch; e += blockDim.x) s_count[e] = 0;
+  __syncthreads();
+  const int l = threadIdx.x % LPR;
+  for (int r = threadIdx.x / LPR; r < rows; r += blockDim.x / LPR) {
+    const int64_t row = (int64_t)blockIdx.x * rows + r;
+    if (__builtin_amdgcn_readfirstlane((int)(row < a.rows)) == 0) break;  // the wave's first row, then all
+    int ch[2];
+    float wt[2];
+    route_row<DT, LPR, VPT, BY>(a, min(row, a.rows - 1), l, ch, wt);
+    if (row < a.rows) store_row<LPR>(a, row, l, ch, wt, s_count);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < pitch; e += blockDim.x) a.counts[(int64_t)blockIdx.x * pitch + e] = s_count[e];
+}
+
+// Exclusive sums of s_off[0..E) in place, their total in s_off[E]; by one wave.
+__device__ __forceinline__ void offsets_of(int* s_off, int E) {
+  const int lane = threadIdx.x & 63;
+  int run = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int c = e < E ? s_off[e] : 0;
+    int inc = c;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(inc, o, 64);
+      if (lane >= o) inc += u;
     }
-    if (lane == 0) s_off[E] = run;
+    if (e < E) s_off[e] = run + inc - c;
+    run += __shfl(inc, 63, 64);
   }
-  __syncthreads();
-  const int64_t all = a.rows * a.top;
-  const int64_t first = (int64_t)b0 * ROUTE_ROWS * a.top;
-  const int64_t last = min(all, first + (int64_t)span * ROUTE_ROWS * a.top);
-  const int64_t each = (last - first + waves - 1) / waves;
-  const int64_t w0 = min(last, first + each * wave), w1 = min(last, w0 + each);
-  for (int64_t c = w0 + lane; c < w1; c += 64) {
-    const int e = a.chosen[c];
-    if (e >= 0) atomicAdd(&s_wave[wave * E + e], 1);
+  if (lane == 0) s_off[E] = run;
+}
+
+// Choices [first, last) of a workgroup: its waves take consecutive pieces, a lane up to four of them, 64
+// apart.  e: their experts (-1: none); rank: how many of the wave's choices before go to the
+// same; s_wave [waves][E], zero before, holds the waves' counts afterwards.
+constexpr int PLACE_PER = 4;
+struct Choices {
+  int64_t at[PLACE_PER];
+  int e[PLACE_PER], rank[PLACE_PER];
+};
+__device__ __forceinline__ void load_choices(const RouteArgs& a, int64_t first, int64_t last, Choices& c) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int64_t each = ((last - first + waves - 1) / waves + 63) / 64 * 64;
+#pragma unroll
+  for (int j = 0; j < PLACE_PER; ++j) {
+    const int64_t at = first + each * wave + 64 * j + lane;
+    c.at[j] = 64 * j < each && at < last ? at : -1;
+    c.e[j] = c.at[j] >= 0 ? a.chosen[at] : -1;
   }
-  __syncthreads();
-  for (int e = tid; e < E; e += blockDim.x) {
-    int at = s_off[e] + s_base[e];
-    for (int w = 0; w < waves; ++w) {
-      const int c = s_wave[w * E + e];
-      s_wave[w * E + e] = at;
-      at += c;
-    }
-  }
-  __syncthreads();
-  volatile int* mine = s_wave + wave * E;
-  for (int64_t c0 = w0; c0 < w1; c0 += 64) {
-    const int64_t c = c0 + lane;
-    const int e = c < w1 ? a.chosen[c] : -1;
-    // The lanes with this lane's expert.
+}
+__device__ __forceinline__ void rank_choices(int E, Choices& c, int* s_wave) {
+  const int lane = threadIdx.x & 63;
+  int* mine = s_wave + (threadIdx.x >> 6) * E;
+#pragma unroll
+  for (int j = 0; j < PLACE_PER; ++j) {
+    const int e = c.e[j];
     uint64_t same = __ballot(e >= 0);
+    if (!same) continue;
+    // The lanes with this lane's expert.
     for (int bit = 0; (1 << bit) < E; ++bit) {
       const uint64_t m = __ballot((e >> bit) & 1);
       same &= ((e >> bit) & 1) ? m : ~m;
     }
-    const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
-    int at = -1;
-    if (e >= 0) at = mine[e] + rank;
-    __builtin_amdgcn_wave_barrier();
-    if (e >= 0 && rank == 0) mine[e] = at + __builtin_popcountll(same);
-    __builtin_amdgcn_wave_barrier();
-    if (c < w1) {
-      a.place[c] = at;
-      if (e >= 0) a.row_of[at] = (int)(c / a.top);
+    const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
+    int old = 0;
+    if (e >= 0 && before == 0) old = atomicAdd(&mine[e], __builtin_popcountll(same));
+    old = __shfl(old, e >= 0 ? __builtin_ctzll(same) : 0, 64);
+    c.rank[j] = old + before;
+  }
+}
+// The waves' counts to where each wave's first choice of an expert goes; s_next: the workgroup's first,
+// afterwards the next one's.
+__device__ __forceinline__ void start_waves(int E, int* s_next, int* s_wave) {
+  const int waves = blockDim.x >> 6;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int n = s_next[e];
+#pragma unroll 4
+    for (int w = 0; w < waves; ++w) {
+      const int c = s_wave[w * E + e];
+      s_wave[w * E + e] = n;
+      n += c;
+    }
+    s_next[e] = n;
+  }
+}
+__device__ __forceinline__ void store_places(const RouteArgs& a, const Choices& c, const int* s_wave) {
+  const int* mine = s_wave + (threadIdx.x >> 6) * a.experts;
+#pragma unroll
+  for (int j = 0; j < PLACE_PER; ++j) {
+    if (c.at[j] < 0) continue;
+    const int e = c.e[j];
+    const int to = e >= 0 ? mine[e] + c.rank[j] : -1;
+    a.place[c.at[j]] = to;
+    if (e >= 0) a.row_of[to] = (int)((unsigned)c.at[j] / (unsigned)a.top);
+  }
+}
+
+// A block places the choices of `span` blocks of k_route_select (`rows` rows each), after adding up
+// everyone's counts.
+__global__ __launch_bounds__(1024) void k_route_place(RouteArgs a, int blocks, int rows, int span) {
+  extern __shared__ int s_mem[];
+  const int E = a.experts, pitch = count_pitch(E);
+  int* s_next = s_mem;              // [pitch]: counts of the blocks before, then where the tile's first goes
+  int* s_off = s_mem + pitch;       // [pitch + 4]
+  int* s_wave = s_off + pitch + 4;  // [waves][E]
+  const int tid = threadIdx.x, waves = blockDim.x >> 6;
+  const int b0 = blockIdx.x * span;
+  const int64_t total = a.rows * a.top;
+  int64_t first = (int64_t)b0 * rows * a.top;
+  const int64_t last = min(total, first + (int64_t)span * rows * a.top);
+  Choices c;
+  load_choices(a, first, min(last, first + PLACE_TILE), c);
+  // Threads take four experts and every parts-th block.
+  const int quads = pitch / 4, parts = max(1, (int)blockDim.x / quads);
+  const int part = tid / quads, q = tid - part * quads;
+  v4i before = v4i{}, all = v4i{};
+  if (part < parts) {
+#pragma unroll 8
+    for (int b = part; b < blocks; b += parts) {
+      const v4i n = *reinterpret_cast<const v4i*>(a.counts + (int64_t)b * pitch + 4 * q);
+      before += b < b0 ? n : v4i{};
+      all += n;
     }
   }
+  for (int e = tid; e < 2 * pitch + 4 + waves * E; e += blockDim.x) s_mem[e] = 0;
+  __syncthreads();
+  if (part < parts) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      atomicAdd(&s_next[4 * q + i], before[i]);
+      atomicAdd(&s_off[4 * q + i], all[i]);
+    }
+  }
+  rank_choices(E, c, s_wave);
+  __syncthreads();
+  if (tid < 64) offsets_of(s_off, E);
+  __syncthreads();
+  for (int e = tid; e < E; e += blockDim.x) s_next[e] += s_off[e];
   if (blockIdx.x == 0)
     for (int e = tid; e <= E; e += blockDim.x) a.offsets[e] = s_off[e];
   // Places that no choice takes, behind the last expert's rows.
-  for (int64_t c = s_off[E] + (int64_t)blockIdx.x * blockDim.x + tid; c < all; c += (int64_t)gridDim.x * blockDim.x)
-    a.row_of[c] = -1;
+  for (int64_t r = s_off[E] + (int64_t)blockIdx.x * blockDim.x + tid; r < total; r += (int64_t)gridDim.x * blockDim.x)
+    a.row_of[r] = -1;
+  for (;;) {
+    __syncthreads();
+    start_waves(E, s_next, s_wave);
+    __syncthreads();
+    store_places(a, c, s_wave);
+    first += PLACE_TILE;
+    if (first >= last) return;
+    load_choices(a, first, min(last, first + PLACE_TILE), c);
+    __syncthreads();
+    for (int e = tid; e < waves * E; e += blockDim.x) s_wave[e] = 0;
+    __syncthreads();
+    rank_choices(E, c, s_wave);
+  }
+}
+
+// Few rows: choices, counts and places by one workgroup, in one launch.
+template <int DT, int LPR, int VPT, int BY>
+__global__ __launch_bounds__(1024) void k_route_few(RouteArgs a) {
+  extern __shared__ int s_mem[];
+  const int E = a.experts, pitch = count_pitch(E);
+  int* s_off = s_mem;               // [pitch + 4]
+  int* s_wave = s_mem + pitch + 4;  // [waves][E]
+  for (int e = threadIdx.x; e < pitch + 4 + ((int)blockDim.x >> 6) * E; e += blockDim.x) s_mem[e] = 0;
+  __syncthreads();
+  const int l = threadIdx.x % LPR;
+  for (int row = threadIdx.x / LPR; row < FEW_ROWS; row += blockDim.x / LPR) {
+    if (__builtin_amdgcn_readfirstlane((int)(row < a.rows)) == 0) break;
+    int ch[2];
+    float wt[2];
+    route_row<DT, LPR, VPT, BY>(a, min((int64_t)row, a.rows - 1), l, ch, wt);
+    if (row < a.rows) store_row<LPR>(a, row, l, ch, wt, s_off);
+  }
+  __syncthreads();
+  const int64_t all = a.rows * a.top;
+  Choices c;
+  load_choices(a, 0, all, c);
+  if (threadIdx.x < 64) offsets_of(s_off, E);
+  rank_choices(E, c, s_wave);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) a.offsets[e] = s_off[e];
+  __syncthreads();
+  start_waves(E, s_off, s_wave);
+  __syncthreads();
+  store_places(a, c, s_wave);
+  for (int64_t c = s_off[E] + threadIdx.x; c < all; c += blockDim.x) a.row_of[c] = -1;
 }
 
 // out[i] = RNE(res[i] + gate * sum_j w[i, j] y[place[i, j]]): a thread owns eight elements of a row.
@@ -412,20 +567,49 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs a, int pieces) {
   }
 }
 
-template <int DT>
-static void launch_select(const RouteArgs& a, int blocks, hipStream_t st) {
-  const size_t lds = 4 * (size_t)a.experts;
+// Waves of a workgroup that places: its [waves][experts] counts within the 64 KiB of a launch without more.
+static int place_waves(int experts) { return experts <= 512 ? 16 : 8; }
+static size_t pitch_bytes(int experts) { return 4 * (size_t)((experts + 3) & ~3); }
+
+template <int DT, int BY>
+static void launch_select(const RouteArgs& a, int blocks, int rows, hipStream_t st) {
   auto go = [&](auto lpr, auto vpt) {
-    hipLaunchKernelGGL((k_route_select<DT, decltype(lpr)::value, decltype(vpt)::value>), dim3(blocks), dim3(256), lds, st, a);
+    constexpr int L = decltype(lpr)::value, V = decltype(vpt)::value;
+    if (!rows) {
+      const int block = std::min(64 * place_waves(a.experts), ((int)a.rows * L + 63) / 64 * 64);
+      const size_t lds = pitch_bytes(a.experts) + 16 + 4 * (size_t)(block / 64) * a.experts;
+      hipLaunchKernelGGL((k_route_few<DT, L, V, BY>), dim3(1), dim3(block), lds, st, a);
+    } else {
+      hipLaunchKernelGGL((k_route_select<DT, L, V, BY>), dim3(blocks), dim3(std::min(1024, rows * L)), pitch_bytes(a.experts),
+                         st, a, rows);
+    }
   };
   const int e = a.experts;
-  if (e <= 16) go(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-  else if (e <= 32) go(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-  else if (e <= 64) go(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
-  else if (e <= 128) go(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
-  else if (e <= 256) go(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
-  else if (e <= 512) go(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
-  else go(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+  const std::integral_constant<int, 16> quarter;
+  const std::integral_constant<int, 64> wave;
+  if (e <= 16) go(quarter, std::integral_constant<int, 1>{});
+  else if (e <= 32) go(quarter, std::integral_constant<int, 2>{});
+  else if (e <= 64) go(quarter, std::integral_constant<int, 4>{});
+  else if (e <= 96) go(quarter, std::integral_constant<int, 6>{});
+  else if (e <= 128) go(quarter, std::integral_constant<int, 8>{});
+  else if (e <= 160) go(quarter, std::integral_constant<int, 10>{});
+  else if (e <= 192) go(quarter, std::integral_constant<int, 12>{});
+  else if (e <= 256) go(quarter, std::integral_constant<int, 16>{});
+  else if (e <= 512) go(wave, std::integral_constant<int, 8>{});
+  else go(wave, std::integral_constant<int, 16>{});
+}
+template <int DT>
+static void launch_select_by(const RouteArgs& a, int blocks, int rows, hipStream_t st) {
+  if (a.bias || (a.groups > 1 && a.best == 2)) launch_select<DT, BY_P>(a, blocks, rows, st);
+  else launch_select<DT, BY_SCORE>(a, blocks, rows, st);
+}
+
+// Rows of a block of k_route_select, 0 where one launch does all: as many (in sixteens, a wave a SIMD) as
+// share the rows out over the compute units.
+static int select_rows(int64_t rows) {
+  if (rows <= FEW_ROWS) return 0;
+  const int64_t cus = vq_internal::persistent_blocks();
+  return (int)(((rows + cus - 1) / cus + 15) / 16 * 16);
 }
 
 }  // namespace vqk
@@ -434,7 +618,10 @@ namespace vq_internal {
 
 using namespace vqk;
 
-int64_t route_experts_blocks(int64_t rows) { return (rows + ROUTE_ROWS - 1) / ROUTE_ROWS; }
+int64_t route_experts_workspace_elems(int64_t rows, int64_t experts) {
+  const int per = select_rows(rows);
+  return per ? (rows + per - 1) / per * ((experts + 3) & ~3) : 0;
+}
 
 hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st) {
   RouteArgs a{};
@@ -456,18 +643,20 @@ hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st) {
   a.chosen = p.chosen;
   a.place = p.place;
   a.counts = p.counts;
-  const int blocks = (int)route_experts_blocks(p.rows);
-  if (blocks) {
-    if (p.dtype == DT_F16) launch_select<DT_F16>(a, blocks, st);
-    else if (p.dtype == DT_BF16) launch_select<DT_BF16>(a, blocks, st);
-    else launch_select<DT_F32>(a, blocks, st);
+  const int rows = select_rows(p.rows);
+  const int blocks = rows ? (int)((p.rows + rows - 1) / rows) : 0;
+  if (p.rows) {
+    if (p.dtype == DT_F16) launch_select_by<DT_F16>(a, blocks, rows, st);
+    else if (p.dtype == DT_BF16) launch_select_by<DT_BF16>(a, blocks, rows, st);
+    else launch_select_by<DT_F32>(a, blocks, rows, st);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || !rows) return e;
   }
-  const int span = 4, grid = std::max(1, (blocks + span - 1) / span);
-  // [waves][experts] counts within the 64 KiB of a launch without more
-  const int waves = p.experts <= 512 ? 16 : 8;
-  hipLaunchKernelGGL(k_route_place, dim3(grid), dim3(64 * waves), 4 * ((waves + 2) * (size_t)p.experts + 1), st, a, blocks, span);
+  // Blocks of choices to place in one tile, where they fit one (without rows: zero offsets alone).
+  const int span = std::max(1, PLACE_TILE / std::max(1, rows * p.top)), grid = std::max(1, (blocks + span - 1) / span);
+  const int waves = place_waves(p.experts);
+  const size_t lds = 2 * pitch_bytes(p.experts) + 16 + 4 * (size_t)waves * p.experts;
+  hipLaunchKernelGGL(k_route_place, dim3(grid), dim3(64 * waves), lds, st, a, blocks, std::max(1, rows), span);
   return hipGetLastError();
 }
 

@@ -777,7 +777,7 @@ bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t
 
 int64_t vq_route_experts_workspace_elems(int64_t m, int64_t experts) {
   if (m < 0 || m > kMaxExpertRows || experts < 1 || experts > kMaxExperts) return 0;
-  return std::max<int64_t>(1, vq_internal::route_experts_blocks(m) * experts);
+  return std::max<int64_t>(1, vq_internal::route_experts_workspace_elems(m, experts));
 }
 
 vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t experts, int64_t ldx, vq_score score,
@@ -793,7 +793,7 @@ vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t expert
   if (experts > kMaxExperts || top > kMaxTop || groups > kMaxGroups || m > kMaxExpertRows / top)
     return VQ_ERR_UNSUPPORTED;
   if (misaligned(x, elem_size(dt)) || misaligned(bias, 4) || misaligned(offsets, 4) || misaligned(rows, 4) ||
-      misaligned(weights, 4) || misaligned(chosen, 4) || misaligned(place, 4) || misaligned(ws, 4))
+      misaligned(weights, 4) || misaligned(chosen, 4) || misaligned(place, 4) || !aligned16(ws))
     return VQ_ERR_SHAPE;
   vq_internal::RouteExpertsParams p{};
   p.x = x;

@@ -167,9 +167,9 @@ struct RouteExpertsParams {
   float* weights;
   int32_t* chosen;
   int32_t* place;
-  int32_t* counts;  // route_experts_blocks(rows) * experts
+  int32_t* counts;  // route_experts_workspace_elems
 };
-int64_t route_experts_blocks(int64_t rows);
+int64_t route_experts_workspace_elems(int64_t rows, int64_t experts);
 hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st);
 struct CombineParams {
   const void* y;

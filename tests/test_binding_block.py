@@ -125,8 +125,8 @@ def test_route_calls_that_are_right_reach_the_launch(vq):
     (ValueError, lambda: dict(bias=dev(15))), (ValueError, lambda: dict(bias=dev(17))), (TypeError, lambda: dict(bias=dev(16, dt=H))),
     (ValueError, lambda: dict(offsets=dev(16, dt=I32))), (TypeError, lambda: dict(offsets=dev(17))),
     (ValueError, lambda: dict(rows=dev(6, 2, dt=I32))), (ValueError, lambda: dict(weights=dev(2, 6))),
-    (ValueError, lambda: dict(weights=dev(2, 6).t())), (TypeError, lambda: dict(experts=dev(6, 2))),
-    (TypeError, lambda: dict(place=torch.empty(6, 2, dtype=I32))), (ValueError, lambda: dict(ws=dev(15, dt=I32))),
+    (ValueError, lambda: dict(weights=dev(2, 6).t())), (TypeError, lambda: dict(experts=dev(6, 2))), (TypeError, lambda: dict(ws=dev(64))),
+    (TypeError, lambda: dict(place=torch.empty(6, 2, dtype=I32))), (ValueError, lambda: dict(ws=dev(0, dt=I32))),
 ])
 def test_route_refusals(vq, error, kw):
     refused(vq, error, route, vq, **kw())
