@@ -142,188 +142,228 @@ __global__ __launch_bounds__(256) void k_lowrank_down(LowrankArgs g) {
   }
 }
 
-// Eight elements of a row, cnt of them inside it.
+#ifndef UP_MB
+#define UP_MB 2
+#define UP_NP 2
+#define UP_MANY 1024
+#endif
+// Eight elements of a row, cnt of them inside it, and what they are with v added.
 template <int DT>
-__device__ __forceinline__ void out_row8(const void* base, void* out, int64_t bi, int64_t oi, int cnt, bool any,
-                                         const float* v) {
-  if constexpr (DT == DT_F32) {
-    const float* b = reinterpret_cast<const float*>(base) + bi;
-    float* o = reinterpret_cast<float*>(out) + oi;
-    if (cnt == 8) {
-      const v4f_el* q = reinterpret_cast<const v4f_el*>(b);
-      v4f q0 = q[0], q1 = q[1];
-      if (any) {
+struct Row8 {
+  typename std::conditional<DT == DT_F32, v4f, u4v>::type q[DT == DT_F32 ? 2 : 1];
+
+  __device__ __forceinline__ void load(const void* base, int64_t at, int cnt) {
+    if constexpr (DT == DT_F32) {
+      const float* b = reinterpret_cast<const float*>(base) + at;
+      if (cnt == 8) {
+        q[0] = reinterpret_cast<const v4f_el*>(b)[0];
+        q[1] = reinterpret_cast<const v4f_el*>(b)[1];
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          q0[i] = q0[i] + v[i];
-          q1[i] = q1[i] + v[4 + i];
-        }
+        for (int i = 0; i < 8; ++i) q[i >> 2][i & 3] = i < cnt ? b[i] : 0.0f;
       }
-      reinterpret_cast<v4f_el*>(o)[0] = q0;
-      reinterpret_cast<v4f_el*>(o)[1] = q1;
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < cnt) o[i] = any ? b[i] + v[i] : b[i];
+      const uint16_t* b = reinterpret_cast<const uint16_t*>(base) + at;
+      q[0] = cnt == 8 ? load8<false, false>(b, 8) : load8<true, false>(b, cnt);
     }
-  } else {
-    const uint16_t* b = reinterpret_cast<const uint16_t*>(base) + bi;
-    uint16_t* o = reinterpret_cast<uint16_t*>(out) + oi;
-    u4v q = cnt == 8 ? load8<false, false>(b, 8) : load8<true, false>(b, cnt);
-    if (any) {
+  }
+  __device__ __forceinline__ void add(const float* v) {
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i >> 2][i & 3] = q[i >> 2][i & 3] + v[i];
+    } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float b0, b1;
-        decode2<DT>(q[i], b0, b1);
-        q[i] = cvt_pair<DT>(b0 + v[2 * i], b1 + v[2 * i + 1]);
+        decode2<DT>(q[0][i], b0, b1);
+        q[0][i] = cvt_pair<DT>(b0 + v[2 * i], b1 + v[2 * i + 1]);
       }
     }
-    if (cnt == 8) store8<false, false>(o, q, 8);
-    else store8<true, false>(o, q, cnt);
   }
-}
+  __device__ __forceinline__ void store(void* out, int64_t at, int cnt) const {
+    if constexpr (DT == DT_F32) {
+      float* o = reinterpret_cast<float*>(out) + at;
+      if (cnt == 8) {
+        reinterpret_cast<v4f_el*>(o)[0] = q[0];
+        reinterpret_cast<v4f_el*>(o)[1] = q[1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < cnt) o[i] = q[i >> 2][i & 3];
+      }
+    } else {
+      uint16_t* o = reinterpret_cast<uint16_t*>(out) + at;
+      if (cnt == 8) store8<false, false>(o, q[0], 8);
+      else store8<true, false>(o, q[0], cnt);
+    }
+  }
+};
 
-constexpr int UP_COLS = 32;  // columns of a wave at a time: two blocks of 16
-
-// 16 MB rows a workgroup, its waves side by side, `each` times 32 columns one after the other.
-template <int DT, int OUT_DT, int MB>
-__global__ __launch_bounds__(256) void k_lowrank_up(LowrankArgs g, int each) {
+// Waves side by side, each 16 MB rows by 32 NP columns.  RS: steps of 32 of the rank.  DU: adapters whose
+// rows of up are on their way at once.  LINES: the sums change places through LDS, so that a load of
+// base and a store of out cover whole 128-byte lines of eight rows (from the product's own
+// layout they cover 64 bytes of sixteen rows).
+template <int DT, int OUT_DT, int MB, int NP, int RS, int DU, bool LINES>
+__global__ __launch_bounds__(256) void k_lowrank_up(LowrankArgs g) {
   typedef typename Half<DT>::V8 V8;
-  extern __shared__ __attribute__((aligned(16))) uint16_t s_t[];  // hi then lo, [16 MB][rp] each
-  __shared__ float s_back[16 * MB];
+  static_assert(!LINES || NP == 2, "eight lanes of eight columns a row");
+  constexpr int COLS = 32 * NP, PITCH = COLS + 4;
+  extern __shared__ __attribute__((aligned(16))) float s_sum[];  // LINES: [waves][16 MB][PITCH]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
   const int rl = lane & 15, kq = lane >> 4;
   const int64_t r0 = (int64_t)(blockIdx.x / g.col_tiles) * (16 * MB);
-  const int n_first = (int)(blockIdx.x % g.col_tiles) * (UP_COLS * waves * each) + UP_COLS * each * wave;
-  const int rp = (g.rank + 31) / 32 * 32;
-  uint16_t* s_lo = s_t + 16 * MB * rp;
+  const int n0 = ((int)(blockIdx.x % g.col_tiles) * (int)(blockDim.x >> 6) + wave) * COLS;
+  if (n0 >= g.n) return;
 
-  // t of the tile's rows: parts summed, scaled, in two pieces.  Sixteen lanes a row.
-  for (int r = threadIdx.x >> 4; r < 16 * MB; r += blockDim.x >> 4) {
-    const int64_t row = r0 + r;
-    const int a = adapter_of(g, row);
-    const float sc = a >= 0 && g.scale ? g.scale[a] : 1.0f;
-    constexpr int CH = 2;  // chunks of four a lane: rank up to 128
-    float v[CH][4];
+  // Piece j of the lane's outputs: its row in the tile and its column.
+  auto row_of = [&](int j) { return LINES ? 8 * j + (lane >> 3) : 16 * (j / NP) + rl; };
+  auto col_of = [&](int j) { return n0 + (LINES ? 8 * (lane & 7) : 32 * (j % NP) + 8 * kq); };
+  int mine[MB];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) mine[mb] = adapter_of(g, r0 + 16 * mb + rl);
+  const int tile_row = adapter_of(g, lane < 16 * MB ? r0 + lane : g.rows);
+  // t: asked for first, and used last of what is asked for here.
+  V8 hi[MB][RS], lo[MB][RS];
+  float back[MB];
+  v4f t[MB][RS][2];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const float* p = g.t + min(r0 + 16 * mb + rl, g.rows - 1) * g.rank + 8 * kq;
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+      t[mb][s][0] = t[mb][s][1] = v4f{};
+      if (32 * s + 8 * kq < g.rank)
+        for (int q = 0; q < g.splits; ++q) {
+          const v4f* e = reinterpret_cast<const v4f*>(p + (int64_t)q * g.rows * g.rank + 32 * s);
+          t[mb][s][0] += e[0];
+          t[mb][s][1] += e[1];
+        }
+    }
+  }
+  Row8<OUT_DT> io[MB * NP];
+#pragma unroll
+  for (int j = 0; j < MB * NP; ++j)
+    if (r0 + row_of(j) < g.rows && col_of(j) < g.n)
+      io[j].load(g.base, (r0 + row_of(j)) * g.ldb + col_of(j), min(8, g.n - col_of(j)));
+  int list;
+  const int nd = distinct(tile_row, list);
+
+  // t, scaled, in two pieces.
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const float sc = mine[mb] >= 0 && g.scale ? g.scale[mine[mb]] : 1.0f;
     float top = 0.0f;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = 4 * (rl + 16 * j);
-      v4f s = v4f{};
-      if (a >= 0 && c < g.rank) {
-        const float* p = g.t + row * g.rank + c;
-        for (int q = 0; q < g.splits; ++q) s += *reinterpret_cast<const v4f*>(p + (int64_t)q * g.rows * g.rank);
-      }
+    for (int s = 0; s < RS; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[j][i] = s[i] * sc;
-        top = fmaxf(top, fabsf(v[j][i]));
+      for (int i = 0; i < 8; ++i) {
+        const float v = t[mb][s][i >> 2][i & 3] * sc;
+        t[mb][s][i >> 2][i & 3] = v;
+        top = fmaxf(top, fabsf(v));
       }
-    }
-    float fit = 1.0f, back = 1.0f;
+    float fit = 1.0f;
+    back[mb] = 1.0f;
     if constexpr (DT == DT_F16) {
-      top = fmaxf(top, dpp_f<0xB1>(top));
-      top = fmaxf(top, dpp_f<0x4E>(top));
-      top = fmaxf(top, dpp_f<0x141>(top));
-      top = fmaxf(top, dpp_f<0x140>(top));
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
       // 2^(13 - exponent of the largest); without a finite, normal one nothing is scaled
       const int e = (int)(f_bits(top) >> 23) - 127;
       const int by = top < bits_f(0x7F800000u) && e > -100 && e < 100 ? 13 - e : 0;
       fit = bits_f((unsigned)(127 + by) << 23);
-      back = bits_f((unsigned)(127 - by) << 23);
+      back[mb] = bits_f((unsigned)(127 - by) << 23);
     }
-    if (rl == 0) s_back[r] = back;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = 4 * (rl + 16 * j);
-      if (c < rp) {
-        u2v hi, lo;
+    for (int s = 0; s < RS; ++s) {
+      u4v h, l;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float t0 = v[j][2 * i] * fit, t1 = v[j][2 * i + 1] * fit;
-          hi[i] = cvt_pair<DT>(t0, t1);
-          float h0, h1;
-          decode2<DT>(hi[i], h0, h1);
-          // an infinite hi has no rest
-          const float d0 = fabsf(h0) < bits_f(0x7F800000u) ? t0 - h0 : 0.0f;
-          const float d1 = fabsf(h1) < bits_f(0x7F800000u) ? t1 - h1 : 0.0f;
-          lo[i] = cvt_pair<DT>(d0, d1);
-        }
-        *reinterpret_cast<u2v*>(s_t + r * rp + c) = hi;
-        *reinterpret_cast<u2v*>(s_lo + r * rp + c) = lo;
+      for (int i = 0; i < 4; ++i) {
+        const float t0 = t[mb][s][i >> 1][2 * (i & 1)] * fit, t1 = t[mb][s][i >> 1][2 * (i & 1) + 1] * fit;
+        h[i] = cvt_pair<DT>(t0, t1);
+        float h0, h1;
+        decode2<DT>(h[i], h0, h1);
+        // an infinite hi has no rest
+        const float d0 = fabsf(h0) < bits_f(0x7F800000u) ? t0 - h0 : 0.0f;
+        const float d1 = fabsf(h1) < bits_f(0x7F800000u) ? t1 - h1 : 0.0f;
+        l[i] = cvt_pair<DT>(d0, d1);
       }
+      hi[mb][s] = __builtin_bit_cast(V8, h);
+      lo[mb][s] = __builtin_bit_cast(V8, l);
     }
   }
-  __syncthreads();
 
-  int list;
-  const int nd = distinct(lane < 16 * MB ? adapter_of(g, r0 + lane) : -1, list);
-  int mine[MB];
-  float back[MB];
+  float* sums = s_sum + wave * (16 * MB * PITCH);
+  for (int d0 = 0; d0 < nd; d0 += DU) {
+    V8 fu[DU][RS][NP][2];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    mine[mb] = adapter_of(g, r0 + 16 * mb + rl);
-    back[mb] = s_back[16 * mb + rl];
-  }
-  for (int w = 0; w < each; ++w) {
-    const int n0 = n_first + UP_COLS * w;
-    if (n0 >= g.n) return;
-    v4f acc[MB][2];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) acc[mb][0] = acc[mb][1] = v4f{};
-    for (int d = 0; d < nd; ++d) {
-      const int a = __builtin_amdgcn_readlane(list, d);
-      v4f one[MB][2];
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) one[mb][0] = one[mb][1] = v4f{};
+    for (int u = 0; u < DU; ++u) {
+      const int64_t a = __builtin_amdgcn_readlane(list, min(d0 + u, nd - 1));
       // Row i of block b is column 8 (i / 4) + 4 b + i % 4, so that a lane's sums are eight
       // consecutive outputs of its row.
-      const uint16_t* pu[2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int n = min(n0 + 8 * (rl >> 2) + 4 * b + (rl & 3), g.n - 1);
-        pu[b] = g.up + ((int64_t)a * g.n + n) * g.rank + 8 * kq;
-      }
-      for (int k = 0; k < rp; k += 32) {
-        V8 fu[2];
+      for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          fu[b] = V8{};
-          if (k + 8 * kq < g.rank) fu[b] = *reinterpret_cast<const V8*>(pu[b] + k);
-        }
+          const int n = min(n0 + 32 * p + 8 * (rl >> 2) + 4 * b + (rl & 3), g.n - 1);
+          const uint16_t* q = g.up + (a * g.n + n) * g.rank + 8 * kq;
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          const int at = (16 * mb + rl) * rp + k + 8 * kq;
-          const V8 hi = *reinterpret_cast<const V8*>(s_t + at), lo = *reinterpret_cast<const V8*>(s_lo + at);
+          for (int s = 0; s < RS; ++s) {
+            fu[u][s][p][b] = V8{};
+            if (32 * s + 8 * kq < g.rank) fu[u][s][p][b] = *reinterpret_cast<const V8*>(q + 32 * s);
+          }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < DU; ++u) {
+      if (d0 + u >= nd) break;
+      const int a = __builtin_amdgcn_readlane(list, d0 + u);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        v4f acc[NP][2];
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            one[mb][b] = mfma32<DT>(fu[b], lo, one[mb][b]);
-            one[mb][b] = mfma32<DT>(fu[b], hi, one[mb][b]);
+            acc[p][b] = v4f{};
+#pragma unroll
+            for (int s = 0; s < RS; ++s) {
+              acc[p][b] = mfma32<DT>(fu[u][s][p][b], lo[mb][s], acc[p][b]);
+              acc[p][b] = mfma32<DT>(fu[u][s][p][b], hi[mb][s], acc[p][b]);
+            }
+          }
+        // Each row takes the sums of its own adapter, once.
+        if (mine[mb] == a) {
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            if constexpr (LINES) {
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                *reinterpret_cast<v4f*>(sums + (16 * mb + rl) * PITCH + 32 * p + 8 * kq + 4 * b) = acc[p][b] * back[mb];
+            } else {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = acc[p][i >> 2][i & 3] * back[mb];
+              io[mb * NP + p].add(v);
+            }
           }
         }
       }
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[mb][b][i] = mine[mb] == a ? one[mb][b][i] : acc[mb][b][i];
     }
-    const int n = n0 + 8 * kq;
-    const int cnt = min(8, g.n - n);
-    if (cnt > 0) {
+  }
+  if constexpr (LINES) __builtin_amdgcn_wave_barrier();
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        const int64_t row = r0 + 16 * mb + rl;
-        if (row < g.rows) {
-          float v[8];
+  for (int j = 0; j < MB * NP; ++j) {
+    const int64_t row = r0 + row_of(j);
+    if constexpr (LINES) {
+      const int own = __shfl(tile_row, row_of(j), 64);
+      if (own >= 0) {
+        float v[8];
+        const v4f* q = reinterpret_cast<const v4f*>(sums + row_of(j) * PITCH + 8 * (lane & 7));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = acc[mb][i >> 2][i & 3] * back[mb];
-          out_row8<OUT_DT>(g.base, g.out, row * g.ldb + n, row * g.ldo + n, cnt, mine[mb] >= 0, v);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = q[i >> 2][i & 3];
+        io[j].add(v);
       }
     }
+    if (row < g.rows && col_of(j) < g.n) io[j].store(g.out, row * g.ldo + col_of(j), min(8, g.n - col_of(j)));
   }
 }
 
@@ -344,7 +384,7 @@ LowrankPlan lowrank_plan(int64_t rows, int adapters, int rank, int64_t k) {
   LowrankPlan p;
   rows = std::max<int64_t>(1, rows);
   const int64_t tiles = (rows + 15) / 16;
-  p.few = tiles < 512;
+  p.few = tiles < 8192;
   const int blocks = (rank + 15) / 16;
   p.cb = blocks <= 2 ? 2 : blocks <= 4 || p.few ? 4 : 8;
   const int64_t cols = (int64_t)std::min<int64_t>(std::min<int64_t>(16, rows), adapters) * rank;
@@ -383,17 +423,25 @@ static void launch_down(const LowrankArgs& a, const LowrankPlan& p, hipStream_t 
   }
 }
 
+template <int DT, int OUT_DT, int RS>
+static void launch_up_rs(LowrankArgs a, hipStream_t st) {
+  const bool many = a.rows >= UP_MANY;
+  constexpr int MB = UP_MB, NP = UP_NP, DU = 4 / RS;
+  const int mb = many ? MB : 1, waves = many ? 4 : 1, cols = 32 * (many ? NP : 1) * waves;
+  a.col_tiles = (a.n + cols - 1) / cols;
+  const dim3 grid((unsigned)((a.rows + 16 * mb - 1) / (16 * mb) * a.col_tiles));
+  if (many) {
+    const size_t lds = (size_t)4 * waves * 16 * MB * (32 * NP + 4);
+    hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, MB, NP, RS, 1, true>), grid, dim3(64 * waves), lds, st, a);
+  } else {
+    hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, 1, 1, RS, DU, false>), grid, dim3(64), 0, st, a);
+  }
+}
 template <int DT, int OUT_DT>
-static void launch_up(LowrankArgs a, hipStream_t st) {
-  const bool many = a.rows >= 1024;
-  const int mb = many ? 4 : 1, waves = many ? 4 : 1, each = many ? 4 : 1;
-  a.col_tiles = (a.n + UP_COLS * waves * each - 1) / (UP_COLS * waves * each);
-  const int64_t tiles = (a.rows + 16 * mb - 1) / (16 * mb);
-  const dim3 grid((unsigned)(tiles * a.col_tiles));
-  const size_t lds = (size_t)2 * 2 * 16 * mb * ((a.rank + 31) / 32 * 32);
-  auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(64 * waves), lds, st, a, each); };
-  if (many) go(k_lowrank_up<DT, OUT_DT, 4>);
-  else go(k_lowrank_up<DT, OUT_DT, 1>);
+static void launch_up(const LowrankArgs& a, hipStream_t st) {
+  if (a.rank <= 32) launch_up_rs<DT, OUT_DT, 1>(a, st);
+  else if (a.rank <= 64) launch_up_rs<DT, OUT_DT, 2>(a, st);
+  else launch_up_rs<DT, OUT_DT, 4>(a, st);
 }
 
 template <int DT>
