@@ -69,84 +69,109 @@ __device__ __forceinline__ int distinct(int a, int& list) {
   return n;
 }
 
-// Columns are those of the tile's adapters one after the other, rank each, CB blocks of 16 a
-// workgroup.  KS waves share a tile's K (1: each of the four has a tile of its own).
-template <int DT, int CB, int KS>
+// 16 MB rows, whose K the four waves share.  Columns are those of the tile's adapters one after the
+// other, rank each; a workgroup takes CB blocks of 16, and again every chunks-th.  U steps of 32 of K on
+// their way at once; those of x before the adapters are known.
+template <int DT, int MB, int CB>
 __global__ __launch_bounds__(256) void k_lowrank_down(LowrankArgs g) {
   typedef typename Half<DT>::V8 V8;
-  __shared__ v4f s_part[KS > 1 ? KS : 1][CB][64];
+  constexpr int U = MB * CB <= 2 ? 8 : 4, KS = 4;
+  __shared__ v4f s_part[KS - 1][MB][CB][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int split = blockIdx.x % g.splits;
   const int rest = blockIdx.x / g.splits;
   const int chunk = rest % g.chunks;
-  const int64_t tile = KS > 1 ? rest / g.chunks : (int64_t)(rest / g.chunks) * 4 + wave;
-  const int kw = KS > 1 ? wave : 0;
+  const int64_t r0 = (int64_t)(rest / g.chunks) * (16 * MB);
   const int rl = lane & 15, kq = lane >> 4;
-  const int64_t row = tile * 16 + rl;
-  const int mine = adapter_of(g, row);
-  int list;
-  const int nd = distinct(mine, list);
-  const int cols = nd * g.rank;
-  const int c0 = chunk * CB * 16;
-  if (c0 >= cols) return;  // the same for a tile's waves
-  const uint16_t* px = g.x + min(row, g.rows - 1) * g.ldx + 8 * kq;
-  const uint16_t* pw[CB];
+  int mine[MB];
+  const uint16_t* px[MB];
 #pragma unroll
-  for (int b = 0; b < CB; ++b) {
-    const int c = min(c0 + 16 * b + rl, cols - 1);
-    const int d = c / g.rank;
-    const int64_t a = __shfl(list, d, 64);
-    pw[b] = g.down + (a * g.rank + (c - d * g.rank)) * g.k + 8 * kq;
+  for (int m = 0; m < MB; ++m) {
+    const int64_t row = r0 + 16 * m + rl;
+    mine[m] = adapter_of(g, row);
+    px[m] = g.x + min(row, g.rows - 1) * g.ldx + 8 * kq;
   }
+  const int tile_row = adapter_of(g, lane < 16 * MB ? r0 + lane : g.rows);
   const int steps = g.k / 32;
-  const int parts = g.splits * KS, part = split * KS + kw;
+  const int parts = g.splits * KS, part = split * KS + wave;
   const int s0 = (int)((int64_t)steps * part / parts), s1 = (int)((int64_t)steps * (part + 1) / parts);
-  v4f acc[CB];
-#pragma unroll
-  for (int b = 0; b < CB; ++b) acc[b] = v4f{};
-  constexpr int U = CB <= 2 ? 8 : 4;
-  for (int s = s0; s < s1; s += U) {
-    V8 fx[U], fw[U][CB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t e = 32 * (int64_t)min(s + u, s1 - 1);
-      fx[u] = *reinterpret_cast<const V8*>(px + e);
-#pragma unroll
-      for (int b = 0; b < CB; ++b) fw[u][b] = *reinterpret_cast<const V8*>(pw[b] + e);
-    }
+  V8 fx[U][MB], next[U][MB];
+  auto load_x = [&](int s) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (s + u < s1) {
 #pragma unroll
-        for (int b = 0; b < CB; ++b) acc[b] = mfma32<DT>(fw[u][b], fx[u], acc[b]);
+        for (int m = 0; m < MB; ++m) next[u][m] = *reinterpret_cast<const V8*>(px[m] + 32 * (int64_t)(s + u));
       }
-  }
-  if constexpr (KS > 1) {
+  };
+  load_x(s0);
+  int list;
+  const int nd = distinct(tile_row, list);
+  const int cols = nd * g.rank;
+  for (int c0 = chunk * CB * 16; c0 < cols; c0 += g.chunks * CB * 16) {  // the same for all waves
+    const uint16_t* pw[CB];
 #pragma unroll
-    for (int b = 0; b < CB; ++b) s_part[kw][b][lane] = acc[b];
+    for (int b = 0; b < CB; ++b) {
+      const int c = min(c0 + 16 * b + rl, cols - 1);
+      const int d = c / g.rank;
+      const int64_t a = __shfl(list, d, 64);
+      pw[b] = g.down + (a * g.rank + (c - d * g.rank)) * g.k + 8 * kq;
+    }
+    if (c0 != chunk * CB * 16) load_x(s0);
+    v4f acc[MB][CB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int b = 0; b < CB; ++b) acc[m][b] = v4f{};
+    for (int s = s0; s < s1; s += U) {
+      V8 fw[U][CB];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int m = 0; m < MB; ++m) fx[u][m] = next[u][m];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s + u < s1) {
+#pragma unroll
+          for (int b = 0; b < CB; ++b) fw[u][b] = *reinterpret_cast<const V8*>(pw[b] + 32 * (int64_t)(s + u));
+        }
+      if (s + U < s1) load_x(s + U);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s + u < s1) {
+#pragma unroll
+          for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int b = 0; b < CB; ++b) acc[m][b] = mfma32<DT>(fw[u][b], fx[u][m], acc[m][b]);
+        }
+    }
+    if (wave) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int b = 0; b < CB; ++b) s_part[wave - 1][m][b][lane] = acc[m][b];
+    }
     __syncthreads();
-    if (wave) return;
+    // Lane (rl, kq) has four columns of row rl in each block, all of one adapter (rank % 8 == 0).
+    if (!wave) {
 #pragma unroll
-    for (int b = 0; b < CB; ++b)
+      for (int b = 0; b < CB; ++b) {
+        const int c = c0 + 16 * b + 4 * kq;
+        const int d = min(c, cols - 1) / g.rank;
+        const int a = __shfl(list, d, 64);
 #pragma unroll
-      for (int w = 1; w < KS; ++w) acc[b] += s_part[w][b][lane];
-  }
-  // Lane (rl, kq) has four columns of row rl in each block, all of one adapter (rank % 8 == 0).
+        for (int m = 0; m < MB; ++m) {
 #pragma unroll
-  for (int b = 0; b < CB; ++b) {
-    const int c = c0 + 16 * b + 4 * kq;
-    const int d = min(c, cols - 1) / g.rank;
-    const int a = __shfl(list, d, 64);
-    if (c < cols && a == mine)
-      *reinterpret_cast<v4f*>(g.t + ((int64_t)split * g.rows + row) * g.rank + (c - d * g.rank)) = acc[b];
+          for (int w = 0; w < KS - 1; ++w) acc[m][b] += s_part[w][m][b][lane];
+          if (c < cols && a == mine[m])
+            *reinterpret_cast<v4f*>(g.t + ((int64_t)split * g.rows + r0 + 16 * m + rl) * g.rank + (c - d * g.rank)) = acc[m][b];
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
-#ifndef UP_MB
-#define UP_MB 2
-#define UP_NP 2
-#define UP_MANY 1024
-#endif
 // Eight elements of a row, cnt of them inside it, and what they are with v added.
 template <int DT>
 struct Row8 {
@@ -199,171 +224,275 @@ struct Row8 {
   }
 };
 
-// Waves side by side, each 16 MB rows by 32 NP columns.  RS: steps of 32 of the rank.  DU: adapters whose
-// rows of up are on their way at once.  LINES: the sums change places through LDS, so that a load of
-// base and a store of out cover whole 128-byte lines of eight rows (from the product's own
-// layout they cover 64 bytes of sixteen rows).
-template <int DT, int OUT_DT, int MB, int NP, int RS, int DU, bool LINES>
-__global__ __launch_bounds__(256) void k_lowrank_up(LowrankArgs g) {
+// What brings an fp16 row whose largest |t| is `top` to [2^13, 2^14), and back (bfloat16 has float32's range).
+template <int DT>
+__device__ __forceinline__ void fit_of(float top, float& fit, float& back) {
+  fit = back = 1.0f;
+  if constexpr (DT == DT_F16) {
+    const int e = (int)(f_bits(top) >> 23) - 127;
+    // without a finite, normal one nothing is scaled
+    const int by = top < bits_f(0x7F800000u) && e > -100 && e < 100 ? 13 - e : 0;
+    fit = bits_f((unsigned)(127 + by) << 23);
+    back = bits_f((unsigned)(127 - by) << 23);
+  }
+}
+// Two values of t in two pieces each.
+template <int DT>
+__device__ __forceinline__ void pieces(float t0, float t1, unsigned& hi, unsigned& lo) {
+  hi = cvt_pair<DT>(t0, t1);
+  float h0, h1;
+  decode2<DT>(hi, h0, h1);
+  // an infinite hi has no rest
+  const float d0 = fabsf(h0) < bits_f(0x7F800000u) ? t0 - h0 : 0.0f;
+  const float d1 = fabsf(h1) < bits_f(0x7F800000u) ? t1 - h1 : 0.0f;
+  lo = cvt_pair<DT>(d0, d1);
+}
+// A step of 32 of the rank from row q of up: eight elements a lane.
+template <typename V8>
+__device__ __forceinline__ V8 up_step(const uint16_t* q, int s, int kq, int rank) {
+  return 32 * s + 8 * kq < rank ? *reinterpret_cast<const V8*>(q + 32 * s) : V8{};
+}
+// Row i of the two blocks of 16 rows of up for 32 columns: column 8 (i / 4) + 4 b + i % 4, so that a
+// lane's sums are eight consecutive outputs of its row.
+__device__ __forceinline__ int up_col(int rl, int b) { return 8 * (rl >> 2) + 4 * b + (rl & 3); }
+
+// Few rows: a wave of its own for 16 rows by 32 columns, t straight into the product's layout.  RS: steps
+// of 32 of the rank.  Four steps of up are on their way at once, of as many adapters.
+template <int DT, int OUT_DT, int RS>
+__global__ __launch_bounds__(64) void k_lowrank_up_few(LowrankArgs g) {
   typedef typename Half<DT>::V8 V8;
-  static_assert(!LINES || NP == 2, "eight lanes of eight columns a row");
-  constexpr int COLS = 32 * NP, PITCH = COLS + 4;
-  extern __shared__ __attribute__((aligned(16))) float s_sum[];  // LINES: [waves][16 MB][PITCH]
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rl = lane & 15, kq = lane >> 4;
-  const int64_t r0 = (int64_t)(blockIdx.x / g.col_tiles) * (16 * MB);
-  const int n0 = ((int)(blockIdx.x % g.col_tiles) * (int)(blockDim.x >> 6) + wave) * COLS;
-  if (n0 >= g.n) return;
-
-  // Piece j of the lane's outputs: its row in the tile and its column.
-  auto row_of = [&](int j) { return LINES ? 8 * j + (lane >> 3) : 16 * (j / NP) + rl; };
-  auto col_of = [&](int j) { return n0 + (LINES ? 8 * (lane & 7) : 32 * (j % NP) + 8 * kq); };
-  int mine[MB];
+  constexpr int DU = 4 / RS;
+  const int lane = threadIdx.x, rl = lane & 15, kq = lane >> 4;
+  const int64_t row = (int64_t)(blockIdx.x / g.col_tiles) * 16 + rl;
+  const int n0 = (int)(blockIdx.x % g.col_tiles) * 32, n = n0 + 8 * kq;
+  const bool here = row < g.rows && n < g.n;
+  const int mine = adapter_of(g, row);
+  v4f t[RS][2];
+  const float* pt = g.t + min(row, g.rows - 1) * g.rank + 8 * kq;
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) mine[mb] = adapter_of(g, r0 + 16 * mb + rl);
-  const int tile_row = adapter_of(g, lane < 16 * MB ? r0 + lane : g.rows);
-  // t: asked for first, and used last of what is asked for here.
-  V8 hi[MB][RS], lo[MB][RS];
-  float back[MB];
-  v4f t[MB][RS][2];
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const float* p = g.t + min(r0 + 16 * mb + rl, g.rows - 1) * g.rank + 8 * kq;
-#pragma unroll
-    for (int s = 0; s < RS; ++s) {
-      t[mb][s][0] = t[mb][s][1] = v4f{};
-      if (32 * s + 8 * kq < g.rank)
-        for (int q = 0; q < g.splits; ++q) {
-          const v4f* e = reinterpret_cast<const v4f*>(p + (int64_t)q * g.rows * g.rank + 32 * s);
-          t[mb][s][0] += e[0];
-          t[mb][s][1] += e[1];
-        }
-    }
+  for (int s = 0; s < RS; ++s) {
+    t[s][0] = t[s][1] = v4f{};
+    if (32 * s + 8 * kq < g.rank)
+      for (int q = 0; q < g.splits; ++q) {
+        const v4f* e = reinterpret_cast<const v4f*>(pt + (int64_t)q * g.rows * g.rank + 32 * s);
+        t[s][0] += e[0];
+        t[s][1] += e[1];
+      }
   }
-  Row8<OUT_DT> io[MB * NP];
-#pragma unroll
-  for (int j = 0; j < MB * NP; ++j)
-    if (r0 + row_of(j) < g.rows && col_of(j) < g.n)
-      io[j].load(g.base, (r0 + row_of(j)) * g.ldb + col_of(j), min(8, g.n - col_of(j)));
+  Row8<OUT_DT> io;
+  if (here) io.load(g.base, row * g.ldb + n, min(8, g.n - n));
   int list;
-  const int nd = distinct(tile_row, list);
-
-  // t, scaled, in two pieces.
+  const int nd = distinct(mine, list);
+  const float sc = mine >= 0 && g.scale ? g.scale[mine] : 1.0f;
+  float top = 0.0f;
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const float sc = mine[mb] >= 0 && g.scale ? g.scale[mine[mb]] : 1.0f;
-    float top = 0.0f;
+  for (int s = 0; s < RS; ++s)
 #pragma unroll
-    for (int s = 0; s < RS; ++s)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = t[mb][s][i >> 2][i & 3] * sc;
-        t[mb][s][i >> 2][i & 3] = v;
-        top = fmaxf(top, fabsf(v));
-      }
-    float fit = 1.0f;
-    back[mb] = 1.0f;
-    if constexpr (DT == DT_F16) {
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      // 2^(13 - exponent of the largest); without a finite, normal one nothing is scaled
-      const int e = (int)(f_bits(top) >> 23) - 127;
-      const int by = top < bits_f(0x7F800000u) && e > -100 && e < 100 ? 13 - e : 0;
-      fit = bits_f((unsigned)(127 + by) << 23);
-      back[mb] = bits_f((unsigned)(127 - by) << 23);
+    for (int i = 0; i < 8; ++i) {
+      t[s][i >> 2][i & 3] = t[s][i >> 2][i & 3] * sc;
+      top = fmaxf(top, fabsf(t[s][i >> 2][i & 3]));
     }
-#pragma unroll
-    for (int s = 0; s < RS; ++s) {
-      u4v h, l;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float t0 = t[mb][s][i >> 1][2 * (i & 1)] * fit, t1 = t[mb][s][i >> 1][2 * (i & 1) + 1] * fit;
-        h[i] = cvt_pair<DT>(t0, t1);
-        float h0, h1;
-        decode2<DT>(h[i], h0, h1);
-        // an infinite hi has no rest
-        const float d0 = fabsf(h0) < bits_f(0x7F800000u) ? t0 - h0 : 0.0f;
-        const float d1 = fabsf(h1) < bits_f(0x7F800000u) ? t1 - h1 : 0.0f;
-        l[i] = cvt_pair<DT>(d0, d1);
-      }
-      hi[mb][s] = __builtin_bit_cast(V8, h);
-      lo[mb][s] = __builtin_bit_cast(V8, l);
-    }
+  if constexpr (DT == DT_F16) {
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
   }
-
-  float* sums = s_sum + wave * (16 * MB * PITCH);
+  float fit, back;
+  fit_of<DT>(top, fit, back);
+  V8 hi[RS], lo[RS];
+#pragma unroll
+  for (int s = 0; s < RS; ++s) {
+    u4v h, l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unsigned hu, lu;
+      pieces<DT>(t[s][i >> 1][2 * (i & 1)] * fit, t[s][i >> 1][2 * (i & 1) + 1] * fit, hu, lu);
+      h[i] = hu;
+      l[i] = lu;
+    }
+    hi[s] = __builtin_bit_cast(V8, h);
+    lo[s] = __builtin_bit_cast(V8, l);
+  }
   for (int d0 = 0; d0 < nd; d0 += DU) {
-    V8 fu[DU][RS][NP][2];
+    V8 fu[DU][RS][2];
 #pragma unroll
     for (int u = 0; u < DU; ++u) {
       const int64_t a = __builtin_amdgcn_readlane(list, min(d0 + u, nd - 1));
-      // Row i of block b is column 8 (i / 4) + 4 b + i % 4, so that a lane's sums are eight
-      // consecutive outputs of its row.
 #pragma unroll
-      for (int p = 0; p < NP; ++p)
+      for (int b = 0; b < 2; ++b) {
+        const uint16_t* q = g.up + (a * g.n + min(n0 + up_col(rl, b), g.n - 1)) * g.rank + 8 * kq;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int n = min(n0 + 32 * p + 8 * (rl >> 2) + 4 * b + (rl & 3), g.n - 1);
-          const uint16_t* q = g.up + (a * g.n + n) * g.rank + 8 * kq;
-#pragma unroll
-          for (int s = 0; s < RS; ++s) {
-            fu[u][s][p][b] = V8{};
-            if (32 * s + 8 * kq < g.rank) fu[u][s][p][b] = *reinterpret_cast<const V8*>(q + 32 * s);
-          }
-        }
+        for (int s = 0; s < RS; ++s) fu[u][s][b] = up_step<V8>(q, s, kq, g.rank);
+      }
     }
 #pragma unroll
     for (int u = 0; u < DU; ++u) {
       if (d0 + u >= nd) break;
-      const int a = __builtin_amdgcn_readlane(list, d0 + u);
+      v4f acc[2];
 #pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        v4f acc[NP][2];
+      for (int b = 0; b < 2; ++b) {
+        acc[b] = v4f{};
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            acc[p][b] = v4f{};
-#pragma unroll
-            for (int s = 0; s < RS; ++s) {
-              acc[p][b] = mfma32<DT>(fu[u][s][p][b], lo[mb][s], acc[p][b]);
-              acc[p][b] = mfma32<DT>(fu[u][s][p][b], hi[mb][s], acc[p][b]);
-            }
-          }
-        // Each row takes the sums of its own adapter, once.
-        if (mine[mb] == a) {
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            if constexpr (LINES) {
-#pragma unroll
-              for (int b = 0; b < 2; ++b)
-                *reinterpret_cast<v4f*>(sums + (16 * mb + rl) * PITCH + 32 * p + 8 * kq + 4 * b) = acc[p][b] * back[mb];
-            } else {
-              float v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = acc[p][i >> 2][i & 3] * back[mb];
-              io[mb * NP + p].add(v);
-            }
-          }
+        for (int s = 0; s < RS; ++s) {
+          acc[b] = mfma32<DT>(fu[u][s][b], lo[s], acc[b]);
+          acc[b] = mfma32<DT>(fu[u][s][b], hi[s], acc[b]);
         }
+      }
+      // Each row takes the sums of its own adapter, once.
+      if (mine == __builtin_amdgcn_readlane(list, d0 + u)) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = acc[i >> 2][i & 3] * back;
+        io.add(v);
       }
     }
   }
-  if constexpr (LINES) __builtin_amdgcn_wave_barrier();
+  if (here) io.store(g.out, row * g.ldo + n, min(8, g.n - n));
+}
+
+// Many rows: 16 MB rows, of which each of the four waves takes 64 columns; t's pieces shared through LDS.
+// The sums of 16 rows change places through LDS, so that a load of base and a store of out cover whole
+// 128-byte lines of eight rows (from the product's own layout they cover 64 bytes of sixteen rows).
+constexpr int UP_WAVES = 4, UP_COLS = 64, UP_PITCH = UP_COLS + 4;
+
+template <int DT, int OUT_DT, int MB, int RS>
+__global__ __launch_bounds__(64 * UP_WAVES) void k_lowrank_up(LowrankArgs g) {
+  typedef typename Half<DT>::V8 V8;
+  constexpr int TP = 32 * RS + 8;  // pitch of t's pieces: eight lanes' rows start in different banks
+  __shared__ __attribute__((aligned(16))) uint16_t s_t[2][16 * MB][TP];  // hi, lo
+  __shared__ __attribute__((aligned(16))) float s_sum[UP_WAVES][16][UP_PITCH];
+  __shared__ float s_back[16 * MB];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rl = lane & 15, kq = lane >> 4;
+  const int64_t r0 = (int64_t)(blockIdx.x / g.col_tiles) * (16 * MB);
+  const int n0 = ((int)(blockIdx.x % g.col_tiles) * UP_WAVES + wave) * UP_COLS;
+  const int tile_row = adapter_of(g, lane < 16 * MB ? r0 + lane : g.rows);
+
+  // t of the tile: sixteen lanes a row, one row of each 16, asked for before base.
+  constexpr int CH = RS > 2 ? 2 : 1;
+  const int tr = threadIdx.x >> 4;
+  v4f t[MB][CH];
 #pragma unroll
-  for (int j = 0; j < MB * NP; ++j) {
-    const int64_t row = r0 + row_of(j);
-    if constexpr (LINES) {
-      const int own = __shfl(tile_row, row_of(j), 64);
-      if (own >= 0) {
-        float v[8];
-        const v4f* q = reinterpret_cast<const v4f*>(sums + row_of(j) * PITCH + 8 * (lane & 7));
+  for (int mb = 0; mb < MB; ++mb) {
+    const float* p = g.t + min(r0 + 16 * mb + tr, g.rows - 1) * g.rank;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = q[i >> 2][i & 3];
-        io[j].add(v);
+    for (int j = 0; j < CH; ++j) {
+      const int c = 4 * (rl + 16 * j);
+      t[mb][j] = v4f{};
+      if (c < g.rank)
+        for (int q = 0; q < g.splits; ++q) t[mb][j] += *reinterpret_cast<const v4f*>(p + (int64_t)q * g.rows * g.rank + c);
+    }
+  }
+  int list;
+  const int nd = distinct(tile_row, list);
+  V8 fu[2][2][RS];
+  auto load_up = [&](int d) {
+    const int64_t a = __builtin_amdgcn_readlane(list, d);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint16_t* q = g.up + (a * g.n + min(n0 + 32 * p + up_col(rl, b), g.n - 1)) * g.rank + 8 * kq;
+#pragma unroll
+        for (int s = 0; s < RS; ++s) fu[p][b][s] = up_step<V8>(q, s, kq, g.rank);
+      }
+  };
+  if (nd) load_up(0);
+  // Piece j of the lane's outputs: row 8 j + lane / 8 of the tile, columns from `col`.
+  const int col = n0 + 8 * (lane & 7);
+  Row8<OUT_DT> io[2 * MB];
+#pragma unroll
+  for (int j = 0; j < 2 * MB; ++j) {
+    const int64_t row = r0 + 8 * j + (lane >> 3);
+    if (row < g.rows && col < g.n) io[j].load(g.base, row * g.ldb + col, min(8, g.n - col));
+  }
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const int a = adapter_of(g, r0 + 16 * mb + tr);
+    const float sc = a >= 0 && g.scale ? g.scale[a] : 1.0f;
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        t[mb][j][i] = t[mb][j][i] * sc;
+        top = fmaxf(top, fabsf(t[mb][j][i]));
+      }
+    if constexpr (DT == DT_F16) {
+      top = fmaxf(top, dpp_f<0xB1>(top));
+      top = fmaxf(top, dpp_f<0x4E>(top));
+      top = fmaxf(top, dpp_f<0x141>(top));
+      top = fmaxf(top, dpp_f<0x140>(top));
+    }
+    float fit, back;
+    fit_of<DT>(top, fit, back);
+    if (rl == 0) s_back[16 * mb + tr] = back;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = 4 * (rl + 16 * j);
+      if (c < 32 * RS) {
+        u2v h, l;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          unsigned hu, lu;
+          pieces<DT>(t[mb][j][2 * i] * fit, t[mb][j][2 * i + 1] * fit, hu, lu);
+          h[i] = hu;
+          l[i] = lu;
+        }
+        *reinterpret_cast<u2v*>(&s_t[0][16 * mb + tr][c]) = h;
+        *reinterpret_cast<u2v*>(&s_t[1][16 * mb + tr][c]) = l;
       }
     }
-    if (row < g.rows && col_of(j) < g.n) io[j].store(g.out, row * g.ldo + col_of(j), min(8, g.n - col_of(j)));
+  }
+  __syncthreads();
+  if (n0 >= g.n) return;
+  float (*sums)[UP_PITCH] = s_sum[wave];
+  for (int d = 0; d < nd; ++d) {
+    const int a = __builtin_amdgcn_readlane(list, d);
+    if (d) load_up(d);
+    const uint64_t rows_of_a = __ballot(tile_row == a);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      if (!((rows_of_a >> (16 * mb)) & 0xFFFF)) continue;
+      v4f acc[2][2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) acc[p][0] = acc[p][1] = v4f{};
+#pragma unroll
+      for (int s = 0; s < RS; ++s) {
+        const V8 hi = *reinterpret_cast<const V8*>(&s_t[0][16 * mb + rl][32 * s + 8 * kq]);
+        const V8 lo = *reinterpret_cast<const V8*>(&s_t[1][16 * mb + rl][32 * s + 8 * kq]);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            acc[p][b] = mfma32<DT>(fu[p][b][s], lo, acc[p][b]);
+            acc[p][b] = mfma32<DT>(fu[p][b][s], hi, acc[p][b]);
+          }
+      }
+      const float back = s_back[16 * mb + rl];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) *reinterpret_cast<v4f*>(&sums[rl][32 * p + 8 * kq + 4 * b]) = acc[p][b] * back;
+      __builtin_amdgcn_wave_barrier();
+      // Each row takes the sums of its own adapter, once.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = 8 * h + (lane >> 3);
+        if ((rows_of_a >> (16 * mb + r)) & 1) {
+          const v4f* q = reinterpret_cast<const v4f*>(&sums[r][8 * (lane & 7)]);
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = q[i >> 2][i & 3];
+          io[2 * mb + h].add(v);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * MB; ++j) {
+    const int64_t row = r0 + 8 * j + (lane >> 3);
+    if (row < g.rows && col < g.n) io[j].store(g.out, row * g.ldo + col, min(8, g.n - col));
   }
 }
 
@@ -374,26 +503,26 @@ namespace vq_internal {
 using namespace vqk;
 
 namespace {
-// How a call is cut: tiles of 16 rows whose K is shared by four waves (and by `splits` workgroups)
-// while rows are few, else a tile a wave.
+constexpr int64_t DOWN_GROUPS = 512;  // two workgroups a compute unit
+// How the first product is cut: tiles of 16 or 32 rows by blocks of 16 columns, workgroups of their own for
+// further columns, and for parts of K, while rows alone do not fill the compute units.
 struct LowrankPlan {
-  bool few;
-  int cb, chunks, splits;
+  int mb, cb, chunks, splits;
+  int64_t tiles;
 };
 LowrankPlan lowrank_plan(int64_t rows, int adapters, int rank, int64_t k) {
   LowrankPlan p;
   rows = std::max<int64_t>(1, rows);
-  const int64_t tiles = (rows + 15) / 16;
-  p.few = tiles < 8192;
-  const int blocks = (rank + 15) / 16;
-  p.cb = blocks <= 2 ? 2 : blocks <= 4 || p.few ? 4 : 8;
-  const int64_t cols = (int64_t)std::min<int64_t>(std::min<int64_t>(16, rows), adapters) * rank;
-  p.chunks = (int)((cols + 16 * p.cb - 1) / (16 * p.cb));
-  p.splits = 1;
-  if (p.few) {
-    const int64_t most = std::max<int64_t>(1, 512 / (tiles * p.chunks));
-    p.splits = (int)std::min<int64_t>(std::min<int64_t>(8, most), std::max<int64_t>(1, k / 512));
-  }
+  // Tiles of 32 rows read the adapters half as often: where they still fill the compute units (17776 rows,
+  // 1920, rank 32, 33 -> 31 us, rank 128 90 -> 73; but 4000 rows of rank 32 14 -> 18), and for large ranks
+  // (1000 rows of rank 128 20 -> 15).
+  p.mb = rows >= 8192 || (rank > 64 && rows > 16) ? 2 : 1;
+  p.tiles = (rows + 16 * p.mb - 1) / (16 * p.mb);
+  p.cb = rank <= 32 ? 2 : 4;
+  const int64_t cols = (int64_t)std::min<int64_t>(std::min<int64_t>(16 * p.mb, rows), adapters) * rank;
+  p.chunks = (int)std::min<int64_t>((cols + 16 * p.cb - 1) / (16 * p.cb), std::max<int64_t>(1, DOWN_GROUPS / p.tiles));
+  const int64_t most = std::max<int64_t>(1, DOWN_GROUPS / (p.tiles * p.chunks));
+  p.splits = (int)std::min<int64_t>(std::min<int64_t>(8, most), std::max<int64_t>(1, k / 512));
   return p;
 }
 }  // namespace
@@ -404,38 +533,33 @@ int64_t lowrank_workspace_elems(int64_t rows, int64_t adapters, int64_t rank, in
 
 int64_t lowrank_groups(int64_t rows, int64_t adapters, int64_t rank, int64_t k, int64_t n) {
   const LowrankPlan p = lowrank_plan(rows, (int)adapters, (int)rank, k);
-  return std::max((rows + 15) / 16 * p.chunks * p.splits, (rows + 15) / 16 * ((n + 31) / 32));
+  return std::max(p.tiles * p.chunks * p.splits, (rows + 15) / 16 * ((n + 31) / 32));
 }
 
 template <int DT>
 static void launch_down(const LowrankArgs& a, const LowrankPlan& p, hipStream_t st) {
-  const int64_t tiles = (a.rows + 15) / 16;
-  const int64_t groups = p.few ? tiles : (tiles + 3) / 4;
-  const dim3 grid((unsigned)(groups * p.chunks * p.splits));
+  const dim3 grid((unsigned)(p.tiles * p.chunks * p.splits));
   auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(256), 0, st, a); };
-  if (p.few) {
-    if (p.cb == 2) go(k_lowrank_down<DT, 2, 4>);
-    else go(k_lowrank_down<DT, 4, 4>);
+  if (p.mb == 1) {
+    if (p.cb == 2) go(k_lowrank_down<DT, 1, 2>);
+    else go(k_lowrank_down<DT, 1, 4>);
   } else {
-    if (p.cb == 2) go(k_lowrank_down<DT, 2, 1>);
-    else if (p.cb == 4) go(k_lowrank_down<DT, 4, 1>);
-    else go(k_lowrank_down<DT, 8, 1>);
+    if (p.cb == 2) go(k_lowrank_down<DT, 2, 2>);
+    else go(k_lowrank_down<DT, 2, 4>);
   }
 }
 
 template <int DT, int OUT_DT, int RS>
 static void launch_up_rs(LowrankArgs a, hipStream_t st) {
-  const bool many = a.rows >= UP_MANY;
-  constexpr int MB = UP_MB, NP = UP_NP, DU = 4 / RS;
-  const int mb = many ? MB : 1, waves = many ? 4 : 1, cols = 32 * (many ? NP : 1) * waves;
+  // 64 rows of rank 32, 1920 -> 5760, 4.0 us with waves of their own, 7.6 with shared tiles of 32; 200 rows 7.6
+  // and 7.0.  Tiles of 64 rows are no faster (17776 rows, rank 32, 92 against 87 us, rank 128 even).
+  const bool many = a.rows > 64;
+  constexpr int MB = 2;
+  const int rows = many ? 16 * MB : 16, cols = many ? UP_WAVES * UP_COLS : 32;
   a.col_tiles = (a.n + cols - 1) / cols;
-  const dim3 grid((unsigned)((a.rows + 16 * mb - 1) / (16 * mb) * a.col_tiles));
-  if (many) {
-    const size_t lds = (size_t)4 * waves * 16 * MB * (32 * NP + 4);
-    hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, MB, NP, RS, 1, true>), grid, dim3(64 * waves), lds, st, a);
-  } else {
-    hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, 1, 1, RS, DU, false>), grid, dim3(64), 0, st, a);
-  }
+  const dim3 grid((unsigned)((a.rows + rows - 1) / rows * a.col_tiles));
+  if (many) hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, MB, RS>), grid, dim3(64 * UP_WAVES), 0, st, a);
+  else hipLaunchKernelGGL((k_lowrank_up_few<DT, OUT_DT, RS>), grid, dim3(64), 0, st, a);
 }
 template <int DT, int OUT_DT>
 static void launch_up(const LowrankArgs& a, hipStream_t st) {
