@@ -80,8 +80,8 @@ __device__ __forceinline__ float param1(const void* p, int f32, int64_t e) {
   return f32 ? reinterpret_cast<const float*>(p)[e] : load1<DT>(p, e);
 }
 
-// BR: the branch.  QUANT: codes and scales instead of n.  T threads a row.
-template <int DT, int BR, bool QUANT, bool DUAL, int END, int NP>
+// BR: the branch.  QUANT: codes and scales instead of n.  PAST: y and h past the cache.  T threads a row.
+template <int DT, int BR, bool QUANT, bool DUAL, int END, int NP, bool PAST = false>
 __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
   static_assert(END == END_WHOLE || !QUANT, "codes are written 8 at a time");
   static_assert(QUANT || !DUAL, "the outlier partition is one of codes");
@@ -89,7 +89,8 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
   __shared__ double s_sum[2][2][16][2];
   __shared__ float s_max[2][16][2];
   __shared__ unsigned s_mask[DUAL ? 1024 : 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // A wave has one row: what goes by the row is the same for its lanes, and kept in scalar registers.
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wpr = T >> 6;  // waves per row
   const int rpb = (int)blockDim.x / T;
   const int rib = wave / wpr;
@@ -147,13 +148,17 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
     u4v raw[NP], rad[BR ? NP : 1];
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      raw[j] = load8<TINY, false>(hr + at(j), a.k);
-      if constexpr (BR != BR_NONE) rad[j] = load8<TINY, false>(yr + at(j), a.k);
+      raw[j] = load8<TINY, PAST>(hr + at(j), a.k);
+      if constexpr (BR != BR_NONE) rad[j] = load8<TINY, PAST>(yr + at(j), a.k);
     }
     // The row's set of modulation rows; one outside them leaves the row without gate's branch, scale and shift.
     const int64_t set = a.index ? a.index[rr] : rr / a.per;
     const bool set_ok = set >= 0 && set < a.sets;
     const int64_t st = set_ok ? set : 0;
+    // Parameters are read again with each row (they stay in the cache); moved out of the loop they
+    // would be held in registers, which cost waves.
+    const void *pw = a.pw, *wt = a.w;
+    asm volatile("" : "+s"(pw), "+s"(wt));
     // The outlier channels' h and y, gathered before anyone stores s (s may be h or y itself).
     float oh[2] = {0.0f, 0.0f}, oy[2] = {0.0f, 0.0f};
     if constexpr (DUAL) {
@@ -165,18 +170,22 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
         }
     }
 
-    float v[NP][8];
-    // Sum and sum of squares of v over the row; the pieces past the row's end repeat its first one.
-    auto moments = [&](int which, int kind, float& mean, float& rstd) {
+    // Sum and sum of squares over the row; the pieces past the row's end repeat its first one.  The
+    // values stay in 16 bits and are decoded again where they are used: in float32 they cost registers,
+    // and with them waves.
+    auto moments = [&](const u4v (&q)[NP], int which, int kind, float& mean, float& rstd) {
       double s1 = 0.0, s2 = 0.0;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         double p1 = 0.0, p2 = 0.0;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) decode2<DT>(q[j][i], v[2 * i], v[2 * i + 1]);
         const int before = END == END_OVERLAP ? elem(j) - at(j) : 0;  // counted by the piece before
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const bool in = TINY ? i < a.k : END == END_OVERLAP ? i >= before : true;
-          const double c = in ? (double)v[j][i] : 0.0;
+          const double c = in ? (double)v[i] : 0.0;
           p1 += c;
           p2 = __builtin_fma(c, c, p2);
         }
@@ -206,29 +215,24 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
     };
 
     float pmean = 0.0f, prstd = 0.0f;
-    if constexpr (BR == BR_NORMED) {
-#pragma unroll
-      for (int j = 0; j < NP; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) decode2<DT>(rad[j][i], v[j][2 * i], v[j][2 * i + 1]);
-      moments(0, a.post, pmean, prstd);
-    }
+    if constexpr (BR == BR_NORMED) moments(rad, 0, a.post, pmean, prstd);
     if constexpr (BR != BR_NONE) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         float p[8], g[8];
-        if (BR == BR_NORMED && a.pw) params8<DT, TINY>(a.pw, a.pw_f32, at(j), a.k, p);
+        if (BR == BR_NORMED && pw) params8<DT, TINY>(pw, a.pw_f32, at(j), a.k, p);
         if (a.gate) params8<DT, TINY>(a.gate, a.mod_f32, st * a.ldg + at(j), a.k, g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float u[2], x[2];
+          asm volatile("" : "+v"(rad[j][i]));  // decoded anew, not kept from the moments
           decode2<DT>(rad[j][i], u[0], u[1]);
           decode2<DT>(raw[j][i], x[0], x[1]);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if constexpr (BR == BR_NORMED) {
               u[t] = (u[t] - pmean) * prstd;
-              if (a.pw) u[t] = u[t] * p[2 * i + t];
+              if (pw) u[t] = u[t] * p[2 * i + t];
             }
             const float ga = a.gate ? g[2 * i + t] * a.alpha : a.alpha;
             u[t] = set_ok ? x[t] + u[t] * ga : x[t];
@@ -237,12 +241,8 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < NP; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) decode2<DT>(raw[j][i], v[j][2 * i], v[j][2 * i + 1]);
     float mean, rstd;
-    moments(1, a.norm, mean, rstd);
+    moments(raw, 1, a.norm, mean, rstd);
 
     if (BR != BR_NONE && row_ok) {
       uint16_t* sr = a.s + row * a.lds;
@@ -250,27 +250,33 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
       for (int j = 0; j < NP; ++j)
         if (elem(j) < a.k) store8<TINY, true>(sr + at(j), raw[j], a.k);
     }
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
+    // Piece j of the output before its last rounding.
+    auto normed = [&](int j, float (&v)[8]) {
       float p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = (v[j][i] - mean) * rstd;
-      if (a.w) {
-        params8<DT, TINY>(a.w, a.w_f32, at(j), a.k, p);
+      for (int i = 0; i < 4; ++i) {
+        float x0, x1;
+        asm volatile("" : "+v"(raw[j][i]));  // decoded anew, as above
+        decode2<DT>(raw[j][i], x0, x1);
+        v[2 * i] = (x0 - mean) * rstd;
+        v[2 * i + 1] = (x1 - mean) * rstd;
+      }
+      if (wt) {
+        params8<DT, TINY>(wt, a.w_f32, at(j), a.k, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * p[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * p[i];
       }
       if (a.sc && set_ok) {
         params8<DT, TINY>(a.sc, a.mod_f32, st * a.ldsc + at(j), a.k, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * (1.0f + p[i]);
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * (1.0f + p[i]);
       }
       if (a.sh && set_ok) {
         params8<DT, TINY>(a.sh, a.mod_f32, st * a.ldsh + at(j), a.k, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] + p[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] + p[i];
       }
-    }
+    };
 
     if constexpr (!QUANT) {
       if (row_ok) {
@@ -278,13 +284,18 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
 #pragma unroll
         for (int j = 0; j < NP; ++j)
           if (elem(j) < a.k) {
+            float v[8];
+            normed(j, v);
             u4v o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = cvt_pair<DT>(v[j][2 * i], v[j][2 * i + 1]);
+            for (int i = 0; i < 4; ++i) o[i] = cvt_pair<DT>(v[2 * i], v[2 * i + 1]);
             store8<TINY, false>(nr + at(j), o, a.k);
           }
       }
     } else {
+      float v[NP][8];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) normed(j, v[j]);
       float ov[2] = {0.0f, 0.0f};
       // A value that is an infinity or NaN: the row's scales say so (a maximum alone would pass a NaN by).
       float bad = 0.0f;
@@ -386,7 +397,15 @@ static void launch_gated_np(const GatedArgs& a, int np, int grid, int block, int
   switch (np) {
     case 1: hipLaunchKernelGGL((k_gated_norm<DT, BR, QUANT, DUAL, END, 1>), dim3(grid), dim3(block), 0, st, a, T); break;
     case 2: hipLaunchKernelGGL((k_gated_norm<DT, BR, QUANT, DUAL, END, 2>), dim3(grid), dim3(block), 0, st, a, T); break;
-    default: hipLaunchKernelGGL((k_gated_norm<DT, BR, QUANT, DUAL, END, 4>), dim3(grid), dim3(block), 0, st, a, T); break;
+    default:
+      // Read once, y and h go past the last-level cache where the call's operands take more than three
+      // quarters of it (17776 x 1920 to 16 bits 70 -> 62 us; 4113 x 4096 to codes, which fit, 31 -> 34).
+      // Outlier channels are read twice.
+      if (!DUAL && a.rows * a.k * ((BR ? 6 : 2) + (QUANT ? 1 : 2)) > ((int64_t)192 << 20))
+        hipLaunchKernelGGL((k_gated_norm<DT, BR, QUANT, DUAL, END, 4, !DUAL>), dim3(grid), dim3(block), 0, st, a, T);
+      else
+        hipLaunchKernelGGL((k_gated_norm<DT, BR, QUANT, DUAL, END, 4>), dim3(grid), dim3(block), 0, st, a, T);
+      break;
   }
 }
 
@@ -463,9 +482,9 @@ hipError_t launch_gated_norm(const GatedNormParams& p, hipStream_t st) {
   const int T = std::min(1024, (pieces + 64 * per - 1) / (64 * per) * 64);
   const int each = (pieces + T - 1) / T;
   const int np = each <= 1 ? 1 : each <= 2 ? 2 : 4;
-  const int block = T <= 128 ? 256 : T;
+  const int block = T <= 128 ? 128 : T;
   const int64_t need = (p.rows + block / T - 1) / (block / T);
-  const int64_t most = (int64_t)persistent_blocks() * 32 / (block / 64);
+  const int64_t most = (int64_t)persistent_blocks() * 64 / (block / 64);
   const int grid = (int)std::min(need, most);
   if (p.dtype == DT_BF16) launch_gated_dt<DT_BF16>(a, np, grid, block, T, st);
   else launch_gated_dt<DT_F16>(a, np, grid, block, T, st);
