@@ -514,56 +514,74 @@ __device__ __forceinline__ void rows8(const void* p, int64_t at, int cnt, float*
   }
 }
 
-// TY: type of y; TO: of the residual and the output; gates in float32 or TG.
+// TY: type of y; TO: of the residual and the output; gates in float32 or the 16-bit one of the two.  A
+// wave has 512 elements of a row, so that the row's places and weights are scalars; four choices' rows
+// are on their way at once.
 template <int TY, int TO>
-__global__ __launch_bounds__(256) void k_combine(CombineArgs a, int pieces) {
-  const int64_t total = a.rows * pieces;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
-    const int64_t row = t / pieces;
-    const int e = 8 * (int)(t - row * pieces);
-    const int cnt = min(8, a.n - e);
-    float v[8] = {};
-    for (int j = 0; j < a.top; ++j) {
-      const int64_t at = a.place[row * a.top + j];
-      const float w = a.w[row * a.top + j];
-      if (at >= 0 && at < a.y_rows) {
-        float q[8];
-        rows8<TY>(a.y, at * a.ldy + e, cnt, q);
+__global__ __launch_bounds__(256) void k_combine(CombineArgs a, int segments, int64_t items) {
+  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (item >= items) return;
+  const int64_t row = item / segments;
+  const int e = (int)(item - row * segments) * 512 + 8 * (threadIdx.x & 63);
+  const int cnt = min(8, a.n - e);
+  if (cnt <= 0) return;
+  float r[8] = {};
+  if (a.res) rows8<TO>(a.res, row * a.ldr + e, cnt, r);
+  float v[8] = {};
+  const int32_t* place = a.place + row * a.top;
+  const float* weight = a.w + row * a.top;
+  for (int j0 = 0; j0 < a.top; j0 += 4) {
+    float q[4][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] + q[i] * w;
+    for (int u = 0; u < 4; ++u) {
+      if (j0 + u >= a.top) break;
+      const int64_t at = place[j0 + u];
+      if (at >= 0 && at < a.y_rows) {
+        rows8<TY>(a.y, at * a.ldy + e, cnt, q[u]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] + 0.0f * w;
+        for (int i = 0; i < 8; ++i) q[u][i] = 0.0f;
       }
     }
-    float r[8] = {};
-    if (a.res) rows8<TO>(a.res, row * a.ldr + e, cnt, r);
-    bool ok = true;
-    if (a.gate) {
-      const int64_t set = a.index ? a.index[row] : row / a.per;
-      ok = set >= 0 && set < a.sets;
-      float g[8];
-      const int64_t ge = (ok ? set : 0) * a.ldg + e;
-      if (a.gate_f32) rows8<DT_F32>(a.gate, ge, cnt, g);
-      else rows8<TY == DT_F32 ? TO : TY>(a.gate, ge, cnt, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] * g[i];
+    for (int u = 0; u < 4; ++u) {
+      if (j0 + u >= a.top) break;
+      const float w = weight[j0 + u];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] + q[u][i] * w;
     }
+  }
+  bool ok = true;
+  if (a.gate) {
+    const int64_t set = a.index ? a.index[row] : row / a.per;
+    ok = set >= 0 && set < a.sets;
+    float g[8];
+    const int64_t ge = (ok ? set : 0) * a.ldg + e;
+    if (a.gate_f32) rows8<DT_F32>(a.gate, ge, cnt, g);
+    else rows8<TY == DT_F32 ? TO : TY>(a.gate, ge, cnt, g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = !ok ? r[i] : a.res ? v[i] + r[i] : v[i];
-    const int64_t o = row * a.ldo + e;
-    if constexpr (TO == DT_F32) {
-      float* p = reinterpret_cast<float*>(a.out) + o;
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * g[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = !ok ? r[i] : a.res ? v[i] + r[i] : v[i];
+  const int64_t o = row * a.ldo + e;
+  if constexpr (TO == DT_F32) {
+    float* p = reinterpret_cast<float*>(a.out) + o;
+    if (cnt == 8) {
+      reinterpret_cast<v4f_el*>(p)[0] = v4f{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<v4f_el*>(p)[1] = v4f{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < cnt) p[i] = v[i];
-    } else {
-      u4v q;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = cvt_pair<TO>(v[2 * i], v[2 * i + 1]);
-      uint16_t* p = reinterpret_cast<uint16_t*>(a.out) + o;
-      if (cnt == 8) store8<false, false>(p, q, 8);
-      else store8<true, false>(p, q, cnt);
     }
+  } else {
+    u4v q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = cvt_pair<TO>(v[2 * i], v[2 * i + 1]);
+    uint16_t* p = reinterpret_cast<uint16_t*>(a.out) + o;
+    if (cnt == 8) store8<false, false>(p, q, 8);
+    else store8<true, false>(p, q, cnt);
   }
 }
 
@@ -680,10 +698,9 @@ hipError_t launch_combine(const CombineParams& p, hipStream_t st) {
   a.n = (int)p.n;
   a.top = p.top;
   a.gate_f32 = p.mod.f32;
-  const int pieces = (int)((p.n + 7) / 8);
-  const int64_t need = (p.rows * pieces + 255) / 256;
-  const int grid = (int)std::min<int64_t>(need, (int64_t)persistent_blocks() * 16);
-  auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3(grid), dim3(256), 0, st, a, pieces); };
+  const int segments = (int)((p.n + 511) / 512);
+  const int64_t items = p.rows * segments;
+  auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, st, a, segments, items); };
   if (p.y_dt == DT_F32) {
     if (p.out_dt == DT_F32) go(k_combine<DT_F32, DT_F32>);
     else if (p.out_dt == DT_BF16) go(k_combine<DT_F32, DT_BF16>);
