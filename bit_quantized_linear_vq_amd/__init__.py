@@ -953,19 +953,19 @@ def _modulation(gate, scale, shift, index, m, k, dt, device_index):
             ptrs.append(None)
             lds.append(k)
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != device_index:
+        if not isinstance(t, torch.Tensor) or t.get_device() != device_index or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor on device {device_index}")
         if first is None:
-            first = t
-            if t.dtype is not dt and t.dtype is not torch.float32:
-                raise TypeError(f"{name} must have dtype {dt} or torch.float32, not {t.dtype}")
-            if t.dim() != 2 or t.shape[1] != k or t.shape[0] < 1:
+            first, dtype, shape = t, t.dtype, t.shape
+            if dtype is not dt and dtype is not torch.float32:
+                raise TypeError(f"{name} must have dtype {dt} or torch.float32, not {dtype}")
+            if len(shape) != 2 or shape[1] != k or shape[0] < 1:
                 raise ValueError(f"{name} must be [sets x {k}]")
-        elif t.dtype is not first.dtype or t.shape != first.shape:
+            sets = shape[0]
+        elif t.dtype is not dtype or t.shape != shape:
             raise ValueError("gate, mod_scale and mod_shift must have one shape and dtype")
         ld, unit = t.stride()
-        sets = t.shape[0]
-        if (k > 1 and unit != 1) or (sets > 1 and ld < k):
+        if (unit != 1 and k > 1) or (ld < k and sets > 1):
             raise ValueError(f"{name} must have unit stride along its rows and a pitch of at least a row")
         ptrs.append(t.data_ptr())
         lds.append(ld if sets > 1 else k)
@@ -973,7 +973,6 @@ def _modulation(gate, scale, shift, index, m, k, dt, device_index):
         if index is not None:
             raise ValueError("index goes with a gate, mod_scale or mod_shift")
         return None
-    sets = first.shape[0]
     i_ptr = None
     if index is not None:
         _dense(index, "index", device_index, _I32, m)
@@ -982,7 +981,7 @@ def _modulation(gate, scale, shift, index, m, k, dt, device_index):
         i_ptr = index.data_ptr()
     elif m % sets:
         raise ValueError(f"{m} rows do not split evenly over {sets} sets: pass index")
-    return Modulation(*ptrs, *lds, i_ptr, sets, _DT[first.dtype], 0)
+    return Modulation(*ptrs, *lds, i_ptr, sets, _DT[dtype], 0)
 
 
 def _gated_operands(branch, residual, post, post_weight, branch_scale, gate, scale, shift, index, norm, weight, eps,
@@ -1106,9 +1105,16 @@ def _rows_any(t, name, index, dtypes):
     return ld if m > 1 else k
 
 
+def _shaped(t, name, index, dtypes, shape):
+    """_dense for a tensor of exactly this shape."""
+    _dense(t, name, index, dtypes, 0)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+
+
 @functools.lru_cache(maxsize=1024)
 def vq_route_experts_workspace_elems(m: int, experts: int) -> int:
-    """Int32 elements of the scratch that vq_route_experts needs for m rows."""
+    """Int32 elements of the scratch that vq_route_experts needs for m rows (0 for a few)."""
     return int(_lib.vq_route_experts_workspace_elems(m, experts))
 
 
@@ -1134,26 +1140,36 @@ def vq_route_experts(scores: torch.Tensor, top: int, score: str = "softmax", bia
             raise ValueError(f"bias must hold {e} elements")
     if not 1 <= top <= e:
         raise ValueError(f"top must be from 1 to {e}")
-    outs = []
-    for t, name, dt, shape in ((offsets, "offsets", torch.int32, (e + 1,)), (rows, "rows", torch.int32, (m * top,)),
-                               (weights, "weights", torch.float32, (m, top)), (experts, "experts", torch.int32, (m, top)),
-                               (place, "place", torch.int32, (m, top))):
-        if t is None:
-            t = torch.empty(shape, dtype=dt, device=device)
-        else:
-            _dense(t, name, dev, (dt,), 0)
-            if t.shape != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
-        outs.append(t)
-    need = vq_route_experts_workspace_elems(m, e)
-    if ws is None:
-        ws = torch.empty(need, dtype=torch.int32, device=device)
+    i32 = torch.int32
+    if offsets is None:
+        offsets = torch.empty(e + 1, dtype=i32, device=device)
     else:
+        _shaped(offsets, "offsets", dev, _I32, (e + 1,))
+    if rows is None:
+        rows = torch.empty(m * top, dtype=i32, device=device)
+    else:
+        _shaped(rows, "rows", dev, _I32, (m * top,))
+    if weights is None:
+        weights = torch.empty(m, top, dtype=torch.float32, device=device)
+    else:
+        _shaped(weights, "weights", dev, _F32, (m, top))
+    if experts is None:
+        experts = torch.empty(m, top, dtype=i32, device=device)
+    else:
+        _shaped(experts, "experts", dev, _I32, (m, top))
+    if place is None:
+        place = torch.empty(m, top, dtype=i32, device=device)
+    else:
+        _shaped(place, "place", dev, _I32, (m, top))
+    need = vq_route_experts_workspace_elems(m, e)
+    if ws is not None:
         _dense(ws, "ws", dev, _I32, need)
+    elif need:
+        ws = torch.empty(need, dtype=i32, device=device)
     _launch("vq_route_experts", dev, scores.data_ptr(), _DT[scores.dtype], m, e, ldx, _SCORE[score], _ptr(bias), groups,
             groups if top_groups is None else top_groups, group_best, top, int(bool(renorm)), scale,
-            *[t.data_ptr() for t in outs], ws.data_ptr())
-    return tuple(outs)
+            offsets.data_ptr(), rows.data_ptr(), weights.data_ptr(), experts.data_ptr(), place.data_ptr(), _ptr(ws))
+    return offsets, rows, weights, experts, place
 
 
 def vq_combine_experts(y: torch.Tensor, place: torch.Tensor, weights: torch.Tensor, residual=None, gate=None, index=None,

@@ -777,7 +777,7 @@ bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t
 
 int64_t vq_route_experts_workspace_elems(int64_t m, int64_t experts) {
   if (m < 0 || m > kMaxExpertRows || experts < 1 || experts > kMaxExperts) return 0;
-  return std::max<int64_t>(1, vq_internal::route_experts_workspace_elems(m, experts));
+  return vq_internal::route_experts_workspace_elems(m, experts);
 }
 
 vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t experts, int64_t ldx, vq_score score,
@@ -786,12 +786,13 @@ vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t expert
                            int32_t* place, int32_t* ws, hipStream_t stream) {
   if (!valid_dt(dt) || m < 0 || experts < 1 || ldx < experts || top < 1) return VQ_ERR_INVALID_ARG;
   if (score != VQ_SCORE_SOFTMAX && score != VQ_SCORE_SIGMOID) return VQ_ERR_INVALID_ARG;
-  if (!offsets || !ws || (m > 0 && (!x || !rows || !weights || !chosen || !place))) return VQ_ERR_INVALID_ARG;
+  if (!offsets || (m > 0 && (!x || !rows || !weights || !chosen || !place))) return VQ_ERR_INVALID_ARG;
   if (groups < 1 || experts % groups || top_groups < 1 || top_groups > groups) return VQ_ERR_INVALID_ARG;
   if (group_best < 1 || group_best > 2 || group_best > experts / groups) return VQ_ERR_INVALID_ARG;
   if (top > experts / groups * top_groups || !std::isfinite((float)scale)) return VQ_ERR_INVALID_ARG;
   if (experts > kMaxExperts || top > kMaxTop || groups > kMaxGroups || m > kMaxExpertRows / top)
     return VQ_ERR_UNSUPPORTED;
+  if (!ws && vq_internal::route_experts_workspace_elems(m, experts)) return VQ_ERR_INVALID_ARG;
   if (misaligned(x, elem_size(dt)) || misaligned(bias, 4) || misaligned(offsets, 4) || misaligned(rows, 4) ||
       misaligned(weights, 4) || misaligned(chosen, 4) || misaligned(place, 4) || !aligned16(ws))
     return VQ_ERR_SHAPE;

@@ -558,7 +558,8 @@ vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const
  *   weights    device float [m x top];  chosen, place: device int32 [m x top] (place: where the
  *              choice is in the sorted order)
  *   ws         device int32 scratch of vq_route_experts_workspace_elems(m, experts) elements, 16-byte
- *              aligned; calls that may run at the same time need one each
+ *              aligned (NULL where that is 0, for a few rows); calls that may run at the same time need
+ *              one each
  * m = 0 writes zero offsets.  Places are the same in every call (no order of atomics enters).
  * Nothing is allocated and the host reads nothing, so a call may be captured.
  * Errors: INVALID_ARG (also top > experts of the kept groups, experts % groups, group_best > a

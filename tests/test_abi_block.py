@@ -96,7 +96,7 @@ def route(vq, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(x=NULL), INVALID), (dict(dt=7), INVALID), (dict(m=-1), INVALID), (dict(e=0), INVALID), (dict(ldx=15), INVALID),
     (dict(score=2), INVALID), (dict(score=-1), INVALID), (dict(off=NULL), INVALID), (dict(rows=NULL), INVALID),
-    (dict(w=NULL), INVALID), (dict(ch=NULL), INVALID), (dict(place=NULL), INVALID), (dict(ws=NULL), INVALID),
+    (dict(w=NULL), INVALID), (dict(ch=NULL), INVALID), (dict(place=NULL), INVALID), (dict(m=65, ws=NULL), INVALID),
     (dict(groups=0), INVALID), (dict(groups=3), INVALID), (dict(keep=0), INVALID), (dict(keep=5), INVALID),
     (dict(best=0), INVALID), (dict(best=3), INVALID), (dict(groups=16, keep=8), INVALID), (dict(top=0), INVALID),
     (dict(top=9), INVALID), (dict(scale=INF), INVALID), (dict(scale=NAN), INVALID),
@@ -112,7 +112,7 @@ def test_route_validation(vq, kw, want):
 def test_route_workspace(vq):
     n = vq._lib.vq_route_experts_workspace_elems
     assert n(-1, 8) == n(8, 0) == n(8, 1025) == n((1 << 26) + 1, 8) == 0
-    assert n(0, 8) > 0 and n(1, 1) > 0 and n(1 << 26, 1024) >= 1024
+    assert n(0, 8) == n(64, 1024) == 0 and n(65, 1) > 0 and n(1 << 26, 1024) >= 1024
 
 
 def combine(vq, **kw):

@@ -126,7 +126,7 @@ def test_route_calls_that_are_right_reach_the_launch(vq):
     (ValueError, lambda: dict(offsets=dev(16, dt=I32))), (TypeError, lambda: dict(offsets=dev(17))),
     (ValueError, lambda: dict(rows=dev(6, 2, dt=I32))), (ValueError, lambda: dict(weights=dev(2, 6))),
     (ValueError, lambda: dict(weights=dev(2, 6).t())), (TypeError, lambda: dict(experts=dev(6, 2))), (TypeError, lambda: dict(ws=dev(64))),
-    (TypeError, lambda: dict(place=torch.empty(6, 2, dtype=I32))), (ValueError, lambda: dict(ws=dev(0, dt=I32))),
+    (TypeError, lambda: dict(place=torch.empty(6, 2, dtype=I32))), (ValueError, lambda: dict(scores=dev(65, 16), rows=None, weights=None, experts=None, place=None, ws=dev(15, dt=I32))),
 ])
 def test_route_refusals(vq, error, kw):
     refused(vq, error, route, vq, **kw())
