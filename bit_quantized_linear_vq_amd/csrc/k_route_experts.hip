@@ -11,7 +11,7 @@
 //   k_route_place   offsets, and each choice's place: rows before it in its expert's segment, by
 //                   ascending token and choice.  Counts are whole numbers, so the order of their sums does not
 //                   matter, and places are the same in every call.
-//   k_route_few     both for up to 64 rows
+//   k_route_few     both for a few rows: 64 of up to 64 experts, 16 of 256, 4 of more
 #include <algorithm>
 #include <type_traits>
 
@@ -27,7 +27,7 @@ struct RouteArgs {
   const float* bias;  // or nullptr
   int64_t ldx;
   int64_t rows;
-  int experts, top, groups, keep, best, softmax, renorm;
+  int dtype, experts, top, groups, keep, best, softmax, renorm;
   float scale;
   int32_t* offsets;
   int32_t* row_of;  // [rows * top]
@@ -37,8 +37,6 @@ struct RouteArgs {
   int32_t* counts;  // [blocks, count_pitch], 16-byte aligned
 };
 
-constexpr int FEW_ROWS = 64;      // the most that one launch does
-constexpr int PLACE_TILE = 2048;  // choices that a workgroup places at a time: as many as 64 rows can have
 
 // All lanes of a row (LPR of them) get the same; register moves inside 16 lanes.
 template <typename K, int CTRL>
@@ -118,101 +116,131 @@ __device__ __forceinline__ double exp_d(double x) {
   return __builtin_ldexp(p, (int)n);
 }
 
+// e^x of x <= 0 to 2^-22 of it, for the sum under weights that end in float32: x / ln 2 in float64, its
+// fraction by the hardware's 2^f (1 ulp, and f's own rounding, 2^-26).
+__device__ __forceinline__ float exp_f(double x) {
+  const double y = fmax(x, -800.0) * 1.4426950408889634;
+  const double n = __builtin_rint(y);
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
+}
+
 // What the choice goes by.  BY_SCORE: the scores themselves, exact in float32.  BY_P: p (+ bias), in
 // float64 for every expert.
 enum : int { BY_SCORE = 0, BY_P = 1 };
 
 // A row's choices: lane l of its LPR holds choices l and l + LPR (of experts l + LPR i, in the loop).
-// Returned: their experts (-1: none) and weights.
-template <int DT, int LPR, int VPT, int BY>
-__device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row, int l, int ch[2], float wt[2]) {
+// Returned: their experts (-1: none) and weights.  s_row: 8-byte aligned, for groups: experts + groups keys.
+template <int LPR, int VPT, int BY, bool SOFT, bool GROUPS>
+__device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row, int l, void* s_row, int ch[2], float wt[2]) {
   typedef typename std::conditional<BY == BY_P, double, float>::type K;
   constexpr K NONE = -(K)__builtin_huge_val();
-  K key[VPT];
+  // What depends on the lane alone stays in the loop over rows: moved out of it, it is held in registers.
+  asm volatile("" : "+v"(l));
+  float x[VPT];
+  auto load = [&](auto dt) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) x[i] = load1<decltype(dt)::value>(a.x, row * a.ldx + min(l + LPR * i, a.experts - 1));
+  };
+  if (a.dtype == DT_F32) load(std::integral_constant<int, DT_F32>{});
+  else if (a.dtype == DT_BF16) load(std::integral_constant<int, DT_BF16>{});
+  else load(std::integral_constant<int, DT_F16>{});
   float top = -__builtin_huge_valf();
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int e = l + LPR * i;
-    const float x = e < a.experts ? load1<DT>(a.x, row * a.ldx + e) : -__builtin_huge_valf();
-    bad |= x != x || (a.softmax && x == __builtin_huge_valf());
-    top = x > top ? x : top;
-    key[i] = (K)x;
+    x[i] = l + LPR * i < a.experts ? x[i] : -__builtin_huge_valf();
+    bad |= x[i] != x[i] || (SOFT && x[i] == __builtin_huge_valf());
+    top = x[i] > top ? x[i] : top;
   }
-  // Of a softmax that is divided by the sum of its chosen, the whole sum is not needed.
-  double base = 0.0, denom = 1.0;  // denom: its reciprocal in the end
-  if (a.softmax) {
+  double base = 0.0;
+  if constexpr (SOFT) {
     top = max_of<LPR>(top);
     base = top > -__builtin_huge_valf() ? (double)top : 0.0;
-    if (BY == BY_P || !a.renorm) {
-      denom = 0.0;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (l + LPR * i < a.experts) denom += exp_d((double)key[i] - base);
-      denom = sum_of<LPR>(denom);
-      denom = denom > 0.0 ? 1.0 / denom : 1.0;
-    }
   }
-  auto p_of = [&](double x) { return a.softmax ? exp_d(x - base) * denom : 1.0 / (1.0 + exp_d(-x)); };
-  if constexpr (BY == BY_P) {
+  // p of every expert where the choice needs it, else their sum where the weights do (of a softmax that
+  // is divided by the sum of its chosen they do not).  Without branches, and two exponentials at a time:
+  // more of them side by side cost registers, and with them waves.
+  double p[BY == BY_P ? VPT : 1];
+  double per = 1.0;
+  if (SOFT && (BY == BY_P || !a.renorm)) {
+    double sum = 0.0;
+    if constexpr (BY == BY_P) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int e = l + LPR * i;
-      if (e >= a.experts || key[i] == NONE) continue;
-      // (by p without a bias the groups go by p, the choice in them by the scores: key stays)
-      if (a.bias) key[i] = p_of(key[i]) + (double)a.bias[e];
+      for (int i = 0; i < VPT; ++i) {
+        p[i] = exp_d((double)x[i] - base);
+        sum += p[i];
+        if (i & 1) __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        sum += (double)exp_f((double)x[i] - base);
+        if (i & 1) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    sum = sum_of<LPR>(sum);
+    per = sum > 0.0 ? 1.0 / sum : 1.0;
+  }
+  K key[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    key[i] = (K)x[i];
+    if constexpr (BY == BY_P) {
+      p[i] = SOFT ? p[i] * per : 1.0 / (1.0 + exp_d(-(double)x[i]));
+      // (by p without a bias the groups go by p, the choice in them by the scores)
+      const double c = a.bias ? p[i] + (double)a.bias[min(l + LPR * i, a.experts - 1)] : (double)x[i];
+      key[i] = key[i] == NONE ? NONE : c;
+      p[i] = a.bias || key[i] == NONE ? key[i] : p[i];
       bad |= key[i] != key[i];
+      if (!SOFT && (i & 1)) __builtin_amdgcn_sched_barrier(0);
     }
   }
   bad = row_ballot<LPR>(bad) != 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) key[i] = bad ? NONE : key[i];
-  if (a.groups > 1) {
+  if constexpr (GROUPS) {
     const int size = a.experts / a.groups;
     const float inv = 1.0f / (float)size;
     // of at most 1024 experts: half a member off a whole number is more than float32's error
     auto group_of = [&](int i) { return (int)(((float)(l + LPR * i) + 0.5f) * inv); };
-    K p[VPT];
+    // Through LDS, so that a lane goes through members of one group: groups side by side (made up to a
+    // power of two), each shared by as many lanes as there are.  A key between the groups that is none
+    // keeps their members in different banks.
+    K* keys = reinterpret_cast<K*>(s_row);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      p[i] = key[i];
-      if constexpr (BY == BY_P)
-        if (!a.bias && key[i] != NONE) p[i] = p_of(key[i]);
-    }
+    for (int i = 0; i < VPT; ++i)
+      if (l + LPR * i < a.experts) {
+        if constexpr (BY == BY_P) keys[l + LPR * i + group_of(i)] = bad ? NONE : p[i];
+        else keys[l + LPR * i + group_of(i)] = key[i];
+      }
+    __builtin_amdgcn_wave_barrier();
     constexpr int SLOTS = 64 / LPR;
+    const int lanes = a.groups > LPR / 2 ? LPR : 1 << (32 - __builtin_clz(a.groups - 1));  // of one part
+    const int parts = LPR / lanes, part = l / lanes;
     K marks[SLOTS];
 #pragma unroll
-    for (int j = 0; j < SLOTS; ++j) marks[j] = NONE;
-    // Four groups at a time: their reductions do not wait for each other.
-    for (int g0 = 0; g0 < a.groups; g0 += 4) {
-      K m1[4], m2[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) m1[u] = m2[u] = NONE;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int gi = group_of(i) - g0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const K k = gi == u ? p[i] : NONE;
-          if (BY == BY_P) m2[u] = larger(smaller(k, m1[u]), m2[u]);
-          m1[u] = larger(k, m1[u]);
+    for (int j = 0; j < SLOTS; ++j) {
+      marks[j] = NONE;
+      if (LPR * j >= a.groups) continue;
+      const int g = (l & (lanes - 1)) + LPR * j;
+      K m1 = NONE, m2 = NONE;
+      if (g < a.groups) {
+#pragma unroll 4
+        for (int i = part; i < size; i += parts) {
+          const K k = keys[g * (size + 1) + i];
+          if (BY == BY_P) m2 = larger(smaller(k, m1), m2);
+          m1 = larger(k, m1);
         }
       }
-      over_row<LPR>([&](auto c) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const K o1 = other<decltype(c)::value>(m1[u]);
-          if constexpr (BY == BY_P) m2[u] = larger(smaller(o1, m1[u]), larger(other<decltype(c)::value>(m2[u]), m2[u]));
-          m1[u] = larger(o1, m1[u]);
-        }
-      });
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (a.best == 2 && m2[u] != NONE) m1[u] += m2[u];
-#pragma unroll
-        for (int j = 0; j < SLOTS; ++j) marks[j] = g0 + u == l + LPR * j ? m1[u] : marks[j];
+      for (int o = lanes; o < LPR; o <<= 1) {
+        const K o1 = __shfl_xor(m1, o, 64);
+        if constexpr (BY == BY_P) m2 = larger(smaller(o1, m1), larger(__shfl_xor(m2, o, 64), m2));
+        m1 = larger(o1, m1);
       }
+      if (a.best == 2 && m2 != NONE) m1 += m2;
+      marks[j] = m1;
     }
+    __builtin_amdgcn_wave_barrier();
     // A group stays if fewer than `keep` are above it (or level with it and before it).
     int above[SLOTS] = {};
     const int lane0 = threadIdx.x & 63 & ~(LPR - 1);
@@ -248,11 +276,14 @@ __device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row, int l
     ch[0] = n == l ? at : ch[0];
     ch[1] = n == l + LPR ? at : ch[1];
   }
-  double w[2], total = 0.0;
+  double w[2] = {0.0, 0.0}, total = 0.0;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    w[j] = 0.0;
-    if (ch[j] >= 0) w[j] = p_of((double)load1<DT>(a.x, row * a.ldx + ch[j]));
+    if (LPR * j >= a.top) break;
+    const int64_t at = row * a.ldx + max(ch[j], 0);
+    const double v = a.dtype == DT_F32 ? load1<DT_F32>(a.x, at) : a.dtype == DT_BF16 ? load1<DT_BF16>(a.x, at) : load1<DT_F16>(a.x, at);
+    w[j] = SOFT ? exp_d(v - base) * per : 1.0 / (1.0 + exp_d(-v));
+    w[j] = ch[j] >= 0 ? w[j] : 0.0;
     total += w[j];
   }
   if (a.renorm) {
@@ -282,9 +313,14 @@ __device__ __forceinline__ void store_row(const RouteArgs& a, int64_t row, int l
 // Counts of a block are a row of 4-aligned length.
 __device__ __forceinline__ int count_pitch(int experts) { return (experts + 3) & ~3; }
 
-template <int DT, int LPR, int VPT, int BY>
+// Where the keys of a thread's row are in LDS, a row for each LPR threads.  (The last two take rows apart.)
+__device__ __forceinline__ void* row_keys(const RouteArgs& a, int* s_keys, int lpr) {
+  return s_keys + (threadIdx.x / lpr) * 2 * (a.experts + a.groups + 2);
+}
+
+template <int LPR, int VPT, int BY, bool SOFT, bool GROUPS>
 __global__ __launch_bounds__(1024) void k_route_select(RouteArgs a, int rows) {
-  extern __shared__ int s_count[];
+  extern __shared__ __attribute__((aligned(16))) int s_count[];
   const int pitch = count_pitch(a.experts);
   for (int e = threadIdx.x; e < pitch; e += blockDim.x) s_count[e] = 0;
   __syncthreads();
@@ -294,7 +330,7 @@ __global__ __launch_bounds__(1024) void k_route_select(RouteArgs a, int rows) {
     if (__builtin_amdgcn_readfirstlane((int)(row < a.rows)) == 0) break;  // the wave's first row, then all
     int ch[2];
     float wt[2];
-    route_row<DT, LPR, VPT, BY>(a, min(row, a.rows - 1), l, ch, wt);
+    route_row<LPR, VPT, BY, SOFT, GROUPS>(a, min(row, a.rows - 1), l, row_keys(a, s_count + pitch, LPR), ch, wt);
     if (row < a.rows) store_row<LPR>(a, row, l, ch, wt, s_count);
   }
   __syncthreads();
@@ -385,6 +421,24 @@ __device__ __forceinline__ void store_places(const RouteArgs& a, const Choices& 
   }
 }
 
+// Places of choices [first, last) in tiles of four a lane; c: the first tile's, ranked already.
+__device__ __forceinline__ void place_tiles(const RouteArgs& a, int64_t first, int64_t last, Choices& c, int* s_next, int* s_wave) {
+  const int tile = PLACE_PER * blockDim.x;
+  for (;;) {
+    __syncthreads();
+    start_waves(a.experts, s_next, s_wave);
+    __syncthreads();
+    store_places(a, c, s_wave);
+    first += tile;
+    if (first >= last) return;
+    load_choices(a, first, min(last, first + tile), c);
+    __syncthreads();
+    for (int e = threadIdx.x; e < ((int)blockDim.x >> 6) * a.experts; e += blockDim.x) s_wave[e] = 0;
+    __syncthreads();
+    rank_choices(a.experts, c, s_wave);
+  }
+}
+
 // A block places the choices of `span` blocks of k_route_select (`rows` rows each), after adding up
 // everyone's counts.
 __global__ __launch_bounds__(1024) void k_route_place(RouteArgs a, int blocks, int rows, int span) {
@@ -399,7 +453,7 @@ __global__ __launch_bounds__(1024) void k_route_place(RouteArgs a, int blocks, i
   int64_t first = (int64_t)b0 * rows * a.top;
   const int64_t last = min(total, first + (int64_t)span * rows * a.top);
   Choices c;
-  load_choices(a, first, min(last, first + PLACE_TILE), c);
+  load_choices(a, first, min(last, first + PLACE_PER * (int64_t)blockDim.x), c);
   // Threads take four experts and every parts-th block.
   const int quads = pitch / 4, parts = max(1, (int)blockDim.x / quads);
   const int part = tid / quads, q = tid - part * quads;
@@ -431,51 +485,37 @@ __global__ __launch_bounds__(1024) void k_route_place(RouteArgs a, int blocks, i
   // Places that no choice takes, behind the last expert's rows.
   for (int64_t r = s_off[E] + (int64_t)blockIdx.x * blockDim.x + tid; r < total; r += (int64_t)gridDim.x * blockDim.x)
     a.row_of[r] = -1;
-  for (;;) {
-    __syncthreads();
-    start_waves(E, s_next, s_wave);
-    __syncthreads();
-    store_places(a, c, s_wave);
-    first += PLACE_TILE;
-    if (first >= last) return;
-    load_choices(a, first, min(last, first + PLACE_TILE), c);
-    __syncthreads();
-    for (int e = tid; e < waves * E; e += blockDim.x) s_wave[e] = 0;
-    __syncthreads();
-    rank_choices(E, c, s_wave);
-  }
+  place_tiles(a, first, last, c, s_next, s_wave);
 }
 
 // Few rows: choices, counts and places by one workgroup, in one launch.
-template <int DT, int LPR, int VPT, int BY>
+template <int LPR, int VPT, int BY, bool SOFT, bool GROUPS>
 __global__ __launch_bounds__(1024) void k_route_few(RouteArgs a) {
-  extern __shared__ int s_mem[];
+  extern __shared__ __attribute__((aligned(16))) int s_mem[];
   const int E = a.experts, pitch = count_pitch(E);
-  int* s_off = s_mem;               // [pitch + 4]
-  int* s_wave = s_mem + pitch + 4;  // [waves][E]
+  int* s_off = s_mem;                 // [pitch + 4]
+  int* s_wave = s_mem + pitch + 4;    // [waves][E], in waves * pitch
+  int* s_keys = s_wave + ((int)blockDim.x >> 6) * pitch;
   for (int e = threadIdx.x; e < pitch + 4 + ((int)blockDim.x >> 6) * E; e += blockDim.x) s_mem[e] = 0;
   __syncthreads();
   const int l = threadIdx.x % LPR;
-  for (int row = threadIdx.x / LPR; row < FEW_ROWS; row += blockDim.x / LPR) {
+  for (int row = threadIdx.x / LPR; row < 64; row += blockDim.x / LPR) {
     if (__builtin_amdgcn_readfirstlane((int)(row < a.rows)) == 0) break;
     int ch[2];
     float wt[2];
-    route_row<DT, LPR, VPT, BY>(a, min((int64_t)row, a.rows - 1), l, ch, wt);
+    route_row<LPR, VPT, BY, SOFT, GROUPS>(a, min((int64_t)row, a.rows - 1), l, row_keys(a, s_keys, LPR), ch, wt);
     if (row < a.rows) store_row<LPR>(a, row, l, ch, wt, s_off);
   }
   __syncthreads();
   const int64_t all = a.rows * a.top;
   Choices c;
-  load_choices(a, 0, all, c);
+  load_choices(a, 0, min(all, PLACE_PER * (int64_t)blockDim.x), c);
   if (threadIdx.x < 64) offsets_of(s_off, E);
   rank_choices(E, c, s_wave);
   __syncthreads();
   for (int e = threadIdx.x; e <= E; e += blockDim.x) a.offsets[e] = s_off[e];
-  __syncthreads();
-  start_waves(E, s_off, s_wave);
-  __syncthreads();
-  store_places(a, c, s_wave);
-  for (int64_t c = s_off[E] + threadIdx.x; c < all; c += blockDim.x) a.row_of[c] = -1;
+  for (int64_t c2 = s_off[E] + threadIdx.x; c2 < all; c2 += blockDim.x) a.row_of[c2] = -1;
+  place_tiles(a, 0, all, c, s_off, s_wave);
 }
 
 // out[i] = RNE(res[i] + gate * sum_j w[i, j] y[place[i, j]]): a thread owns eight elements of a row.
@@ -589,17 +629,23 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs a, int segments, in
 static int place_waves(int experts) { return experts <= 512 ? 16 : 8; }
 static size_t pitch_bytes(int experts) { return 4 * (size_t)((experts + 3) & ~3); }
 
-template <int DT, int BY>
+template <int BY, bool SOFT, bool GROUPS>
 static void launch_select(const RouteArgs& a, int blocks, int rows, hipStream_t st) {
   auto go = [&](auto lpr, auto vpt) {
     constexpr int L = decltype(lpr)::value, V = decltype(vpt)::value;
+    const size_t pitch = pitch_bytes(a.experts);
+    // Groups keep eight bytes an expert in LDS for each row at work: as many waves as 63 KiB hold beside
+    // their counts.
+    const size_t row = 8 * (size_t)(a.experts + a.groups + 2);
+    const int fit = (int)((63 * 1024 - pitch - 16) / (pitch + 64 / L * row));
+    const int most = a.groups > 1 ? 64 * std::max(1, std::min(16, fit)) : 1024;
+    auto keys = [&](int block) { return a.groups > 1 ? (block / L) * row : (size_t)0; };
     if (!rows) {
-      const int block = std::min(64 * place_waves(a.experts), ((int)a.rows * L + 63) / 64 * 64);
-      const size_t lds = pitch_bytes(a.experts) + 16 + 4 * (size_t)(block / 64) * a.experts;
-      hipLaunchKernelGGL((k_route_few<DT, L, V, BY>), dim3(1), dim3(block), lds, st, a);
+      const int block = std::min(std::min(most, 64 * place_waves(a.experts)), ((int)a.rows * L + 63) / 64 * 64);
+      hipLaunchKernelGGL((k_route_few<L, V, BY, SOFT, GROUPS>), dim3(1), dim3(block), pitch + 16 + (block / 64) * pitch + keys(block), st, a);
     } else {
-      hipLaunchKernelGGL((k_route_select<DT, L, V, BY>), dim3(blocks), dim3(std::min(1024, rows * L)), pitch_bytes(a.experts),
-                         st, a, rows);
+      const int block = std::min(most, rows * L);
+      hipLaunchKernelGGL((k_route_select<L, V, BY, SOFT, GROUPS>), dim3(blocks), dim3(block), pitch + keys(block), st, a, rows);
     }
   };
   const int e = a.experts;
@@ -616,18 +662,35 @@ static void launch_select(const RouteArgs& a, int blocks, int rows, hipStream_t 
   else if (e <= 512) go(wave, std::integral_constant<int, 8>{});
   else go(wave, std::integral_constant<int, 16>{});
 }
-template <int DT>
+template <int BY>
 static void launch_select_by(const RouteArgs& a, int blocks, int rows, hipStream_t st) {
-  if (a.bias || (a.groups > 1 && a.best == 2)) launch_select<DT, BY_P>(a, blocks, rows, st);
-  else launch_select<DT, BY_SCORE>(a, blocks, rows, st);
+  if (a.softmax) {
+    if (a.groups > 1) launch_select<BY, true, true>(a, blocks, rows, st);
+    else launch_select<BY, true, false>(a, blocks, rows, st);
+  } else {
+    if (a.groups > 1) launch_select<BY, false, true>(a, blocks, rows, st);
+    else launch_select<BY, false, false>(a, blocks, rows, st);
+  }
 }
 
-// Rows of a block of k_route_select, 0 where one launch does all: as many (in sixteens, a wave a SIMD) as
-// share the rows out over the compute units.
-static int select_rows(int64_t rows) {
-  if (rows <= FEW_ROWS) return 0;
-  const int64_t cus = vq_internal::persistent_blocks();
-  return (int)(((rows + cus - 1) / cus + 15) / 16 * 16);
+// Rows of a block of k_route_select, 0 where one launch does all (in one pass of its workgroup, also where
+// groups' keys fill LDS: 16 rows of 1024 experts in 64 groups take 86 us in one launch, 64 rows 36 in two;
+// without groups 64 rows of 160 take 13 us in one and 14 in two).  Otherwise as many whole waves as leave
+// the busiest compute unit the fewest rows, in one pass of a workgroup and no more than two workgroups a
+// compute unit (k_route_place reads every one's counts) while rows are few enough for that; passes one after
+// the other wait for each other's loads.
+static int select_rows(int64_t rows, int64_t experts) {
+  const int64_t wave = experts <= 256 ? 4 : 1;  // rows of a wave
+  if (rows <= (experts <= 64 ? 64 : 4 * wave)) return 0;
+  const int64_t cus = vq_internal::persistent_blocks(), share = (rows + cus - 1) / cus;
+  int64_t best = (share + 16 * wave - 1) / (16 * wave) * 16 * wave, cost = best + 1;
+  for (int64_t r = wave; r <= 16 * wave; r += wave) {
+    const int64_t blocks = (rows + r - 1) / r, c = (blocks + cus - 1) / cus * r;
+    if (blocks > 2 * cus || c >= cost) continue;
+    best = r;
+    cost = c;
+  }
+  return (int)best;
 }
 
 }  // namespace vqk
@@ -637,7 +700,7 @@ namespace vq_internal {
 using namespace vqk;
 
 int64_t route_experts_workspace_elems(int64_t rows, int64_t experts) {
-  const int per = select_rows(rows);
+  const int per = select_rows(rows, experts);
   return per ? (rows + per - 1) / per * ((experts + 3) & ~3) : 0;
 }
 
@@ -645,6 +708,7 @@ hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st) {
   RouteArgs a{};
   a.x = p.x;
   a.bias = p.bias;
+  a.dtype = p.dtype;
   a.ldx = p.ldx;
   a.rows = p.rows;
   a.experts = p.experts;
@@ -661,17 +725,16 @@ hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st) {
   a.chosen = p.chosen;
   a.place = p.place;
   a.counts = p.counts;
-  const int rows = select_rows(p.rows);
+  const int rows = select_rows(p.rows, p.experts);
   const int blocks = rows ? (int)((p.rows + rows - 1) / rows) : 0;
   if (p.rows) {
-    if (p.dtype == DT_F16) launch_select_by<DT_F16>(a, blocks, rows, st);
-    else if (p.dtype == DT_BF16) launch_select_by<DT_BF16>(a, blocks, rows, st);
-    else launch_select_by<DT_F32>(a, blocks, rows, st);
+    if (a.bias || (a.groups > 1 && a.best == 2)) launch_select_by<BY_P>(a, blocks, rows, st);
+    else launch_select_by<BY_SCORE>(a, blocks, rows, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !rows) return e;
   }
-  // Blocks of choices to place in one tile, where they fit one (without rows: zero offsets alone).
-  const int span = std::max(1, PLACE_TILE / std::max(1, rows * p.top)), grid = std::max(1, (blocks + span - 1) / span);
+  // Blocks of choices for two or four a lane, where that many fit (without rows: zero offsets alone).
+  const int span = std::max(1, 2048 / std::max(1, rows * p.top)), grid = std::max(1, (blocks + span - 1) / span);
   const int waves = place_waves(p.experts);
   const size_t lds = 2 * pitch_bytes(p.experts) + 16 + 4 * (size_t)waves * p.experts;
   hipLaunchKernelGGL(k_route_place, dim3(grid), dim3(64 * waves), lds, st, a, blocks, std::max(1, rows), span);

@@ -112,7 +112,7 @@ def test_route_validation(vq, kw, want):
 def test_route_workspace(vq):
     n = vq._lib.vq_route_experts_workspace_elems
     assert n(-1, 8) == n(8, 0) == n(8, 1025) == n((1 << 26) + 1, 8) == 0
-    assert n(0, 8) == n(64, 1024) == 0 and n(65, 1) > 0 and n(1 << 26, 1024) >= 1024
+    assert n(0, 8) == n(64, 64) == n(16, 256) == n(4, 1024) == 0 and n(17, 256) > 0 and n(5, 1024) > 0 and n(65, 1) > 0 and n(1 << 26, 1024) >= 1024
 
 
 def combine(vq, **kw):
