@@ -46,8 +46,9 @@ struct GatedArgs {
   const int32_t* idx;
   const float* sgiven;
   int64_t ldy, ldh, lds, ldn, ldg, ldsc, ldsh;
-  int64_t rows, sets, per;
+  int64_t rows, sets;
   double eps;
+  unsigned per;  // rows of a set without an index (rows < 2^31)
   float alpha;
   int k, kp, pw_f32, w_f32, mod_f32, post, norm, qbits, n_out, p1;
 };
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
       if constexpr (BR != BR_NONE) rad[j] = load8<TINY, PAST>(yr + at(j), a.k);
     }
     // The row's set of modulation rows; one outside them leaves the row without gate's branch, scale and shift.
-    const int64_t set = a.index ? a.index[rr] : rr / a.per;
+    const int64_t set = a.index ? a.index[rr] : (unsigned)rr / a.per;
     const bool set_ok = set >= 0 && set < a.sets;
     const int64_t st = set_ok ? set : 0;
     // Parameters are read again with each row (they stay in the cache); moved out of the loop they
@@ -462,7 +463,7 @@ hipError_t launch_gated_norm(const GatedNormParams& p, hipStream_t st) {
   a.ldsh = p.mod.ldsh;
   a.rows = p.rows;
   a.sets = p.mod.sets;
-  a.per = p.rows / p.mod.sets;
+  a.per = (unsigned)(p.rows / p.mod.sets);
   a.eps = p.eps;
   a.alpha = p.alpha;
   a.k = (int)p.k;

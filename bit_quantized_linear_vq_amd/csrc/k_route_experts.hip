@@ -528,7 +528,8 @@ struct CombineArgs {
   const int32_t* index;
   void* out;
   int64_t ldy, ldr, ldg, ldo;
-  int64_t rows, y_rows, sets, per;
+  int64_t rows, y_rows, sets;
+  unsigned per;  // rows of a set without an index
   int n, top, gate_f32;
 };
 
@@ -558,11 +559,11 @@ __device__ __forceinline__ void rows8(const void* p, int64_t at, int cnt, float*
 // wave has 512 elements of a row, so that the row's places and weights are scalars; four choices' rows
 // are on their way at once.
 template <int TY, int TO>
-__global__ __launch_bounds__(256) void k_combine(CombineArgs a, int segments, int64_t items) {
-  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void k_combine(CombineArgs a, unsigned segments, unsigned items) {
+  const unsigned item = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (item >= items) return;
   const int64_t row = item / segments;
-  const int e = (int)(item - row * segments) * 512 + 8 * (threadIdx.x & 63);
+  const int e = (int)(item % segments) * 512 + 8 * (threadIdx.x & 63);
   const int cnt = min(8, a.n - e);
   if (cnt <= 0) return;
   float r[8] = {};
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs a, int segments, in
   }
   bool ok = true;
   if (a.gate) {
-    const int64_t set = a.index ? a.index[row] : row / a.per;
+    const int64_t set = a.index ? a.index[row] : (unsigned)row / a.per;
     ok = set >= 0 && set < a.sets;
     float g[8];
     const int64_t ge = (ok ? set : 0) * a.ldg + e;
@@ -757,13 +758,12 @@ hipError_t launch_combine(const CombineParams& p, hipStream_t st) {
   a.rows = p.rows;
   a.y_rows = p.y_rows;
   a.sets = p.mod.sets;
-  a.per = std::max<int64_t>(1, p.rows / p.mod.sets);
+  a.per = (unsigned)std::max<int64_t>(1, p.rows / p.mod.sets);
   a.n = (int)p.n;
   a.top = p.top;
   a.gate_f32 = p.mod.f32;
-  const int segments = (int)((p.n + 511) / 512);
-  const int64_t items = p.rows * segments;
-  auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, st, a, segments, items); };
+  const unsigned segments = (unsigned)((p.n + 511) / 512), items = (unsigned)p.rows * segments;  // below 2^32
+  auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3(items / 4 + (items % 4 != 0)), dim3(256), 0, st, a, segments, items); };
   if (p.y_dt == DT_F32) {
     if (p.out_dt == DT_F32) go(k_combine<DT_F32, DT_F32>);
     else if (p.out_dt == DT_BF16) go(k_combine<DT_F32, DT_BF16>);

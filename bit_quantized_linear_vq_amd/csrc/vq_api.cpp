@@ -828,7 +828,7 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
   if (mod && (mod->scale || mod->shift)) return VQ_ERR_INVALID_ARG;
   if (is_16bit(y_dt) && is_16bit(out_dt) && y_dt != out_dt) return VQ_ERR_UNSUPPORTED;
   if (top > kMaxTop || n > kMaxExpertCols || m > kMaxExpertRows || y_rows > kMaxExpertRows) return VQ_ERR_UNSUPPORTED;
-  if ((n + 511) / 512 * m > ((int64_t)1 << 32)) return VQ_ERR_UNSUPPORTED;  // waves of its launch
+  if ((n + 511) / 512 * m >= ((int64_t)1 << 32) - 4) return VQ_ERR_UNSUPPORTED;  // waves of its launch, counted in 32 bits
   if (misaligned(y, elem_size(y_dt)) || misaligned(res, elem_size(out_dt)) || misaligned(out, elem_size(out_dt)) ||
       misaligned(place, 4) || misaligned(weights, 4))
     return VQ_ERR_SHAPE;

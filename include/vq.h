@@ -588,7 +588,7 @@ vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t expert
  *              itself (same pointer and stride)
  * Any n, strides and element-aligned addresses.  m = 0 enqueues nothing.  One kernel; nothing is
  * allocated.  Errors: INVALID_ARG, SHAPE (alignment, m % sets), UNSUPPORTED (top > 32, n > 2^20,
- * m or y_rows > 2^26, more than 2^32 pieces of 512 elements, y_dt and out_dt two 16-bit types).
+ * m or y_rows > 2^26, 2^32 pieces of 512 elements, y_dt and out_dt two 16-bit types).
  */
 vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64_t ldy, const int32_t* place,
                              const float* weights, int64_t m, int64_t n, int top, const void* res, int64_t ldr,
