@@ -278,10 +278,12 @@ __global__ __launch_bounds__(64) void k_lowrank_up_few(LowrankArgs g) {
   v4f t[RS][2];
   const float* pt = g.t + min(row, g.rows - 1) * g.rank + 8 * kq;
 #pragma unroll
-  for (int s = 0; s < RS; ++s) {
-    t[s][0] = t[s][1] = v4f{};
-    if (32 * s + 8 * kq < g.rank)
-      for (int q = 0; q < g.splits; ++q) {
+  for (int s = 0; s < RS; ++s) t[s][0] = t[s][1] = v4f{};
+#pragma unroll 4
+  for (int q = 0; q < g.splits; ++q) {
+#pragma unroll
+    for (int s = 0; s < RS; ++s)
+      if (32 * s + 8 * kq < g.rank) {
         const v4f* e = reinterpret_cast<const v4f*>(pt + (int64_t)q * g.rows * g.rank + 32 * s);
         t[s][0] += e[0];
         t[s][1] += e[1];
@@ -380,14 +382,19 @@ __global__ __launch_bounds__(64 * UP_WAVES) void k_lowrank_up(LowrankArgs g) {
   const int tr = threadIdx.x >> 4;
   v4f t[MB][CH];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const float* p = g.t + min(r0 + 16 * mb + tr, g.rows - 1) * g.rank;
+  for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = 4 * (rl + 16 * j);
-      t[mb][j] = v4f{};
-      if (c < g.rank)
-        for (int q = 0; q < g.splits; ++q) t[mb][j] += *reinterpret_cast<const v4f*>(p + (int64_t)q * g.rows * g.rank + c);
+    for (int j = 0; j < CH; ++j) t[mb][j] = v4f{};
+#pragma unroll 4
+  for (int q = 0; q < g.splits; ++q) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const float* p = g.t + (q * g.rows + min(r0 + 16 * mb + tr, g.rows - 1)) * g.rank;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const int c = 4 * (rl + 16 * j);
+        if (c < g.rank) t[mb][j] += *reinterpret_cast<const v4f*>(p + c);
+      }
     }
   }
   int list;
@@ -529,8 +536,11 @@ LowrankPlan lowrank_plan(int64_t rows, int adapters, int rank, int64_t k) {
   p.cb = rank <= 32 ? 2 : 4;
   const int64_t cols = (int64_t)std::min<int64_t>(std::min<int64_t>(16 * p.mb, rows), adapters) * rank;
   p.chunks = (int)std::min<int64_t>((cols + 16 * p.cb - 1) / (16 * p.cb), std::max<int64_t>(1, DOWN_GROUPS / p.tiles));
-  const int64_t most = std::max<int64_t>(1, DOWN_GROUPS / (p.tiles * p.chunks));
-  p.splits = (int)std::min<int64_t>(std::min<int64_t>(8, most), std::max<int64_t>(1, k / 512));
+  // Parts of 512 of K up to two workgroups a compute unit, of 2048 up to four (5159 rows, 7424, 323 tiles: three
+  // parts 44 -> 32 us; 13439 rows, 3520, 420 tiles: two parts 25 -> 27).  The second product adds up to eight.
+  const int64_t groups = p.tiles * p.chunks;
+  p.splits = (int)std::max<int64_t>({1, std::min<int64_t>({8, DOWN_GROUPS / groups, k / 512}),
+                                     std::min<int64_t>({8, 2 * DOWN_GROUPS / groups, k / 2048})});
   return p;
 }
 }  // namespace
@@ -561,12 +571,15 @@ template <int DT, int OUT_DT, int RS>
 static void launch_up_rs(LowrankArgs a, hipStream_t st) {
   // 64 rows of rank 32, 1920 -> 5760, 4.0 us with waves of their own, 7.6 with shared tiles of 32; 200 rows 7.6
   // and 7.0.  Tiles of 64 rows are no faster (17776 rows, rank 32, 92 against 87 us, rank 128 even).
-  const bool many = a.rows > 64;
-  constexpr int MB = 2;
-  const int rows = many ? 16 * MB : 16, cols = many ? UP_WAVES * UP_COLS : 32;
+  // Waves of their own, shared tiles of 16 rows, of 32 (us, 1920 -> 5760, rank 32: 64 rows 4.0, 4.8, 7.6; 200 rows
+  // 7.6, 5.2, 7.0; 1000 rows 13.2, 8.4, 8.9; 17776 rows -, 97, 87; fewer rows a tile read up more often).
+  // Tiles of 64 rows are no faster (17776 rows 92, rank 128 even).
+  const int mb = a.rows <= 64 ? 0 : a.rows < 1024 ? 1 : 2;
+  const int rows = mb == 2 ? 32 : 16, cols = mb ? UP_WAVES * UP_COLS : 32;
   a.col_tiles = (a.n + cols - 1) / cols;
   const dim3 grid((unsigned)((a.rows + rows - 1) / rows * a.col_tiles));
-  if (many) hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, MB, RS>), grid, dim3(64 * UP_WAVES), 0, st, a);
+  if (mb == 2) hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, 2, RS>), grid, dim3(64 * UP_WAVES), 0, st, a);
+  else if (mb == 1) hipLaunchKernelGGL((k_lowrank_up<DT, OUT_DT, 1, RS>), grid, dim3(64 * UP_WAVES), 0, st, a);
   else hipLaunchKernelGGL((k_lowrank_up_few<DT, OUT_DT, RS>), grid, dim3(64), 0, st, a);
 }
 template <int DT, int OUT_DT>
