@@ -237,9 +237,8 @@ template <int DT>
 __device__ __forceinline__ void fit_of(float top, float& fit, float& back) {
   fit = back = 1.0f;
   if constexpr (DT == DT_F16) {
-    const int e = (int)(f_bits(top) >> 23) - 127;
-    // without a finite, normal one nothing is scaled
-    const int by = top < bits_f(0x7F800000u) && e > -100 && e < 100 ? 13 - e : 0;
+    // (an infinite or NaN t is not scaled; 2^126 is the largest scale whose inverse is normal too)
+    const int by = top < bits_f(0x7F800000u) ? min(13 - ((int)(f_bits(top) >> 23) - 127), 126) : 0;
     fit = bits_f((unsigned)(127 + by) << 23);
     back = bits_f((unsigned)(127 - by) << 23);
   }

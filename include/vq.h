@@ -585,7 +585,7 @@ vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t expert
  *   mod        host or NULL: its gate [sets x n], F32 or of the 16-bit type among y_dt and out_dt, as
  *              for vq_gated_norm (scale and shift NULL); a row outside the sets is res[i], or 0
  *   out        device out_dt [m x n], stride ldo: y_dt or F32, any if y_dt is F32.  It may be res
- *              itself (same pointer and stride)
+ *              itself (same pointer and stride); no other overlap of inputs and outputs
  * Any n, strides and element-aligned addresses.  m = 0 enqueues nothing.  One kernel; nothing is
  * allocated.  Errors: INVALID_ARG, SHAPE (alignment, m % sets), UNSUPPORTED (top > 32, n > 2^20,
  * m or y_rows > 2^26, 2^32 pieces of 512 elements, y_dt and out_dt two 16-bit types).
@@ -612,7 +612,7 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
  *              a tile of 16 to 64 rows reads every adapter that occurs in it
  *   scale      device float [adapters], or NULL for ones
  *   base, out  device out_dt (dt or F32), [m x n], strides ldb, ldo; out may be base itself (same
- *              pointer and stride)
+ *              pointer and stride); no other overlap of inputs and outputs
  *   ws         device float scratch of vq_lowrank_workspace_elems(m, adapters, rank, k) elements, 16-byte
  *              aligned; calls that may run at the same time need one each
  * rank is 8 to 128, a multiple of 8 (a smaller adapter is padded with zeros); k % 64 == 0; any n.

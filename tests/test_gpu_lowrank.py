@@ -115,6 +115,16 @@ def test_loud_and_quiet_rows(vq, dt, size):
     check(vq.vq_lowrank_add(**on(c)), c, dt, "fp32")
 
 
+@pytest.mark.parametrize("m", [40, 1100])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("size", [1e33, 1e-30])
+def test_scales_at_the_ends_of_float32(vq, dt, size, m):
+    c = make(m, 96, 512, 16, 3, dt, "fp32", "any")
+    c["base"] = c["base"] * size
+    c["scales"] = c["scales"] * size
+    check(vq.vq_lowrank_add(**on(c)), c, dt, "fp32")
+
+
 def test_without_scales(vq):
     c = make(20, 64, 128, 8, 3, "bf16", "bf16", "any")
     c["scales"] = None
