@@ -568,8 +568,6 @@ static void launch_down(const LowrankArgs& a, const LowrankPlan& p, hipStream_t 
 
 template <int DT, int OUT_DT, int RS>
 static void launch_up_rs(LowrankArgs a, hipStream_t st) {
-  // 64 rows of rank 32, 1920 -> 5760, 4.0 us with waves of their own, 7.6 with shared tiles of 32; 200 rows 7.6
-  // and 7.0.  Tiles of 64 rows are no faster (17776 rows, rank 32, 92 against 87 us, rank 128 even).
   // Waves of their own, shared tiles of 16 rows, of 32 (us, 1920 -> 5760, rank 32: 64 rows 4.0, 4.8, 7.6; 200 rows
   // 7.6, 5.2, 7.0; 1000 rows 13.2, 8.4, 8.9; 17776 rows -, 97, 87; fewer rows a tile read up more often).
   // Tiles of 64 rows are no faster (17776 rows 92, rank 128 even).

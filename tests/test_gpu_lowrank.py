@@ -76,7 +76,7 @@ SHAPES = [
     (130, 257, 4096, 104, 7, "sorted"), (1024, 320, 128, 8, 6, "sorted"), (1100, 129, 320, 128, 9, "any"),
     (1030, 1030, 64, 72, 3, "sorted"), (64, 40, 512, 32, 2, "none"), (8200, 40, 256, 32, 5, "sorted"), (8197, 24, 128, 56, 30, "any"),
     (8300, 17, 192, 120, 4, "sorted"), (300, 130, 256, 48, 4, "sorted"), (100, 64, 9088, 64, 2, "any"), (65, 33, 8256, 8, 3, "any"),
-    (5200, 19, 4160, 16, 4, "sorted"), (1023, 70, 64, 24, 3, "any"),
+    (5200, 19, 4160, 16, 4, "sorted"), (1023, 70, 64, 24, 3, "any"), (8300, 1100, 64, 104, 9, "any"), (8200, 1283, 128, 40, 4, "sorted"),
 ]
 
 
