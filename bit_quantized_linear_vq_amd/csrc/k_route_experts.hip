@@ -562,6 +562,8 @@ __device__ __forceinline__ void rows8(const void* p, int64_t at, int cnt, float*
   }
 }
 
+constexpr unsigned COMBINE_WIDE = 1u << 23;  // workgroups along x: a launch has less than 2^32 threads there
+
 // TY: type of y; TO: of the residual and the output; gates in float32 or the 16-bit one of the two.  A
 // wave has 512 elements of a row, so that the row's places and weights are scalars; four choices' rows
 // are on their way at once.  Bound by the bytes of y, res and out: 17776 x 1920 of two choices with residual
@@ -569,7 +571,7 @@ __device__ __forceinline__ void rows8(const void* p, int64_t at, int cnt, float*
 // addresses, 22.4 us = 4.2 TB/s; eight rows 3.7 us.
 template <int TY, int TO>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs a, unsigned segments, unsigned items) {
-  const unsigned item = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned item = (blockIdx.y * COMBINE_WIDE + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (item >= items) return;
   const int64_t row = item / segments;
   const int e = (int)(item % segments) * 512 + 8 * (threadIdx.x & 63);
@@ -772,7 +774,9 @@ hipError_t launch_combine(const CombineParams& p, hipStream_t st) {
   a.top = p.top;
   a.gate_f32 = p.mod.f32;
   const unsigned segments = (unsigned)((p.n + 511) / 512), items = (unsigned)p.rows * segments;  // below 2^32
-  auto go = [&](auto k) { hipLaunchKernelGGL(k, dim3(items / 4 + (items % 4 != 0)), dim3(256), 0, st, a, segments, items); };
+  const unsigned blocks = items / 4 + (items % 4 != 0);
+  const dim3 grid(std::min(blocks, COMBINE_WIDE), (blocks + COMBINE_WIDE - 1) / COMBINE_WIDE);
+  auto go = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(256), 0, st, a, segments, items); };
   if (p.y_dt == DT_F32) {
     if (p.out_dt == DT_F32) go(k_combine<DT_F32, DT_F32>);
     else if (p.out_dt == DT_BF16) go(k_combine<DT_F32, DT_BF16>);

@@ -52,6 +52,21 @@ def test_combining(vq):
         assert torch.equal(out[at], want)
 
 
+@pytest.mark.parametrize("m,n", [(1 << 26, 1), ((1 << 25) + 3, 520)])
+def test_combining_of_many_rows(vq, m, n):
+    """2^26 pieces of a row and more: 2^32 threads."""
+    y = half(16, n)
+    place = torch.arange(m, dtype=torch.int32, device=DEV).remainder_(17).view(m, 1)  # the 17th is none
+    w = torch.ones(m, 1, device=DEV)
+    out = vq.vq_combine_experts(y, place, w)
+    want = torch.cat([y, torch.zeros_like(y[:1])])
+    whole = m // 17 * 17
+    for at in range(0, whole, 17 << 18):
+        part = out[at:min(whole, at + (17 << 18))].view(-1, 17, n)
+        assert bool((part == want).all()), at
+    assert torch.equal(out[whole:], want[:m - whole])
+
+
 @pytest.mark.parametrize("m,n,k", [(80000, 28672, 64), (270000, 16, 8192)])
 def test_adapters(vq, m, n, k):
     x, base = half(m, k), half(m, n, seed=1)
