@@ -550,7 +550,7 @@ int64_t lowrank_workspace_elems(int64_t rows, int64_t adapters, int64_t rank, in
 
 int64_t lowrank_groups(int64_t rows, int64_t adapters, int64_t rank, int64_t k, int64_t n) {
   const LowrankPlan p = lowrank_plan(rows, (int)adapters, (int)rank, k);
-  return std::max(p.tiles * p.chunks * p.splits, (rows + 15) / 16 * ((n + 31) / 32));
+  return std::max(p.tiles * p.chunks * p.splits, (rows + 31) / 32 * ((n + 255) / 256));
 }
 
 template <int DT>

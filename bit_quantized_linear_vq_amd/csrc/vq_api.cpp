@@ -883,7 +883,8 @@ vq_status vq_lowrank_add(const void* x, vq_dtype dt, int64_t m, int64_t n, int64
       misaligned(out, elem_size(out_dt)))
     return VQ_ERR_SHAPE;
   if (m == 0) return VQ_OK;
-  if (vq_internal::lowrank_groups(m, adapters, rank, k, n) > ((int64_t)1 << 30)) return VQ_ERR_UNSUPPORTED;
+  // Less than 2^32 threads of a launch.
+  if (vq_internal::lowrank_groups(m, adapters, rank, k, n) >= ((int64_t)1 << 24)) return VQ_ERR_UNSUPPORTED;
   vq_internal::LowrankParams p{};
   p.x = x;
   p.dtype = (int)dt;

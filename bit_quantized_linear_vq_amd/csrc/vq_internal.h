@@ -204,7 +204,7 @@ struct LowrankParams {
   float* t;
 };
 int64_t lowrank_workspace_elems(int64_t rows, int64_t adapters, int64_t rank, int64_t k);
-// Workgroups of the larger of its two launches, at most.
+// Workgroups of 256 threads of the larger of its two launches, where they are many.
 int64_t lowrank_groups(int64_t rows, int64_t adapters, int64_t rank, int64_t k, int64_t n);
 hipError_t launch_lowrank(const LowrankParams& p, hipStream_t st);
 

@@ -620,7 +620,7 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
  * m = 0 enqueues nothing.  Two kernels; nothing is allocated and the host does not read the index,
  * so a call may be captured in a graph and replayed with another index.
  * Errors: INVALID_ARG, SHAPE (k % 64, rank % 8, alignment), UNSUPPORTED (rank > 128, adapters > 2^20,
- * n or k > 2^24, more than 2^30 tiles).
+ * n or k > 2^24, 2^24 tiles of 32 rows or of 32 rows by 256 outputs).
  */
 int64_t vq_lowrank_workspace_elems(int64_t m, int64_t adapters, int64_t rank, int64_t k);
 vq_status vq_lowrank_add(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k, int64_t ldx, const void* down,

@@ -153,6 +153,7 @@ def lowrank(vq, **kw):
     (dict(base=NULL), INVALID), (dict(out=NULL), INVALID), (dict(ws=NULL), INVALID),
     (dict(r=136), UNSUP), (dict(ad=(1 << 20) + 1), UNSUP), (dict(n=(1 << 24) + 1, ldb=1 << 25, ldo=1 << 25), UNSUP),
     (dict(k=(1 << 24) + 64, ldx=1 << 25), UNSUP), (dict(m=(1 << 31) - 1, n=1 << 20, ldb=1 << 20, ldo=1 << 20), UNSUP),
+    (dict(m=1 << 29), UNSUP), (dict(m=1 << 20, n=1 << 17, ldb=1 << 17, ldo=1 << 17), UNSUP),
     (dict(r=12), SHAPE), (dict(k=96, ldx=96), SHAPE), (dict(ldx=132), SHAPE), (dict(x=ODD), SHAPE), (dict(down=ODD), SHAPE),
     (dict(up=ODD), SHAPE), (dict(ws=ODD), SHAPE), (dict(index=0x10002), SHAPE), (dict(scale=0x10002), SHAPE),
     (dict(base=BYTE), SHAPE), (dict(out=0x10002, odt=F32), SHAPE),
