@@ -41,7 +41,7 @@ struct LowrankArgs {
   const float* scale;  // or nullptr
   const void* base;
   void* out;
-  float* t;  // [splits, rows, rank]
+  float* t;  // [splits, rows, rank], of lowrank_t_rows rows in all
   int64_t ldx, ldb, ldo, rows;
   int adapters, rank, k, n, splits, chunks, col_tiles;
 };
@@ -518,6 +518,14 @@ using namespace vqk;
 
 namespace {
 constexpr int64_t DOWN_GROUPS = 512;  // two workgroups a compute unit
+constexpr int64_t MAX_PARTS = 8, PART_K = 512;
+// Rows of t in the scratch, over all parts of K.  A buffer made for a larger call (more rows, adapters, rank or
+// K) has to do for a smaller one, whose plan may have more parts, so this is no plan's own product but
+// what none exceeds: parts are at most MAX_PARTS and K / PART_K, and a plan with more than one has at most
+// 2 DOWN_GROUPS workgroups, each of at most 32 rows.
+int64_t lowrank_t_rows(int64_t rows, int64_t k) {
+  return std::max(rows, std::min(std::min(MAX_PARTS, std::max<int64_t>(1, k / PART_K)) * rows, 2 * DOWN_GROUPS * 32));
+}
 // How the first product is cut: tiles of 16 or 32 rows by blocks of 16 columns, workgroups of their own for
 // further columns, and for parts of K, while rows alone do not fill the compute units.
 struct LowrankPlan {
@@ -538,14 +546,14 @@ LowrankPlan lowrank_plan(int64_t rows, int adapters, int rank, int64_t k) {
   // Parts of 512 of K up to two workgroups a compute unit, of 2048 up to four (5159 rows, 7424, 323 tiles: three
   // parts 44 -> 32 us; 13439 rows, 3520, 420 tiles: two parts 25 -> 27).  The second product adds up to eight.
   const int64_t groups = p.tiles * p.chunks;
-  p.splits = (int)std::max<int64_t>({1, std::min<int64_t>({8, DOWN_GROUPS / groups, k / 512}),
-                                     std::min<int64_t>({8, 2 * DOWN_GROUPS / groups, k / 2048})});
+  p.splits = (int)std::max<int64_t>({1, std::min<int64_t>({MAX_PARTS, DOWN_GROUPS / groups, k / PART_K}),
+                                     std::min<int64_t>({MAX_PARTS, 2 * DOWN_GROUPS / groups, k / 2048})});
   return p;
 }
 }  // namespace
 
-int64_t lowrank_workspace_elems(int64_t rows, int64_t adapters, int64_t rank, int64_t k) {
-  return std::max<int64_t>(1, rows) * rank * lowrank_plan(rows, (int)adapters, (int)rank, k).splits;
+int64_t lowrank_workspace_elems(int64_t rows, int64_t rank, int64_t k) {
+  return lowrank_t_rows(std::max<int64_t>(1, rows), k) * rank;
 }
 
 int64_t lowrank_groups(int64_t rows, int64_t adapters, int64_t rank, int64_t k, int64_t n) {

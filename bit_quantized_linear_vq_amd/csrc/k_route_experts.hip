@@ -691,14 +691,16 @@ static void launch_select_by(const RouteArgs& a, int blocks, int rows, hipStream
 // the busiest compute unit the fewest rows, in one pass of a workgroup and no more than two workgroups a
 // compute unit (k_route_place reads every one's counts) while rows are few enough for that; passes one after
 // the other wait for each other's loads.
+static int64_t wave_rows(int64_t experts) { return experts <= 256 ? 4 : 1; }
+static int64_t most_select_blocks() { return 2 * (int64_t)vq_internal::persistent_blocks(); }
 static int select_rows(int64_t rows, int64_t experts) {
-  const int64_t wave = experts <= 256 ? 4 : 1;  // rows of a wave
+  const int64_t wave = wave_rows(experts);
   if (rows <= (experts <= 64 ? 64 : 4 * wave)) return 0;
   const int64_t cus = vq_internal::persistent_blocks(), share = (rows + cus - 1) / cus;
   int64_t best = (share + 16 * wave - 1) / (16 * wave) * 16 * wave, cost = best + 1;
   for (int64_t r = wave; r <= 16 * wave; r += wave) {
     const int64_t blocks = (rows + r - 1) / r, c = (blocks + cus - 1) / cus * r;
-    if (blocks > 2 * cus || c >= cost) continue;
+    if (blocks > most_select_blocks() || c >= cost) continue;
     best = r;
     cost = c;
   }
@@ -711,9 +713,12 @@ namespace vq_internal {
 
 using namespace vqk;
 
+// A buffer made for a larger call has to do for a smaller one, which may be cut into more blocks: so many
+// as no cut exceeds (blocks of a wave's rows or more, and at most most_select_blocks()).
 int64_t route_experts_workspace_elems(int64_t rows, int64_t experts) {
-  const int per = select_rows(rows, experts);
-  return per ? (rows + per - 1) / per * ((experts + 3) & ~3) : 0;
+  if (!select_rows(rows, experts)) return 0;
+  const int64_t wave = wave_rows(experts);
+  return std::min((rows + wave - 1) / wave, most_select_blocks()) * ((experts + 3) & ~3);
 }
 
 hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st) {

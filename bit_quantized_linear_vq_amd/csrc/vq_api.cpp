@@ -864,7 +864,7 @@ bool lowrank_sizes(int64_t m, int64_t adapters, int64_t rank, int64_t k) {
 }  // namespace
 
 int64_t vq_lowrank_workspace_elems(int64_t m, int64_t adapters, int64_t rank, int64_t k) {
-  return lowrank_sizes(m, adapters, rank, k) ? vq_internal::lowrank_workspace_elems(m, adapters, rank, k) : 0;
+  return lowrank_sizes(m, adapters, rank, k) ? vq_internal::lowrank_workspace_elems(m, rank, k) : 0;
 }
 
 vq_status vq_lowrank_add(const void* x, vq_dtype dt, int64_t m, int64_t n, int64_t k, int64_t ldx, const void* down,

@@ -169,6 +169,7 @@ struct RouteExpertsParams {
   int32_t* place;
   int32_t* counts;  // route_experts_workspace_elems
 };
+// Not smaller for more rows or experts.
 int64_t route_experts_workspace_elems(int64_t rows, int64_t experts);
 hipError_t launch_route_experts(const RouteExpertsParams& p, hipStream_t st);
 struct CombineParams {
@@ -203,7 +204,8 @@ struct LowrankParams {
   int64_t ldb, ldo;
   float* t;
 };
-int64_t lowrank_workspace_elems(int64_t rows, int64_t adapters, int64_t rank, int64_t k);
+// Not smaller for more rows, a larger rank or a longer K.
+int64_t lowrank_workspace_elems(int64_t rows, int64_t rank, int64_t k);
 // Workgroups of 256 threads of the larger of its two launches, where they are many.
 int64_t lowrank_groups(int64_t rows, int64_t adapters, int64_t rank, int64_t k, int64_t n);
 hipError_t launch_lowrank(const LowrankParams& p, hipStream_t st);

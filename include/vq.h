@@ -559,8 +559,8 @@ vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const
  *   weights    device float [m x top];  chosen, place: device int32 [m x top] (place: where the
  *              choice is in the sorted order)
  *   ws         device int32 scratch of vq_route_experts_workspace_elems(m, experts) elements, 16-byte
- *              aligned (NULL where that is 0, for a few rows); calls that may run at the same time need
- *              one each
+ *              aligned (NULL where that is 0, for a few rows); one made for a larger m or more experts does
+ *              for a smaller call; calls that may run at the same time need one each
  * m = 0 writes zero offsets.  Places are the same in every call (no order of atomics enters).
  * Nothing is allocated and the host reads nothing, so a call may be captured.
  * Errors: INVALID_ARG (also top > experts of the kept groups, experts % groups, group_best > a
@@ -614,7 +614,8 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
  *   base, out  device out_dt (dt or F32), [m x n], strides ldb, ldo; out may be base itself (same
  *              pointer and stride); no other overlap of inputs and outputs
  *   ws         device float scratch of vq_lowrank_workspace_elems(m, adapters, rank, k) elements, 16-byte
- *              aligned; calls that may run at the same time need one each
+ *              aligned; one made for a larger m, rank or k, whatever its adapters, does for a smaller call;
+ *              calls that may run at the same time need one each
  * rank is 8 to 128, a multiple of 8 (a smaller adapter is padded with zeros); k % 64 == 0; any n.
  * An infinity or NaN in a row of x or in an adapter shows in that row or that adapter's rows alone.
  * m = 0 enqueues nothing.  Two kernels; nothing is allocated and the host does not read the index,
