@@ -9,9 +9,12 @@
 // with mean = fl32(sum x / K) for a layer norm and 0 for a root-mean-square one, and
 // rstd = fl32(1 / sqrt(sum x^2 / K - (sum x / K)^2 + eps)).
 //
-// Sums, moments, division and root are float64: a 16-bit value and its square are exact there, so
-// a sum of them loses at most K 2^-53 of its terms' size, and the variance, from one pass, keeps
-// 2^-53 (mean / deviation)^2 of it: a mean a thousand times the deviation still leaves it 33 bits.
+// Sums, moments, division and root are float64: a 16-bit value and its square are exact there, and a
+// sum of them loses at most some 2^-53 of its terms' size.  A layer norm's variance is (K S2 - S1^2) / K^2 of one pass's
+// sums, both products in two parts: rounded (or as S2 / K - mean^2) their difference keeps only 2^-53
+// (mean / deviation)^2 of itself, tens of float32 steps for fp16 rows of which one or two elements differ.  Nothing
+// else is lost: in a row without an element below 2^-7 of its largest the sums are exact (squares of 11-bit values, 2^15
+// of them, within 53 bits), and in any other the square of the mean is at most about 2 K times the variance.
 // The float32 statistics, and with them the codes, do not depend on the order of the sums.
 //
 // Work layout as in the norm of one sum: T threads own a row, each NP pieces of 8 elements that
@@ -216,11 +219,15 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
           s2 += s_sum[buf][which][rib * wpr + w][1];
         }
       }
-      const double mu = kind == NORM_LAYER ? s1 / kd : 0.0;
-      // (NaN stays: max would take it away)
-      double var = s2 / kd - mu * mu;
-      var = var < 0.0 ? 0.0 : var;
-      mean = (float)mu;
+      double var = s2 / kd;
+      mean = 0.0f;
+      if (kind == NORM_LAYER) {
+        const double q = kd * s2, p = s1 * s1;
+        var = ((q - p) + (__builtin_fma(kd, s2, -q) - __builtin_fma(s1, s1, -p))) / (kd * kd);
+        // (NaN stays: max would take it away)
+        var = var < 0.0 ? 0.0 : var;
+        mean = (float)(s1 / kd);
+      }
       rstd = (float)(1.0 / sqrt(var + a.eps));
     };
 
