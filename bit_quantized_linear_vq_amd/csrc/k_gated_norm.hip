@@ -252,9 +252,10 @@ __global__ __launch_bounds__(1024) void k_gated_norm(GatedArgs a, int T) {
               if (pw) u[t] = u[t] * p[2 * i + t];
             }
             const float ga = a.gate ? g[2 * i + t] * a.alpha : a.alpha;
-            u[t] = set_ok ? x[t] + u[t] * ga : x[t];
+            u[t] = x[t] + u[t] * ga;
           }
-          raw[j][i] = cvt_pair<DT>(u[0], u[1]);
+          const unsigned sum = cvt_pair<DT>(u[0], u[1]);
+          raw[j][i] = set_ok ? sum : raw[j][i];  // h as it is, a NaN's bits too
         }
       }
     }

@@ -96,3 +96,14 @@ def test_an_infinity_or_nan_anywhere_in_a_row(vq, norm, k, m):
                 want[:] = float("nan")
             assert torch.equal(n[1].float().nan_to_num(7.0), want.nan_to_num(7.0)), (at, v)
             assert torch.equal(n[[0, 2]], good[[0, 2]])
+
+
+def test_rows_outside_the_sets_keep_every_bit(vq):
+    """Also those of a NaN, quiet or signaling, and of numbers below the normal range."""
+    for dt, odd in ((torch.bfloat16, [0x7F81, 0x7FC1, 0xFFFF, 0x7F80, 0x0001, 0x8000]), (torch.float16, [0x7C01, 0x7E55, 0xFFFF, 0x7C00, 0x0001, 0x8000])):
+        h = torch.randn(6, 256, device=DEV).to(dt)
+        h.view(torch.int16)[3, 10:16] = torch.tensor(odd, dtype=torch.int32).to(torch.int16).to(DEV)
+        index = torch.tensor([0, 1, 0, 2, 1, -1], dtype=torch.int32, device=DEV)
+        for post in (None, "rms"):
+            _, s = vq.vq_gated_norm(torch.randn_like(h), h, post=post, gate=torch.ones(2, 256, device=DEV), index=index)
+            assert torch.equal(s.view(torch.int16)[[3, 5]], h.view(torch.int16)[[3, 5]])
