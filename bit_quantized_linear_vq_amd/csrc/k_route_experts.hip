@@ -632,6 +632,10 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs a, unsigned segment
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = cvt_pair<TO>(v[2 * i], v[2 * i + 1]);
     uint16_t* p = reinterpret_cast<uint16_t*>(a.out) + o;
+    if (!ok && a.res) {  // the residual as it is, a NaN's bits too
+      const uint16_t* rp = reinterpret_cast<const uint16_t*>(a.res) + row * a.ldr + e;
+      q = cnt == 8 ? load8<false, false>(rp, 8) : load8<true, false>(rp, cnt);
+    }
     if (cnt == 8) store8<false, false>(p, q, 8);
     else store8<true, false>(p, q, cnt);
   }
