@@ -13,10 +13,11 @@
 //                   matter, and places are the same in every call.
 //   k_route_few     both for a few rows: 64 of up to 64 experts, 16 of 256, 4 of more
 // Bound by latency and by instructions (17776 rows of 160 scores are 11 MB): a row's exponentials, and for
-// each choice a maximum over the row's lanes.  Sixteen lanes a row, since the maximum's steps are then
+// each choice a maximum over the row's lanes.  (Exponentials of a softmax's sum by the hardware's float32 2^x took
+// 11.2 us instead of 12.7, and put 2^-22 on the weights; they are float64.)  Sixteen lanes a row, since the maximum's steps are then
 // register moves that four rows share (a wave a row: 17776 x 160 28 us instead of 14).
 //
-// Measured: 17776 rows of 160, softmax, six choices, 11.2 + 10.4 us; 4124 of 96 in six groups, sigmoid with
+// Measured: 17776 rows of 160, softmax, six choices, 12.7 + 10.5 us; 4124 of 96 in six groups, sigmoid with
 // a bias, four choices, 9.7 + 8.2 us; one row of 16 3.8 us.  The placing waits for loads one after the
 // other: every block's counts and its choices, then LDS.
 #include <algorithm>
@@ -123,14 +124,6 @@ __device__ __forceinline__ double exp_d(double x) {
   return __builtin_ldexp(p, (int)n);
 }
 
-// e^x of x <= 0 to 2^-22 of it, for the sum under weights that end in float32: x / ln 2 in float64, its
-// fraction by the hardware's 2^f (1 ulp, and f's own rounding, 2^-26).
-__device__ __forceinline__ float exp_f(double x) {
-  const double y = fmax(x, -800.0) * 1.4426950408889634;
-  const double n = __builtin_rint(y);
-  return __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
-}
-
 // What the choice goes by.  BY_SCORE: the scores themselves, exact in float32.  BY_P: p (+ bias), in
 // float64 for every expert.
 enum : int { BY_SCORE = 0, BY_P = 1 };
@@ -171,19 +164,12 @@ __device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row, int l
   double per = 1.0;
   if (SOFT && (BY == BY_P || !a.renorm)) {
     double sum = 0.0;
-    if constexpr (BY == BY_P) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        p[i] = exp_d((double)x[i] - base);
-        sum += p[i];
-        if (i & 1) __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        sum += (double)exp_f((double)x[i] - base);
-        if (i & 1) __builtin_amdgcn_sched_barrier(0);
-      }
+    for (int i = 0; i < VPT; ++i) {
+      const double t = exp_d((double)x[i] - base);
+      if constexpr (BY == BY_P) p[i] = t;
+      sum += t;
+      if (i & 1) __builtin_amdgcn_sched_barrier(0);
     }
     sum = sum_of<LPR>(sum);
     per = sum > 0.0 ? 1.0 / sum : 1.0;

@@ -546,9 +546,8 @@ vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const
  *   chosen[i,0..top)  the experts of the largest c, descending
  *   weights[i,j] = p[i,chosen] / (renorm ? sum_j p[i,chosen] : 1) * scale  (0 where that sum is 0)
  * Ties go to the lower index, among groups and experts alike.  What is compared is exact or
- * computed in float64; weights are computed in float64 and rounded once to float32 (a softmax
- * that is not renormalised, chosen by the scores, sums its denominator of terms to 2^-22).  An expert whose score or bias is -infinity is
- * closed to the token: never chosen, with p = 0.  Where fewer than top experts are open the
+ * computed in float64; weights are computed in float64 and rounded once to float32.  An expert whose score or
+ * bias is -infinity is closed to the token: never chosen, with p = 0.  Where fewer than top experts are open the
  * remaining choices are expert -1, place -1 and weight 0.  A row with a NaN score or c, or (softmax)
  * an infinite score, is not routed: -1 throughout, and NaN weights.
  *   x          device, dt in {F16, BF16, F32}, [m x experts], stride ldx

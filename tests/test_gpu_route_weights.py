@@ -1,0 +1,46 @@
+"""Weights of the routing against the definition in 64 bits (oracle/router.py): float64 values rounded once, so
+within half a step of float32, 2^-24, and what E float64 operations may add, E 2^-50."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import router
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def vq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_quantized_linear_vq_amd as m
+    return m
+
+
+def scores(m, e, seed=0, masked=0.0):
+    rng = np.random.default_rng([m, e, seed])
+    x = (1.5 * rng.standard_normal((m, e))).astype(np.float32)
+    x[rng.random((m, e)) < masked] = -np.inf
+    return torch.from_numpy(x)
+
+
+def check(got, x, top, scale=1.0, bias=None, top_groups=None, group_best=1, **how):
+    torch.cuda.synchronize()
+    off, rows, w, ch, place = (t.cpu().numpy() for t in got)
+    want = router.route(x.double().numpy(), top, bias=None if bias is None else bias.double().numpy(), keep=top_groups, best=group_best, **how)
+    assert np.array_equal(ch, want[3]) and np.array_equal(off, want[0]) and np.array_equal(rows, want[1]) and np.array_equal(place, want[4])
+    exact = want[2] * scale
+    assert np.all(np.abs(w.astype(np.float64) - exact) <= (2.0 ** -24 + x.shape[1] * 2.0 ** -50) * np.abs(exact) + 2.0 ** -150)
+    return w
+
+
+@pytest.mark.parametrize("m,e,top,how", [
+    (3, 7, 2, {}), (300, 16, 3, {}), (500, 160, 6, {}), (200, 256, 8, dict(groups=8, top_groups=3)), (150, 300, 5, {}), (100, 1024, 9, {}),
+    (40, 64, 4, {}), (400, 96, 4, dict(groups=4, top_groups=2)),
+])
+def test_a_softmax_that_is_not_renormalised(vq, m, e, top, how):
+    for masked in (0.0, 0.1):
+        x = scores(m, e, masked=masked)
+        check(vq.vq_route_experts(x.to(DEV), top, renorm=False, **how), x, top, renorm=False, **how)
