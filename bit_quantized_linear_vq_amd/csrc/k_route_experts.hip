@@ -36,7 +36,7 @@ struct RouteArgs {
   int64_t ldx;
   int64_t rows;
   int dtype, experts, top, groups, keep, best, softmax, renorm;
-  float scale;
+  double scale;
   int32_t* offsets;
   int32_t* row_of;  // [rows * top]
   float* weights;   // [rows, top]
@@ -286,7 +286,7 @@ __device__ __forceinline__ void route_row(const RouteArgs& a, int64_t row, int l
     for (int j = 0; j < 2; ++j) w[j] = w[j] / by;
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) wt[j] = bad ? bits_f(0x7FC00000u) : (float)(w[j] * (double)a.scale);
+  for (int j = 0; j < 2; ++j) wt[j] = bad ? bits_f(0x7FC00000u) : (float)(w[j] * a.scale);
 }
 
 // Weights and choices of a row, stored; its choices counted in LDS.

@@ -809,7 +809,7 @@ vq_status vq_route_experts(const void* x, vq_dtype dt, int64_t m, int64_t expert
   p.best = group_best;
   p.softmax = score == VQ_SCORE_SOFTMAX;
   p.renorm = renorm != 0;
-  p.scale = (float)scale;
+  p.scale = scale;
   p.offsets = offsets;
   p.row_of = rows;
   p.weights = weights;

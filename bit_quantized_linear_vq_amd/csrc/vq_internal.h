@@ -161,7 +161,7 @@ struct RouteExpertsParams {
   const float* bias;  // or nullptr
   int64_t ldx, rows;
   int experts, top, groups, keep, best, softmax, renorm;
-  float scale;
+  double scale;
   int32_t* offsets;
   int32_t* row_of;
   float* weights;

@@ -552,6 +552,7 @@ vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const
  * an infinite score, is not routed: -1 throughout, and NaN weights.
  *   x          device, dt in {F16, BF16, F32}, [m x experts], stride ldx
  *   bias       device float [experts] or NULL
+ *   scale      finite, also as a float32; taken as it is
  *   offsets    device int32 [experts + 1]: expert e's choices are at [offsets[e], offsets[e + 1])
  *   rows       device int32 [m * top]: the token of each sorted choice, in an expert by ascending
  *              token; -1 from offsets[experts] on

@@ -43,7 +43,7 @@ def choose(x, top, score="softmax", bias=None, groups=1, keep=None, best=1, reno
     if renorm:
         w = [v / total if total > 0 else 0.0 for v in w]
     none = top - len(order)
-    return order + [-1] * none, [v * float(F(scale)) for v in w] + [0.0] * none
+    return order + [-1] * none, [v * scale for v in w] + [0.0] * none
 
 
 def route(x, top, **how):

@@ -44,3 +44,12 @@ def test_a_softmax_that_is_not_renormalised(vq, m, e, top, how):
     for masked in (0.0, 0.1):
         x = scores(m, e, masked=masked)
         check(vq.vq_route_experts(x.to(DEV), top, renorm=False, **how), x, top, renorm=False, **how)
+
+
+@pytest.mark.parametrize("scale", [0.1, 2.446, 1.0 / 3.0, -0.7])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_a_scale_that_float32_does_not_hold(vq, renorm, score, scale):
+    for m in (20, 400):
+        x = scores(m, 48)
+        check(vq.vq_route_experts(x.to(DEV), 5, score=score, renorm=renorm, scale=scale), x, 5, scale, score=score, renorm=renorm)
