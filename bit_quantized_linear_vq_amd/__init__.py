@@ -1125,9 +1125,9 @@ def vq_route_experts(scores: torch.Tensor, top: int, score: str = "softmax", bia
 
     score: "softmax" or "sigmoid".  bias (float32 [E]) is added for the choice only.  groups,
     top_groups, group_best: only the experts of the top_groups groups (default all) whose best one
-    or two sum highest.  Scores of -inf close an expert to a token.  Returns (offsets int32 [E + 1],
-    rows int32 [M * top], weights float32 [M x top], experts int32 [M x top], place int32 [M x top]):
-    offsets and rows as the experts' products take them, place and weights as vq_combine_experts does."""
+    or two sum highest.  Scores or biases of -inf close an expert (a bias leaves the weights' p as
+    they are).  Returns (offsets int32 [E + 1], rows int32 [M * top], weights float32 [M x top], experts int32
+    [M x top], place int32 [M x top]): offsets and rows as the experts' products take them, place and weights as vq_combine_experts does."""
     ldx = _rows_any(scores, "scores", None, _ANY)
     m, e = scores.shape
     dev, device = scores.get_device(), scores.device

@@ -547,9 +547,10 @@ vq_status vq_gemm_dense_experts(const void* x, const void* w, vq_dtype dt, const
  *   weights[i,j] = p[i,chosen] / (renorm ? sum_j p[i,chosen] : 1) * scale  (0 where that sum is 0)
  * Ties go to the lower index, among groups and experts alike.  What is compared is exact or
  * computed in float64; weights are computed in float64 and rounded once to float32.  An expert whose score or
- * bias is -infinity is closed to the token: never chosen, with p = 0.  Where fewer than top experts are open the
- * remaining choices are expert -1, place -1 and weight 0.  A row with a NaN score or c, or (softmax)
- * an infinite score, is not routed: -1 throughout, and NaN weights.
+ * bias is -infinity is closed to the token, that is never chosen.  Closed by its score it has p = 0;
+ * a bias moves the choice alone, so an expert closed by its bias keeps its p and its share of a softmax's
+ * sum.  Where fewer than top experts are open the remaining choices are expert -1, place -1 and weight 0.
+ * A row with a NaN score or c, or (softmax) an infinite score, is not routed: -1 throughout, and NaN weights.
  *   x          device, dt in {F16, BF16, F32}, [m x experts], stride ldx
  *   bias       device float [experts] or NULL
  *   scale      finite, also as a float32; taken as it is

@@ -2,8 +2,8 @@
 
 Row by row, choice by choice, in float64: scores p (softmax or sigmoid), c = p + bias (the scores
 themselves without a bias) for the choice, groups by the sum of their best one or two, ties to the
-lower index, weights p / sum p.  Closed experts (score or bias -inf) are never chosen; a row with a
-NaN (or, for softmax, an infinite score) is not routed and has NaN weights.
+lower index, weights p / sum p.  Closed experts (score or bias -inf) are never chosen (a bias leaves p
+as it is); a row with a NaN (or, for softmax, an infinite score) is not routed and has NaN weights.
 """
 from __future__ import annotations
 

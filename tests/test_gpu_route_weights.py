@@ -53,3 +53,21 @@ def test_a_scale_that_float32_does_not_hold(vq, renorm, score, scale):
     for m in (20, 400):
         x = scores(m, 48)
         check(vq.vq_route_experts(x.to(DEV), 5, score=score, renorm=renorm, scale=scale), x, 5, scale, score=score, renorm=renorm)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("how", [{}, dict(groups=4, top_groups=2, group_best=2)])
+def test_an_expert_closed_by_its_bias_is_never_chosen_and_keeps_its_share(vq, how, renorm, score):
+    """A bias moves the choice alone: the others' p are what they are without it."""
+    m, e = 200, 40
+    x = scores(m, e)
+    bias = torch.linspace(-0.1, 0.1, e)
+    bias[::7] = -float("inf")
+    got = vq.vq_route_experts(x.to(DEV), 4, score=score, renorm=renorm, bias=bias.to(DEV), **how)
+    w = check(got, x, 4, score=score, renorm=renorm, bias=bias, **how)
+    ch = got[3].cpu().long()
+    assert not torch.isin(ch, torch.arange(0, e, 7)).any()
+    if not renorm:
+        p = torch.softmax(x.double(), 1) if score == "softmax" else torch.sigmoid(x.double())
+        assert np.allclose(w, torch.gather(p, 1, ch).numpy(), rtol=2.0 ** -23, atol=0)
