@@ -71,3 +71,20 @@ def test_an_expert_closed_by_its_bias_is_never_chosen_and_keeps_its_share(vq, ho
     if not renorm:
         p = torch.softmax(x.double(), 1) if score == "softmax" else torch.sigmoid(x.double())
         assert np.allclose(w, torch.gather(p, 1, ch).numpy(), rtol=2.0 ** -23, atol=0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("m", [3, 20, 150])
+@pytest.mark.parametrize("e,top,how", [
+    (161, 6, {}), (192, 8, dict(groups=8, top_groups=4, group_best=2)), (200, 8, {}), (224, 8, dict(groups=7, top_groups=3)),
+    (256, 8, {}), (256, 8, dict(groups=8, top_groups=4, group_best=2)), (256, 32, dict(groups=64, top_groups=20)),
+    (513, 5, {}), (600, 8, dict(groups=6, top_groups=2, group_best=2)), (1024, 32, {}), (1024, 9, dict(groups=64, top_groups=9, group_best=2)),
+])
+def test_many_experts_chosen_by_p(vq, e, top, how, m, score):
+    x = scores(m, e, masked=0.1)
+    bias = 0.05 * torch.randn(e, generator=torch.Generator().manual_seed(e))
+    for renorm in (True, False):
+        check(vq.vq_route_experts(x.to(DEV), top, score=score, bias=bias.to(DEV), renorm=renorm, **how), x, top, score=score, bias=bias,
+              renorm=renorm, **how)
+    if how.get("group_best") == 2:
+        check(vq.vq_route_experts(x.to(DEV), top, score=score, **how), x, top, score=score, **how)
