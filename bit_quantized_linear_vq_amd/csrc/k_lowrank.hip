@@ -10,11 +10,13 @@
 //   k_lowrank_up    out = base + t . up^T: a tile goes through the adapters of its rows one after the
 //                   other, and each row takes the one that is its own.  Sums of different adapters do
 //                   not meet, so an infinity or NaN in one adapter stays out of the other requests' rows.
-// t, scaled, enters the second product as the sum of two 16-bit values (hi = RNE16(t), lo = RNE16(t - hi)):
-// rounded once it would cost the output up to 2^-9 of the adapter's part in bfloat16, in two
-// pieces 2^-17 (fp16 2^-22), for a second matrix instruction in a kernel that waits for memory.  An
-// fp16 row is scaled by the power of two that brings its largest |t| to [2^13, 2^14), since t is not bound to
-// fp16's range; the products are scaled back, both exactly (a lo below 2^-24 is lost).
+// t, scaled, enters the second product as the sum of two 16-bit values, hi and lo = RNE16(t - hi): rounded once
+// it would cost the output up to 2^-9 of the adapter's part in bfloat16, in two pieces 2^-16 (fp16
+// 2^-22), for a second matrix instruction in a kernel that waits for memory.  hi is cut off, so that lo has t's
+// sign, and neither is zero where t is not: an infinity in up times t is then the infinity that the
+// formula gives, and not NaN.  (Taking NaN sums from hi alone costs the inner loop 84 -> 93 us, rank 128 159 ->
+// 196.)  An fp16 row is scaled by the power of two that brings its largest |t| to [2^13, 2^14), since t is not
+// bound to fp16's range; the products are scaled back, both exactly (a lo below 2^-24 is lost).
 //
 // Measured, three sets of buffers in turn: 17776 rows of seven requests, 1920 -> 5760, rank 32, 31 + 85 us (base
 // and out alone are 79 us at a large copy's rate, and take 78 in a copy with this access pattern), rank 64
@@ -243,16 +245,32 @@ __device__ __forceinline__ void fit_of(float top, float& fit, float& back) {
     back = bits_f((unsigned)(127 - by) << 23);
   }
 }
+// t moved a unit of its last place towards zero (an infinity to the largest number), 0 as it is.
+__device__ __forceinline__ unsigned inward(float t) { return f_bits(t) - (t != 0.0f ? 1u : 0u); }
+// Two values of t cut off to their upper pieces; t becomes what is left, which is not zero and of t's sign.
+template <int DT>
+__device__ __forceinline__ unsigned upper(float& t0, float& t1) {
+  if constexpr (DT == DT_BF16) {
+    const unsigned u0 = inward(t0), u1 = inward(t1);
+    t0 -= bits_f(u0 & 0xFFFF0000u);
+    t1 -= bits_f(u1 & 0xFFFF0000u);
+    return u0 >> 16 | (u1 & 0xFFFF0000u);
+  } else {
+    // (at least 3 2^-26 is left of all but the smallest, which rounds to 2^-24, the least of fp16)
+    const float i0 = bits_f(inward(t0)) - copysignf(0x1.8p-25f, t0), i1 = bits_f(inward(t1)) - copysignf(0x1.8p-25f, t1);
+    const unsigned u = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_pkrtz(i0, i1));
+    float h0, h1;
+    decode2<DT>(u, h0, h1);
+    t0 -= h0;
+    t1 -= h1;
+    return u;
+  }
+}
 // Two values of t in two pieces each.
 template <int DT>
 __device__ __forceinline__ void pieces(float t0, float t1, unsigned& hi, unsigned& lo) {
-  hi = cvt_pair<DT>(t0, t1);
-  float h0, h1;
-  decode2<DT>(hi, h0, h1);
-  // an infinite hi has no rest
-  const float d0 = fabsf(h0) < bits_f(0x7F800000u) ? t0 - h0 : 0.0f;
-  const float d1 = fabsf(h1) < bits_f(0x7F800000u) ? t1 - h1 : 0.0f;
-  lo = cvt_pair<DT>(d0, d1);
+  hi = upper<DT>(t0, t1);
+  lo = cvt_pair<DT>(t0, t1);
 }
 // A step of 32 of the rank from row q of up: eight elements a lane.
 template <typename V8>

@@ -618,7 +618,8 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
  *              aligned; one made for a larger m, rank or k, whatever its adapters, does for a smaller call;
  *              calls that may run at the same time need one each
  * rank is 8 to 128, a multiple of 8 (a smaller adapter is padded with zeros); k % 64 == 0; any n.
- * An infinity or NaN in a row of x or in an adapter shows in that row or that adapter's rows alone.
+ * An infinity or NaN in a row of x or in an adapter shows in that row or that adapter's rows alone, as the formula
+ * has it (an infinity of up beside a |t| below 2^-100, F16 2^-36 T, may show as NaN).
  * m = 0 enqueues nothing.  Two kernels; nothing is allocated and the host does not read the index,
  * so a call may be captured in a graph and replayed with another index.
  * Errors: INVALID_ARG, SHAPE (k % 64, rank % 8, alignment), UNSUPPORTED (rank > 128, adapters > 2^20,

@@ -1,0 +1,57 @@
+"""Low-rank adapters: infinities among their weights."""
+import numpy as np
+import pytest
+import torch
+
+import gen
+from oracle import lowrank as ol
+from oracle import numerics as onum
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def vq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import bit_quantized_linear_vq_amd as m
+    return m
+
+
+def f64(t, dt):
+    return onum.to_f32(gen.as_numpy_bits(t), dt).astype(np.float64)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("r", [8, 64, 104])
+@pytest.mark.parametrize("m", [5, 200, 1100])
+def test_an_infinite_weight_of_up_is_an_infinity_of_its_sign(vq, m, r, dt):
+    """t times an infinity, whatever the pieces in which t goes on: its own sign where t is not zero, NaN where
+    t is zero or two infinities meet, and the other columns as they are."""
+    rng = np.random.default_rng([m, r])
+    k, n, ad = 64, 70, 3
+
+    def whole(shape, big):
+        return rng.integers(-big, big + 1, shape).astype(np.float32)
+    x, down = gen.to_storage(whole((m, k), 4), dt), gen.to_storage(whole((ad, r, k), 3), dt)
+    u = whole((ad, n, r), 5)
+    u[1, 3, 2], u[1, 40, 0], u[1, 69, r - 1] = np.inf, -np.inf, np.inf
+    u[2, 10, 1], u[2, 10, 4] = np.inf, -np.inf
+    up = gen.to_storage(u, dt)
+    index = torch.from_numpy(rng.integers(-1, ad, m).astype(np.int32))
+    scales = torch.tensor([1.0, 0.5, 0.3])
+    base = torch.from_numpy(whole((m, n), 99))
+    x[0] = 0  # t = 0: NaN in those columns
+    index[:3] = torch.tensor([1, 1, 2])
+    got = vq.vq_lowrank_add(base.to(DEV), x.to(DEV), down.to(DEV), up.to(DEV), index.to(DEV), scales=scales.to(DEV))
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        delta, bound = ol.exact(f64(x, dt), f64(down, dt), f64(up, dt), index.numpy(), scales.numpy(), dt)
+    want, g = base.numpy().astype(np.float64) + delta, got.cpu().numpy().astype(np.float64)
+    odd = ~np.isfinite(want)
+    assert odd.any() and np.isinf(want).any() and np.isnan(want).any()
+    assert np.array_equal(g[odd], want[odd], equal_nan=True)
+    off, delta, bound, base = np.abs(g[~odd] - want[~odd]), delta[~odd], bound[~odd], base.numpy()[~odd]
+    assert np.all(off <= bound + 2.0 ** -23 * (np.abs(base) + np.abs(delta) + bound))
