@@ -234,13 +234,15 @@ struct Row8 {
   }
 };
 
+// The larger of an fp16 row's largest |t| and |t|, of which only numbers count.
+__device__ __forceinline__ float top_of(float top, float t) { return fabsf(t) < bits_f(0x7F800000u) ? fmaxf(top, fabsf(t)) : top; }
 // What brings an fp16 row whose largest |t| is `top` to [2^13, 2^14), and back (bfloat16 has float32's range).
 template <int DT>
 __device__ __forceinline__ void fit_of(float top, float& fit, float& back) {
   fit = back = 1.0f;
   if constexpr (DT == DT_F16) {
-    // (an infinite or NaN t is not scaled; 2^126 is the largest scale whose inverse is normal too)
-    const int by = top < bits_f(0x7F800000u) ? min(13 - ((int)(f_bits(top) >> 23) - 127), 126) : 0;
+    // (2^126 is the largest scale whose inverse is normal too)
+    const int by = min(13 - ((int)(f_bits(top) >> 23) - 127), 126);
     fit = bits_f((unsigned)(127 + by) << 23);
     back = bits_f((unsigned)(127 - by) << 23);
   }
@@ -317,7 +319,7 @@ __global__ __launch_bounds__(64) void k_lowrank_up_few(LowrankArgs g) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       t[s][i >> 2][i & 3] = t[s][i >> 2][i & 3] * sc;
-      top = fmaxf(top, fabsf(t[s][i >> 2][i & 3]));
+      if constexpr (DT == DT_F16) top = top_of(top, t[s][i >> 2][i & 3]);
     }
   if constexpr (DT == DT_F16) {
     top = fmaxf(top, __shfl_xor(top, 16, 64));
@@ -447,7 +449,7 @@ __global__ __launch_bounds__(64 * UP_WAVES) void k_lowrank_up(LowrankArgs g) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         t[mb][j][i] = t[mb][j][i] * sc;
-        top = fmaxf(top, fabsf(t[mb][j][i]));
+        if constexpr (DT == DT_F16) top = top_of(top, t[mb][j][i]);
       }
     if constexpr (DT == DT_F16) {
       top = fmaxf(top, dpp_f<0xB1>(top));

@@ -55,3 +55,25 @@ def test_an_infinite_weight_of_up_is_an_infinity_of_its_sign(vq, m, r, dt):
     assert np.array_equal(g[odd], want[odd], equal_nan=True)
     off, delta, bound, base = np.abs(g[~odd] - want[~odd]), delta[~odd], bound[~odd], base.numpy()[~odd]
     assert np.all(off <= bound + 2.0 ** -23 * (np.abs(base) + np.abs(delta) + bound))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("m", [5, 1100])
+def test_an_infinite_t_beside_large_ones(vq, m, dt):
+    """One infinite t in a row whose others are beyond fp16's range: the infinity's sign, whatever theirs."""
+    rng = np.random.default_rng(m)
+    k, n, r, ad = 64, 40, 16, 2
+    x = gen.to_storage((3e4 * (1 + rng.random((m, k)))).astype(np.float32), dt)
+    d = (1 + rng.random((ad, r, k))).astype(np.float32)  # every t far above 65504
+    d[1, 3, 5] = np.inf
+    u = np.full((ad, n, r), -1.0, np.float32)
+    u[:, :, 3] = 1.0
+    u[:, ::2] *= -1.0
+    down, up = gen.to_storage(d, dt), gen.to_storage(u, dt)
+    index = torch.arange(m, dtype=torch.int32) % 3 - 1
+    base = torch.zeros(m, n)
+    got = vq.vq_lowrank_add(base.to(DEV), x.to(DEV), down.to(DEV), up.to(DEV), index.to(DEV)).cpu().numpy().astype(np.float64)
+    delta, bound = ol.exact(f64(x, dt), f64(down, dt), f64(up, dt), index.numpy(), None, dt)
+    odd = ~np.isfinite(delta)
+    assert np.isinf(delta[index.numpy() == 1]).all() and np.array_equal(got[odd], delta[odd])
+    assert np.all(np.abs(got[~odd] - delta[~odd]) <= bound[~odd] + 2.0 ** -23 * (np.abs(delta[~odd]) + bound[~odd]))
