@@ -12,7 +12,8 @@
 //                   not meet, so an infinity or NaN in one adapter stays out of the other requests' rows.
 // t, scaled, enters the second product as the sum of two 16-bit values, hi and lo = RNE16(t - hi): rounded once
 // it would cost the output up to 2^-9 of the adapter's part in bfloat16, in two pieces 2^-16 (fp16
-// 2^-22), for a second matrix instruction in a kernel that waits for memory.  hi is cut off, so that lo has t's
+// 2^-22), for a second matrix instruction in a kernel that waits for memory.  A float32 output of bfloat16 operands
+// would show 2^-16: it takes a third piece, and nothing is lost.  hi is cut off, so that lo has t's
 // sign, and neither is zero where t is not: an infinity in up times t is then the infinity that the
 // formula gives, and not NaN.  (Taking NaN sums from hi alone costs the inner loop 84 -> 93 us, rank 128 159 ->
 // 196.)  An fp16 row is scaled by the power of two that brings its largest |t| to [2^13, 2^14), since t is not
@@ -268,11 +269,14 @@ __device__ __forceinline__ unsigned upper(float& t0, float& t1) {
     return u;
   }
 }
-// Two values of t in two pieces each.
-template <int DT>
-__device__ __forceinline__ void pieces(float t0, float t1, unsigned& hi, unsigned& lo) {
-  hi = upper<DT>(t0, t1);
-  lo = cvt_pair<DT>(t0, t1);
+// Pieces of t: two; three where a float32 output of bfloat16 operands would show the third (24 bits are t).
+template <int DT, int OUT_DT>
+constexpr int PIECES = DT == DT_BF16 && OUT_DT == DT_F32 ? 3 : 2;
+template <int DT, int N>
+__device__ __forceinline__ void pieces(float t0, float t1, unsigned (&p)[N]) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) p[i] = upper<DT>(t0, t1);
+  p[N - 1] = cvt_pair<DT>(t0, t1);
 }
 // A step of 32 of the rank from row q of up: eight elements a lane.
 template <typename V8>
@@ -288,7 +292,7 @@ __device__ __forceinline__ int up_col(int rl, int b) { return 8 * (rl >> 2) + 4 
 template <int DT, int OUT_DT, int RS>
 __global__ __launch_bounds__(64) void k_lowrank_up_few(LowrankArgs g) {
   typedef typename Half<DT>::V8 V8;
-  constexpr int DU = 4 / RS;
+  constexpr int DU = 4 / RS, P = PIECES<DT, OUT_DT>;
   const int lane = threadIdx.x, rl = lane & 15, kq = lane >> 4;
   const int64_t row = (int64_t)(blockIdx.x / g.col_tiles) * 16 + rl;
   const int n0 = (int)(blockIdx.x % g.col_tiles) * 32, n = n0 + 8 * kq;
@@ -327,19 +331,19 @@ __global__ __launch_bounds__(64) void k_lowrank_up_few(LowrankArgs g) {
   }
   float fit, back;
   fit_of<DT>(top, fit, back);
-  V8 hi[RS], lo[RS];
+  V8 part[P][RS];
 #pragma unroll
   for (int s = 0; s < RS; ++s) {
-    u4v h, l;
+    u4v q[P];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      unsigned hu, lu;
-      pieces<DT>(t[s][i >> 1][2 * (i & 1)] * fit, t[s][i >> 1][2 * (i & 1) + 1] * fit, hu, lu);
-      h[i] = hu;
-      l[i] = lu;
+      unsigned u[P];
+      pieces<DT>(t[s][i >> 1][2 * (i & 1)] * fit, t[s][i >> 1][2 * (i & 1) + 1] * fit, u);
+#pragma unroll
+      for (int p = 0; p < P; ++p) q[p][i] = u[p];
     }
-    hi[s] = __builtin_bit_cast(V8, h);
-    lo[s] = __builtin_bit_cast(V8, l);
+#pragma unroll
+    for (int p = 0; p < P; ++p) part[p][s] = __builtin_bit_cast(V8, q[p]);
   }
   for (int d0 = 0; d0 < nd; d0 += DU) {
     V8 fu[DU][RS][2];
@@ -362,8 +366,8 @@ __global__ __launch_bounds__(64) void k_lowrank_up_few(LowrankArgs g) {
         acc[b] = v4f{};
 #pragma unroll
         for (int s = 0; s < RS; ++s) {
-          acc[b] = mfma32<DT>(fu[u][s][b], lo[s], acc[b]);
-          acc[b] = mfma32<DT>(fu[u][s][b], hi[s], acc[b]);
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p) acc[b] = mfma32<DT>(fu[u][s][b], part[p][s], acc[b]);
         }
       }
       // Each row takes the sums of its own adapter, once.
@@ -387,7 +391,8 @@ template <int DT, int OUT_DT, int MB, int RS>
 __global__ __launch_bounds__(64 * UP_WAVES) void k_lowrank_up(LowrankArgs g) {
   typedef typename Half<DT>::V8 V8;
   constexpr int TP = 32 * RS + 8;  // pitch of t's pieces: eight lanes' rows start in different banks
-  __shared__ __attribute__((aligned(16))) uint16_t s_t[2][16 * MB][TP];  // hi, lo
+  constexpr int P = PIECES<DT, OUT_DT>;
+  __shared__ __attribute__((aligned(16))) uint16_t s_t[P][16 * MB][TP];
   __shared__ __attribute__((aligned(16))) float s_sum[UP_WAVES][16][UP_PITCH];
   __shared__ float s_back[16 * MB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -464,16 +469,16 @@ __global__ __launch_bounds__(64 * UP_WAVES) void k_lowrank_up(LowrankArgs g) {
     for (int j = 0; j < CH; ++j) {
       const int c = 4 * (rl + 16 * j);
       if (c < 32 * RS) {
-        u2v h, l;
+        u2v q[P];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          unsigned hu, lu;
-          pieces<DT>(t[mb][j][2 * i] * fit, t[mb][j][2 * i + 1] * fit, hu, lu);
-          h[i] = hu;
-          l[i] = lu;
+          unsigned u[P];
+          pieces<DT>(t[mb][j][2 * i] * fit, t[mb][j][2 * i + 1] * fit, u);
+#pragma unroll
+          for (int p = 0; p < P; ++p) q[p][i] = u[p];
         }
-        *reinterpret_cast<u2v*>(&s_t[0][16 * mb + tr][c]) = h;
-        *reinterpret_cast<u2v*>(&s_t[1][16 * mb + tr][c]) = l;
+#pragma unroll
+        for (int p = 0; p < P; ++p) *reinterpret_cast<u2v*>(&s_t[p][16 * mb + tr][c]) = q[p];
       }
     }
   }
@@ -492,14 +497,15 @@ __global__ __launch_bounds__(64 * UP_WAVES) void k_lowrank_up(LowrankArgs g) {
       for (int p = 0; p < 2; ++p) acc[p][0] = acc[p][1] = v4f{};
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        const V8 hi = *reinterpret_cast<const V8*>(&s_t[0][16 * mb + rl][32 * s + 8 * kq]);
-        const V8 lo = *reinterpret_cast<const V8*>(&s_t[1][16 * mb + rl][32 * s + 8 * kq]);
+        V8 part[P];
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < P; ++p) part[p] = *reinterpret_cast<const V8*>(&s_t[p][16 * mb + rl][32 * s + 8 * kq]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            acc[p][b] = mfma32<DT>(fu[p][b][s], lo, acc[p][b]);
-            acc[p][b] = mfma32<DT>(fu[p][b][s], hi, acc[p][b]);
+#pragma unroll
+            for (int p = P - 1; p >= 0; --p) acc[c][b] = mfma32<DT>(fu[c][b][s], part[p], acc[c][b]);
           }
       }
       const float back = s_back[16 * mb + rl];

@@ -602,10 +602,10 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
  * and a row whose index lies outside [0, adapters) has none: out[i] = base[i], bit for bit.
  * base is the shared projection's output (vq_qgemm_dequant, vq_gemm_dense, vq_w4_gemv ..).
  *   t = x[i] . down[a]^T: products exact, sums in float32, times scale rounded to float32; it
- *   enters the second product as two 16-bit pieces, sums in float32.  With K = k, R = rank, T the
- *   largest |t| of the row and S = sum_j |t_j| |up_j|:
- *     |out - exact| <= scale (2 K + 10) 2^-24 sum_j (sum_k |x_k down_jk|) |up_j|
- *                      + (4 R + 4) 2^-24 S + 2^-16 S (F16: 2^-22 S + 2^-38 T sum_j |up_j|)
+ *   enters the second product as two 16-bit pieces (three for BF16 and an F32 output, which are t), sums
+ *   in float32.  With K = k, R = rank, T the largest |t| of the row and S = sum_j |t_j| |up_j|:
+ *     |out - exact| <= scale (2 K + 10) 2^-24 sum_j (sum_k |x_k down_jk|) |up_j| + (4 R + 4) 2^-24 S
+ *                      + 2^-16 S (BF16, BF16 output), or 2^-22 S + 2^-38 T sum_j |up_j| (F16)
  *   before the addition of base and the output's rounding
  *   x          device, dt in {F16, BF16}, [m x k], stride ldx (16-byte aligned, ldx % 8 == 0)
  *   down       device dt [adapters x rank x k];  up: device dt [adapters x n x rank] (16-byte aligned)

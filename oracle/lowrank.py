@@ -4,16 +4,16 @@
 
 and the bound on a kernel that sums in float32 and passes t = scale * x . down^T on in two 16-bit
 pieces: an addition is counted at 2^-23 (K of them for t, two R for the output), t's own
-rounding and that of the pieces (bf16 2^-16 of t; fp16 2^-22 of t, and 2^-38 of the row's largest
-where a piece is below fp16's normal range).
+rounding and that of the pieces (bf16 2^-16 of t, nothing for a float32 output, which takes three pieces;
+fp16 2^-22 of t, and 2^-38 of the row's largest where a piece is below fp16's normal range).
 """
 from __future__ import annotations
 
 import numpy as np
 
 
-def exact(x, down, up, index, scale=None, dtype="bf16"):
-    """float64 (delta, bound) [m x n]; x, down, up float64 arrays."""
+def exact(x, down, up, index, scale=None, dtype="bf16", out=None):
+    """float64 (delta, bound) [m x n]; x, down, up float64 arrays; out: the output's type, dtype or "fp32"."""
     m, n = len(x), up.shape[1]
     k, r = x.shape[1], down.shape[1]
     delta, bound = np.zeros((m, n)), np.zeros((m, n))
@@ -30,7 +30,7 @@ def exact(x, down, up, index, scale=None, dtype="bf16"):
             sums = np.abs(t) @ ua
             bound[at] = (2 * k + 10) * 2.0 ** -24 * (ta @ ua) + (4 * r + 4) * 2.0 ** -24 * sums
             if dtype == "bf16":
-                bound[at] += 2.0 ** -16 * sums
+                bound[at] += 0.0 if out == "fp32" else 2.0 ** -16 * sums
             else:
                 bound[at] += 2.0 ** -22 * sums + 2.0 ** -38 * np.abs(t).max(1, keepdims=True) * ua.sum(0)[None, :]
     return delta, bound

@@ -1,4 +1,4 @@
-"""Low-rank adapters: infinities among their weights."""
+"""Low-rank adapters: infinities among their weights, and a float32 output of bfloat16 operands."""
 import numpy as np
 import pytest
 import torch
@@ -77,3 +77,47 @@ def test_an_infinite_t_beside_large_ones(vq, m, dt):
     odd = ~np.isfinite(delta)
     assert np.isinf(delta[index.numpy() == 1]).all() and np.array_equal(got[odd], delta[odd])
     assert np.all(np.abs(got[~odd] - delta[~odd]) <= bound[~odd] + 2.0 ** -23 * (np.abs(delta[~odd]) + bound[~odd]))
+
+
+@pytest.mark.parametrize("m,n,k,r,adapters", [(1, 96, 512, 64, 1), (40, 130, 256, 16, 4), (64, 70, 4096, 128, 3), (200, 515, 128, 40, 5),
+                                              (1100, 129, 192, 128, 6), (1025, 320, 320, 32, 2)])
+def test_a_float32_output_of_bfloat16_operands(vq, m, n, k, r, adapters):
+    """t goes on in three pieces of 8 bits, which are t: nothing but the float32 sums is lost."""
+    rng = np.random.default_rng([m, n, k, r])
+
+    def half(shape, scale):
+        return gen.to_storage((scale * rng.standard_normal(shape)).astype(np.float32), "bf16")
+    # K of few terms that are not zero, so that the first product's own roundings are few
+    x = half((m, k), 1.0)
+    x[:, 3:] = 0
+    down, up = half((adapters, r, k), 1.0), half((adapters, n, r), r ** -0.5)
+    up[:, :, 1:] = 0  # one term: t's pieces times one weight, and a rounding of each sum
+    index = torch.from_numpy(rng.integers(-1, adapters, m).astype(np.int32))
+    index[0] = 0
+    base = torch.zeros(m, n)
+    got = vq.vq_lowrank_add(base.to(DEV), x.to(DEV), down.to(DEV), up.to(DEV), index.to(DEV))
+    torch.cuda.synchronize()
+    xd, dd, ud = f64(x, "bf16"), f64(down, "bf16"), f64(up, "bf16")
+    delta, _ = ol.exact(xd, dd, ud, index.numpy(), None, "bf16")
+    bound = np.zeros((m, n))
+    for a in range(adapters):
+        at = np.nonzero(index.numpy() == a)[0]
+        ta = np.abs(xd[at]) @ np.abs(dd[a]).T  # three products, two additions that round, the zeros' none
+        bound[at] = (4 * ta * 2.0 ** -23 + 4 * np.abs(xd[at] @ dd[a].T) * 2.0 ** -23) @ np.abs(ud[a]).T
+    assert np.all(np.abs(got.cpu().numpy().astype(np.float64) - delta) <= bound)
+
+
+@pytest.mark.parametrize("m,n,k,r,adapters", [(3, 33, 128, 24, 2), (64, 100, 1024, 64, 5), (200, 257, 640, 128, 9), (1100, 320, 256, 16, 4)])
+def test_a_float32_output_within_the_bound_of_three_pieces(vq, m, n, k, r, adapters):
+    rng = np.random.default_rng([m, n, k])
+
+    def half(shape, scale):
+        return gen.to_storage((scale * rng.standard_normal(shape)).astype(np.float32), "bf16")
+    x, down, up = half((m, k), 1.0), half((adapters, r, k), k ** -0.5), half((adapters, n, r), r ** -0.5)
+    index = torch.from_numpy(rng.integers(-1, adapters, m).astype(np.int32))
+    scales = torch.from_numpy((0.5 + rng.random(adapters)).astype(np.float32))
+    base = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32))
+    got = vq.vq_lowrank_add(base.to(DEV), x.to(DEV), down.to(DEV), up.to(DEV), index.to(DEV), scales=scales.to(DEV)).cpu().numpy()
+    delta, bound = ol.exact(f64(x, "bf16"), f64(down, "bf16"), f64(up, "bf16"), index.numpy(), scales.numpy(), "bf16", out="fp32")
+    b = base.numpy().astype(np.float64)
+    assert np.all(np.abs(got - (b + delta)) <= bound + 2.0 ** -24 * (np.abs(b + delta) + bound))
