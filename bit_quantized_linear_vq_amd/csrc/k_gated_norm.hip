@@ -24,8 +24,10 @@
 // took 160 registers and spilled (17776 x 1920 85 us).
 //
 // Measured, three sets of buffers in turn: 17776 x 1920, layer norm, the branch's own norm, a gate, scale and
-// shift in float32 for each of 16 frames, to 16 bits 61.8 us = 4.4 TB/s (a large copy reaches 5.2); 4113 x
-// 4096 with an index, to codes, 31.5 us = 3.7 TB/s; one row of 1920 4.0 us.  Tried and not kept: rows
+// shift in float32 for each of 16 frames, to 16 bits 61.5 us = 4.4 TB/s (a large copy reaches 5.2); 4113 x
+// 4096 with an index, to codes, 31.9 us = 3.7 TB/s; 17776 x 1920 without a branch 28.8 us; one row of 1920 4.1 us.
+// A row of 1920 takes its wave 1222 vector instructions, about a quarter of them in float64: at least 35 of the 61.5 us are
+// their issue, not waiting.  Tried and not kept: rows
 // next to each other for one workgroup (modulation then stays in the first cache; 68 -> 76 us, 31 -> 35),
 // two pieces a thread (62 -> 75 us, 31 -> 33), more waves by fewer registers (five waves a SIMD 62 -> 65, six
 // 92: spills).

@@ -5,7 +5,7 @@
 // over rows whose requests use different adapters, or none (index -1: out[i] = base[i]).  The inner
 // dimension, the rank, is small, so the products are bound by the bytes of x, base and out
 // (and, for few rows, of the adapters); both run on the matrix cores.
-//   k_lowrank_down  t = x . down^T: 16 rows a tile, against the columns of the adapters that
+//   k_lowrank_down  t = x . down^T: 16 or 32 rows a tile, against the columns of the adapters that
 //                   its rows use, each once; K in parts where rows are few.  Sums in float32.
 //   k_lowrank_up    out = base + t . up^T: a tile goes through the adapters of its rows one after the
 //                   other, and each row takes the one that is its own.  Sums of different adapters do
@@ -19,11 +19,11 @@
 // 196.)  An fp16 row is scaled by the power of two that brings its largest |t| to [2^13, 2^14), since t is not
 // bound to fp16's range; the products are scaled back, both exactly (a lo below 2^-24 is lost).
 //
-// Measured, three sets of buffers in turn: 17776 rows of seven requests, 1920 -> 5760, rank 32, 31 + 85 us (base
+// Measured, three sets of buffers in turn: 17776 rows of seven requests, 1920 -> 5760, rank 32, 32 + 85 us (base
 // and out alone are 79 us at a large copy's rate, and take 78 in a copy with this access pattern), rank 64
-// 42 + 105, rank 128 73 + 164: there every tile's reads of up and down through the second-level caches bound
-// both; 48 requests of one row over 12 adapters, 4096 -> 12288, rank 16, 5.5 + 8.6 us; one row, 1920 -> 5760, rank
-// 64, 6.3 + 5.2 us: launches and dependent loads.  Tried and not kept: loads of base or stores of out past the
+// 43 + 108, rank 128 73 + 163: there every tile's reads of up and down through the second-level caches bound
+// both; with base and out in float32 32 + 154, 42 + 171 and 74 + 223; 48 requests of one row over 12 adapters, 4096 ->
+// 12288, rank 16, 5.8 + 8.9 us; one row, 1920 -> 5760, rank 64, 6.5 + 4.8 us: launches and dependent loads.  Tried and not kept: loads of base or stores of out past the
 // cache (109 -> 113 to 123 us), several column tiles of a workgroup one after the other (94 -> 111 in a plain
 // copy), a contiguous range of tiles for each XCD (92 -> 105), tiles of 64 rows.
 #include <algorithm>

@@ -3,9 +3,9 @@
 //
 // Routing.  p = softmax or sigmoid of a row of scores; the choice goes by p + bias (by the scores
 // themselves without a bias: the same order, with no rounding), in the groups whose best one or two
-// sum highest; ties go to the lower index.  Whole numbers come out, so what they are compared by is
-// float64: two values of p + bias may differ by less than float32 holds, and the exponentials are
-// some tens of instructions against a launch.
+// sum highest; ties go to the lower index.  Whole numbers come out, so scores are compared as they are, exact in
+// float32, and p (+ bias) in float64: two values may differ by less than float32 holds, and the exponentials
+// are some tens of instructions against a launch.
 //   k_route_select  a wave (or 16 of its lanes) a row: choices, weights, and the block's count for
 //                   each expert
 //   k_route_place   offsets, and each choice's place: rows before it in its expert's segment, by
@@ -13,12 +13,14 @@
 //                   matter, and places are the same in every call.
 //   k_route_few     both for a few rows: 64 of up to 64 experts, 16 of 256, 4 of more
 // Bound by latency and by instructions (17776 rows of 160 scores are 11 MB): a row's exponentials, and for
-// each choice a maximum over the row's lanes.  (Exponentials of a softmax's sum by the hardware's float32 2^x took
-// 11.2 us instead of 12.7, and put 2^-22 on the weights; they are float64.)  Sixteen lanes a row, since the maximum's steps are then
-// register moves that four rows share (a wave a row: 17776 x 160 28 us instead of 14).
+// each choice a maximum over the row's lanes.  Sixteen lanes a row, since the maximum's steps are then
+// register moves that four rows share (a wave a row: 17776 x 160 28 us instead of 14).  The exponentials of a
+// softmax's sum are float64 too: by the hardware's float32 2^x they take 1.5 us less there, and put 2^-22 on weights
+// that are not renormalised.  By p with more than 160 experts a lane's keys and p no longer fit its 128 registers
+// (of a workgroup of 1024): 8 to 164 bytes a lane go through scratch.
 //
-// Measured: 17776 rows of 160, softmax, six choices, 12.7 + 10.5 us; 4124 of 96 in six groups, sigmoid with
-// a bias, four choices, 9.7 + 8.2 us; one row of 16 3.8 us.  The placing waits for loads one after the
+// Measured: 17776 rows of 160, softmax, six choices, 13.5 + 10.3 us; 4124 of 96 in six groups, sigmoid with
+// a bias, four choices, 10.6 + 7.9 us; 4096 of 256 in eight, eight choices, 20.7 + 11.6 us; one row of 16 3.7 us.  The placing waits for loads one after the
 // other: every block's counts and its choices, then LDS.
 #include <algorithm>
 #include <type_traits>
@@ -553,8 +555,8 @@ constexpr unsigned COMBINE_WIDE = 1u << 23;  // workgroups along x: a launch has
 // TY: type of y; TO: of the residual and the output; gates in float32 or the 16-bit one of the two.  A
 // wave has 512 elements of a row, so that the row's places and weights are scalars; four choices' rows
 // are on their way at once.  Bound by the bytes of y, res and out: 17776 x 1920 of two choices with residual
-// and gate 52.5 us = 5.2 TB/s, a large copy's rate; 4097 x 2047 of four, a tenth of them absent, rows at odd
-// addresses, 22.4 us = 4.2 TB/s; eight rows 3.7 us.
+// and gate 52.5 us = 5.2 TB/s, a large copy's rate (float32 y and out 102.7 us = 5.3); 4097 x 2047 of four, a tenth of
+// them absent, rows at odd addresses, 22.8 us = 4.1 TB/s; eight rows 4.0 us.
 template <int TY, int TO>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs a, unsigned segments, unsigned items) {
   const unsigned item = (blockIdx.y * COMBINE_WIDE + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

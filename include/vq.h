@@ -610,7 +610,7 @@ vq_status vq_combine_experts(const void* y, vq_dtype y_dt, int64_t y_rows, int64
  *   x          device, dt in {F16, BF16}, [m x k], stride ldx (16-byte aligned, ldx % 8 == 0)
  *   down       device dt [adapters x rank x k];  up: device dt [adapters x n x rank] (16-byte aligned)
  *   index      device int32 [m], in any order; rows of one adapter next to each other are fastest:
- *              a tile of 16 to 64 rows reads every adapter that occurs in it
+ *              a tile of 16 or 32 rows reads every adapter that occurs in it
  *   scale      device float [adapters], or NULL for ones
  *   base, out  device out_dt (dt or F32), [m x n], strides ldb, ldo; out may be base itself (same
  *              pointer and stride); no other overlap of inputs and outputs
